@@ -19,12 +19,16 @@ import ctypes
 import torch
 
 from . import _native
+from .attention import (PagedKVCache, PagedSequences, append_kv, attention_workspace, page_errors,
+                        paged_attention_decode, paged_attention_prefill)
 
 __all__ = ["mxfp4_expert_linear", "workspace_size", "device_errors", "wait_timeouts",
            "LibraryNotBuilt", "MXFP4Error", "router_topk", "mxfp4_expert_linear_routed",
            "mxfp4_swiglu_expert", "swiglu_workspace_size", "PreparedWeights",
            "prepare_weights", "prepared_bytes", "mxfp4_expert_linear_prepared",
-           "prepared_workspace_size"]
+           "prepared_workspace_size", "PagedKVCache", "PagedSequences", "append_kv",
+           "paged_attention_decode", "paged_attention_prefill", "attention_workspace",
+           "page_errors"]
 
 LibraryNotBuilt = _native.LibraryNotBuilt
 MXFP4Error = _native.MXFP4Error

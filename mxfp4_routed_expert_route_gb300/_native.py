@@ -13,7 +13,8 @@ import threading
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmxfp4_expert_linear.so")
 
-# Values of the #defines in include/mxfp4_expert_linear.h.
+# Values of the #defines in include/mxfp4_expert_linear.h (the attention
+# operators of include/mxfp4el_attention.h share them).
 OK = 0
 ERR_INVALID_ARGUMENT = -1
 ERR_UNSUPPORTED_DTYPE = -2
@@ -38,6 +39,22 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_FLT = ctypes.c_float
+
+
+class KvCache(ctypes.Structure):
+    """mxfp4el_kv_cache of include/mxfp4el_attention.h."""
+    _fields_ = [("k", _P), ("v", _P)] + [(n, _I64) for n in (
+        "num_pages", "num_kv_heads", "page_size", "head_dim", "k_page_stride", "k_head_stride",
+        "k_slot_stride", "v_page_stride", "v_head_stride", "v_slot_stride", "dtype")]
+
+
+class Sequences(ctypes.Structure):
+    """mxfp4el_sequences of include/mxfp4el_attention.h."""
+    _fields_ = [("page_table", _P), ("seq_lens", _P), ("q_offsets", _P), ("num_seqs", _I64),
+                ("max_pages", _I64), ("table_stride", _I64)]
+
+
 SIGNATURES = {
     "mxfp4_expert_linear": (_INT, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64,
                                    _I64, _I64, _INT, _INT, _P]),
@@ -74,6 +91,16 @@ SIGNATURES = {
     "mxfp4_expert_linear_prepared_with_workspace": (_INT, [_P, _P, _P, _P, _P, _P, _I64, _I64,
                                                            _I64, _I64, _I64, _INT, _INT, _P,
                                                            _SZ, _P]),
+    # The structs go as addresses (ctypes.addressof): the handles that hold
+    # them keep the address, and a call converts one integer.
+    "mxfp4el_append_kv": (_INT, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _FLT,
+                                 _P, _I64, _I64, _INT, _P, _P, _P, _I64, _I64, _P]),
+    "mxfp4el_attention_decode": (_INT, [_P, _I64, _I64, _P, _P, _FLT, _I64, _I64, _P, _P, _I64,
+                                        _P, _SZ, _P]),
+    "mxfp4el_attention_prefill": (_INT, [_P, _I64, _I64, _P, _P, _FLT, _I64, _I64, _P, _P, _I64,
+                                         _I64, _P, _SZ, _P]),
+    "mxfp4el_attention_workspace_size": (_SZ, []),
+    "mxfp4el_page_errors": (_INT, [_P, ctypes.POINTER(_I64)]),
 }
 
 _lock = threading.Lock()

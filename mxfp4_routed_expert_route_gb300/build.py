@@ -21,7 +21,8 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libmxfp4_expert_linear.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "gemv.cu", "gemm_tc.cu", "combine.cu", "static_scratch.cu",
-           "router.cu", "swiglu.cu", "prepare.cu"]
+           "router.cu", "swiglu.cu", "prepare.cu", "attn_api.cu", "kv_append.cu",
+           "attn_simt.cu"]
 
 
 def nvcc() -> str:
@@ -40,7 +41,8 @@ def _flags():
 
 def _newest_input_mtime():
     paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    paths.append(os.path.join(ROOT, "include", "mxfp4_expert_linear.h"))
+    inc = os.path.join(ROOT, "include")
+    paths += [os.path.join(inc, f) for f in os.listdir(inc)]
     paths.append(os.path.abspath(__file__))
     return max(os.path.getmtime(p) for p in paths)
 

@@ -1,0 +1,64 @@
+// attn.h -- declarations shared by the attention operators' translation
+// units (include/mxfp4el_attention.h).
+#pragma once
+
+#include "internal.h"
+
+namespace mxfp4el {
+
+// Keys and values of one sequence are found through its page table; strides
+// are in elements.
+struct KvCacheView {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int64_t k_page, k_head, k_slot;
+  int64_t v_page, v_head, v_slot;
+  int page_size, page_shift;
+  int kv_heads, head_dim;
+  int token_dtype;
+};
+
+struct SequencesView {
+  const int* page_table;
+  const int* seq_lens;
+  const int* q_offsets;      // null: one new token per sequence
+  int64_t table_stride;
+  int num_seqs;
+  int max_pages;
+};
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  const void *q_norm, *k_norm;
+  const float* cos_sin;
+  int64_t max_positions;
+  float eps;
+  int rotary_dim;
+  int T, heads;
+  void* q_out;
+  KvCacheView cache;
+  SequencesView seqs;
+  unsigned long long* status;
+};
+cudaError_t launch_append_kv(const AppendArgs& a, bool interleaved, cudaStream_t stream);
+
+struct AttnArgs {
+  const void* q;
+  int64_t q_token, q_head;
+  void* out;                 // (T, heads, head_dim), dense
+  const float* sink_logits;  // (heads) or null
+  float scale;
+  int T, heads, group;       // group: query heads per key head
+  int window;                // 0: none
+  int sinks;                 // 0 without a window
+  KvCacheView cache;
+  SequencesView seqs;
+  unsigned long long* status;
+};
+
+// Any dtype, any number of new tokens, on the CUDA cores (attn_simt.cu).
+cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream);
+
+}  // namespace mxfp4el

@@ -21,6 +21,7 @@ constexpr size_t kRouteSmemLimit = 96 * 1024;
 // Device status words (one array per device, see device_status_words()).
 constexpr int kStatusBadPairs = 0;      // (t, k) pairs with an out-of-range id
 constexpr int kStatusWaitTimeouts = 1;  // kernel waits that hit their time limit
+constexpr int kStatusBadPages = 2;      // attention: page ids, lengths or positions out of range
 constexpr int kStatusWords = 4;
 
 // Slots of RoutePlan::meta.
