@@ -48,8 +48,8 @@ extern "C" {
  * element strides of their own for pages, heads and slots, so both
  * (page, head, slot, width) and (page, slot, head, width) memory orders fit;
  * a row's head_dim elements are contiguous. Bases and strides are multiples
- * of 16 bytes. page_size is a power of two from 8 to 1024; head_dim is 64 or
- * 128.
+ * of 16 bytes. num_pages is at least 1; page_size is a power of two from 8 to
+ * 1024; head_dim is 64 or 128.
  */
 typedef struct mxfp4el_kv_cache {
   void* k;

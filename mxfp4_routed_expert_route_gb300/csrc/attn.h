@@ -58,6 +58,11 @@ struct AttnArgs {
   unsigned long long* status;
 };
 
+// One new token of each sequence, split over the cache's length and joined
+// through the workspace (attn_decode.cu).
+cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream);
+size_t decode_workspace_bytes();
+
 // Any dtype, any number of new tokens, on the CUDA cores (attn_simt.cu).
 cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream);
 

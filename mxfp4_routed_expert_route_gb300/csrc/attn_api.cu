@@ -43,7 +43,7 @@ int check_cache(const mxfp4el_kv_cache* c, KvCacheView* v, Span* k_span, Span* v
   if (c == nullptr) return MXFP4EL_ERR_INVALID_ARGUMENT;
   if (c->dtype != MXFP4EL_DTYPE_F32 && c->dtype != MXFP4EL_DTYPE_BF16)
     return MXFP4EL_ERR_UNSUPPORTED_DTYPE;
-  if (c->num_pages < 0 || c->num_kv_heads <= 0 || (c->head_dim != 64 && c->head_dim != 128) ||
+  if (c->num_pages <= 0 || c->num_kv_heads <= 0 || (c->head_dim != 64 && c->head_dim != 128) ||
       c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) != 0)
     return MXFP4EL_ERR_INVALID_ARGUMENT;
   if (c->num_pages > kMaxDim || c->num_kv_heads > kMaxHeads) return MXFP4EL_ERR_TOO_LARGE;
@@ -58,11 +58,9 @@ int check_cache(const mxfp4el_kv_cache* c, KvCacheView* v, Span* k_span, Span* v
     if (st[i][2] * es % 16 != 0) return MXFP4EL_ERR_INVALID_ARGUMENT;
     if (st[i][2] > kMaxStride / 1024) return MXFP4EL_ERR_TOO_LARGE;
     Span* s = i == 0 ? k_span : v_span;
-    if (c->num_pages > 0) {
-      const int rc = check_rows(base[i], c->num_pages, st[i][0], c->num_kv_heads, st[i][1],
-                                (c->page_size - 1) * st[i][2] + c->head_dim, es, s);
-      if (rc != MXFP4EL_OK) return rc;
-    }
+    const int rc = check_rows(base[i], c->num_pages, st[i][0], c->num_kv_heads, st[i][1],
+                              (c->page_size - 1) * st[i][2] + c->head_dim, es, s);
+    if (rc != MXFP4EL_OK) return rc;
   }
   v->k = c->k;
   v->v = c->v;
@@ -217,7 +215,7 @@ extern "C" int mxfp4el_append_kv(const void* q, int64_t q_token_stride, int64_t 
              : MXFP4EL_ERR_CUDA;
 }
 
-extern "C" size_t mxfp4el_attention_workspace_size(void) { return 256; }
+extern "C" size_t mxfp4el_attention_workspace_size(void) { return decode_workspace_bytes(); }
 
 extern "C" int mxfp4el_attention_decode(const void* q, int64_t q_token_stride,
                                         int64_t q_head_stride, const mxfp4el_kv_cache* cache,
@@ -232,7 +230,7 @@ extern "C" int mxfp4el_attention_decode(const void* q, int64_t q_token_stride,
                                  sinks, sink_logits, out, seqs->num_seqs, num_heads, workspace,
                                  workspace_bytes, &a, &nothing);
   if (rc != MXFP4EL_OK || nothing) return rc;
-  return launch_attention_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return launch_attention_decode(a, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MXFP4EL_OK
              : MXFP4EL_ERR_CUDA;
 }

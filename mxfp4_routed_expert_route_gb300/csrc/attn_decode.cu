@@ -1,0 +1,865 @@
+// attn_decode.cu -- attention of one new token of each sequence over the
+// paged cache, split over the cache's length and joined.
+//
+// The query heads that share a key head are the rows of one unit of work
+// (sequence, key head, block of up to 16 kMT query heads), so every key and
+// value is read once per unit:
+//
+//   s = scale q K^T,  m = max s,  l = sum e^(s - m),  o = sum e^(s - m) v / l
+//
+// kept as a running (m, l, o) over tiles of keys, in powers of two.
+//
+// Bound: bytes. A unit reads 2 len D elements of cache and does 2 len D
+// multiply-adds a row, a few operations per byte, so the design is about
+// keeping HBM busy: one warp issues tensor copies of whole pages into a ring
+// of stages and never computes; four warps per 16 heads consume.
+//
+// Split. Lengths live on the device, so the host launches a fixed grid and
+// every CTA derives the same split: the tiles of all units, in unit order,
+// are cut into equal runs, one per CTA. A unit that lies inside one run is
+// finished there. Otherwise each of its CTAs writes an unnormalised piece
+// (m, l, o) to the workspace, and the CTA that arrives last joins the pieces
+// in their order along the keys, so the result does not depend on who is
+// last. Every run holds at least kMinTiles tiles: a piece costs a round trip
+// through L2, about what three tiles cost.
+//
+// Matrix products. bf16: mma.sync m16n8k16 with the 16 heads as rows. The
+// legacy tensor path is enough here (two instructions per key and 16 heads
+// against 512 bytes of cache at D = 128), and its register fragments let the
+// softmax follow without a trip through tensor memory. e^(s - m) is rounded
+// to bf16 for the second product, whose other operand is bf16 (a relative
+// error of 2^-8 at most, as the result's own rounding); the sum l adds the
+// rounded values, so that the weights still add to one. float32: CUDA-core
+// multiply-adds.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <mutex>
+
+#include "attn.cuh"
+
+namespace mxfp4el {
+namespace {
+
+constexpr int kGroups = 4;              // key groups of a tile: one consumer warp each per 16 heads
+constexpr int kMinTiles = 4;            // tiles per run at least (see above)
+constexpr int kMaxCtas = 256;
+constexpr int kMaxSeqs = 1024;          // sequences per launch (the prefix sums' shared memory)
+constexpr int kRowsMax = 64;            // query heads per unit: 16 kMT, kMT <= 4
+constexpr int kQSlots = 2;
+
+// Bytes of a piece in the workspace: rows of o (128 floats), m and l.
+constexpr size_t kPieceBytes = (size_t)kRowsMax * 128 * 4 + 2 * kRowsMax * 4;
+constexpr size_t kCounterBytes = (size_t)kMaxCtas * 4;
+
+template <typename Tok, int D, int kMT = 1>
+struct Shape {
+  static constexpr int kTile = sizeof(Tok) == 2 ? 64 : 32;          // keys per tile
+  static constexpr int kPer = kTile / kGroups;                      // keys per consumer warp
+  static constexpr int kSub = 128 / sizeof(Tok);                    // elements in 128 bytes
+  static constexpr int kSubs = D / kSub;                            // 128-byte columns of a row
+  static constexpr uint32_t kHalf = (uint32_t)kTile * D * sizeof(Tok);   // keys (or values) of a tile
+  // 160 KB of keys and values in flight per SM, less beside the buffers of 32
+  // and 64 heads; HBM's latency times an SM's share of its bandwidth is 45 KB.
+  static constexpr int kStages =
+      (kMT == 1 ? 5 : kMT == 2 ? 4 : sizeof(Tok) == 2 ? 3 : 2) * 32768 / (2 * (int)kHalf);
+  static constexpr int kQRow = D * (int)sizeof(Tok) + 16;           // padded row in shared memory
+  static constexpr int kAcc = 16 * D / 32;                          // result elements per lane
+};
+
+struct Unit {
+  int b, head0, rows;     // sequence, first query head, heads
+  int kvh;
+  int len, lo;            // keys; first key of the window
+  int sink_tiles, first_tile, tiles;
+};
+
+struct DecodeArgs {
+  AttnArgs a;
+  int seq0, num_seqs;     // sequences of this launch
+  int units_per_seq;      // key heads x head blocks
+  int head_blocks;
+  int box_rows, box_shift;     // slots per tensor copy: min(page_size, kTile)
+  unsigned int* counters;
+  unsigned char* pieces;
+};
+
+struct DecodeMaps {
+  CUtensorMap k, v;       // (128 bytes, slot, 128-byte column, head, page), 128-byte swizzle
+};
+
+template <int kMT>
+struct __align__(16) DecodeShared {
+  uint64_t full[16], empty[16];
+  uint64_t q_full[kQSlots], q_empty[kQSlots];
+  float merge_m[kMT][2][16], merge_l[kMT][2][16];
+  int last;
+  long long scan[8 + 4 * kMT];
+  long long prefix[kMaxSeqs + 1];     // tiles of all units before sequence b
+};
+
+__device__ __forceinline__ int sequence_len(const DecodeArgs& d, int b) {
+  const int64_t room = (int64_t)d.a.seqs.max_pages << d.a.cache.page_shift;
+  return (int)min((int64_t)max(__ldg(d.a.seqs.seq_lens + d.seq0 + b), 0), room);
+}
+
+// Tiles with a key that the token of a sequence of n keys sees; one (empty)
+// tile for a sequence without keys, so that its zeros get written.
+template <int kTile>
+__device__ __forceinline__ void tiles_of(const AttnArgs& a, int n, int* lo, int* sink_tiles,
+                                         int* first_tile, int* tiles) {
+  *lo = a.window && n > a.window ? n - a.window : 0;
+  *first_tile = *lo / kTile;
+  *sink_tiles = min((a.sinks + kTile - 1) / kTile, *first_tile);
+  *tiles = max(1, *sink_tiles + (n + kTile - 1) / kTile - *first_tile);
+}
+
+template <typename Tok, int D, int kMT>
+__device__ __forceinline__ Unit locate(const DecodeArgs& d, const DecodeShared<kMT>& sh,
+                                       long long tile, long long* unit_first) {
+  int lo = 0, hi = d.num_seqs;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sh.prefix[mid] <= tile) lo = mid;
+    else hi = mid;
+  }
+  Unit u;
+  u.b = lo;
+  u.len = sequence_len(d, lo);
+  tiles_of<Shape<Tok, D>::kTile>(d.a, u.len, &u.lo, &u.sink_tiles, &u.first_tile, &u.tiles);
+  const int i = (int)((tile - sh.prefix[lo]) / u.tiles);
+  *unit_first = sh.prefix[lo] + (long long)i * u.tiles;
+  u.kvh = i / d.head_blocks;
+  const int blk = i - u.kvh * d.head_blocks;
+  u.head0 = u.kvh * d.a.group + blk * 16 * kMT;
+  u.rows = min(16 * kMT, d.a.group - blk * 16 * kMT);
+  return u;
+}
+
+// ---------------------------------------------------------------- consumers --
+__device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_bf16(float* c, const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The keys of a tile: key j lies in row j of its box, boxes of box_rows rows
+// of kSubs columns of 128 bytes, 16-byte pieces swapped by the row (the
+// tensor copy's 128-byte swizzle).
+__device__ __forceinline__ uint32_t box_row(int j, int box_rows, int box_shift, int subs) {
+  return (uint32_t)(((j >> box_shift) * subs << box_shift) + (j & (box_rows - 1))) * 128u;
+}
+
+// One warp: 16 query heads x the warp's share of each tile's keys.
+// Result element i of a lane: row row(i), column col(i).
+template <typename Tok, int D>
+struct Consumer;
+
+template <int D>
+struct Consumer<__nv_bfloat16, D> {
+  using S = Shape<__nv_bfloat16, D>;
+  uint32_t q[D / 16][4];
+  float m[2], l[2];          // rows lane / 4 and lane / 4 + 8; l: this lane's keys only
+  float acc[S::kAcc];
+
+  static __device__ __forceinline__ int row(int i, int lane) { return lane / 4 + (i & 2) * 4; }
+  static __device__ __forceinline__ int col(int i, int lane) {
+    return (i >> 2) * 8 + (lane & 3) * 2 + (i & 1);
+  }
+  __device__ __forceinline__ void start(uint32_t q_addr, int lane) {
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+      ldmatrix_x4(q_addr + (uint32_t)((lane & 15) * S::kQRow + k * 32 + (lane >> 4) * 16), q[k]);
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < S::kAcc; ++i) acc[i] = 0.f;
+  }
+  // vis: bit j set: key j of this warp's 16 is seen (all ones: no mask).
+  __device__ __forceinline__ void tile(uint32_t k_addr, uint32_t v_addr, int group, int lane,
+                                       float scale, uint32_t vis, const DecodeArgs& d, float*) {
+    const int x = lane & 7;
+    const uint32_t box = (uint32_t)d.box_rows * 128u;
+    const uint32_t krow = k_addr + box_row(group * 16 + (lane >> 4) * 8 + x, d.box_rows,
+                                           d.box_shift, S::kSubs);
+    float s[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t b[4];
+      const int c = (k & 3) * 2 + ((lane >> 3) & 1);
+      ldmatrix_x4(krow + (uint32_t)(k / 4) * box + (uint32_t)((c ^ x) << 4), b);
+      mma_bf16(s[0], q[k], b[0], b[1]);
+      mma_bf16(s[1], q[k], b[2], b[3]);
+    }
+    const int j0 = (lane & 3) * 2;       // this lane's keys: j0, j0 + 1, j0 + 8, j0 + 9
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[n][e] = (vis >> (n * 8 + j0 + (e & 1))) & 1u ? s[n][e] * scale : -INFINITY;
+    float top[2], base[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 1));
+      top[r] = fmaxf(m[r], fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 2)));
+    }
+    // The maximum rarely moves after the first tiles: rescale only then.
+    if (__any_sync(kFullMask, top[0] != m[0] || top[1] != m[1])) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float keep = top[r] == -INFINITY ? 0.f : exp2_approx(m[r] - top[r]);
+        l[r] *= keep;
+#pragma unroll
+        for (int i = 0; i < S::kAcc; ++i)
+          if (((i >> 1) & 1) == r) acc[i] *= keep;
+        m[r] = top[r];
+      }
+    }
+    uint32_t p[4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      base[r] = top[r] == -INFINITY ? 0.f : top[r];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t w = pack_bf16(exp2_approx(s[n][2 * r] - base[r]),
+                                     exp2_approx(s[n][2 * r + 1] - base[r]));
+        l[r] += bf16_lo(w) + bf16_hi(w);
+        p[2 * n + r] = w;
+      }
+    }
+    // Values of keys that are not seen may be anything: they count as zeros.
+    uint32_t keep[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+      keep[n] = ((vis >> (n * 8 + j0)) & 1u ? 0x0000ffffu : 0u) |
+                ((vis >> (n * 8 + j0 + 1)) & 1u ? 0xffff0000u : 0u);
+    const bool whole = (vis & 0xffffu) == 0xffffu;
+    const uint32_t vrow = v_addr + box_row(group * 16 + ((lane >> 3) & 1) * 8 + x, d.box_rows,
+                                           d.box_shift, S::kSubs);
+#pragma unroll
+    for (int n = 0; n < D / 16; ++n) {
+      uint32_t b[4];
+      const int c = (n & 3) * 2 + (lane >> 4);
+      ldmatrix_x4_trans(vrow + (uint32_t)(n / 4) * box + (uint32_t)((c ^ x) << 4), b);
+      if (!whole) {
+        b[0] &= keep[0];
+        b[1] &= keep[1];
+        b[2] &= keep[0];
+        b[3] &= keep[1];
+      }
+      mma_bf16(acc + 8 * n, p, b[0], b[1]);
+      mma_bf16(acc + 8 * n + 4, p, b[2], b[3]);
+    }
+  }
+  // Joins the piece (ms, ls, o) of other keys, o laid out as acc.
+  __device__ __forceinline__ void merge(const float* ms, const float* ls, const float* o, int lane,
+                                        float*) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float mo = ms[lane / 4 + 8 * r], top = fmaxf(m[r], mo);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = exp2_approx(m[r] - base), g = exp2_approx(mo - base);
+      l[r] = l[r] * f + ((lane & 3) == 0 ? ls[lane / 4 + 8 * r] * g : 0.f);
+      m[r] = top;
+#pragma unroll
+      for (int i = 0; i < S::kAcc; ++i)
+        if (((i >> 1) & 1) == r) acc[i] = acc[i] * f + o[i * 32 + lane] * g;
+    }
+  }
+  // Row statistics to shared memory (16 each).
+  __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float t = l[r];
+      t += __shfl_xor_sync(kFullMask, t, 1);
+      t += __shfl_xor_sync(kFullMask, t, 2);
+      if ((lane & 3) == 0) {
+        ms[lane / 4 + 8 * r] = m[r];
+        ls[lane / 4 + 8 * r] = t;
+      }
+    }
+  }
+};
+
+template <int D>
+struct Consumer<float, D> {
+  using S = Shape<float, D>;
+  static constexpr int kW = D / 32;    // result columns per lane
+  uint32_t q_addr;
+  float m[4], l[4];          // heads 4 (lane / 8) ..; l: this lane's key (lane % 8) only
+  float acc[S::kAcc];        // [16 heads][kW]
+
+  static __device__ __forceinline__ int row(int i, int) { return i / kW; }
+  static __device__ __forceinline__ int col(int i, int lane) { return lane * kW + i % kW; }
+  __device__ __forceinline__ void start(uint32_t q_smem, int) {
+    q_addr = q_smem;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kAcc; ++i) acc[i] = 0.f;
+  }
+  __device__ __forceinline__ static float4 lds4(uint32_t addr) {
+    const uint4 v = lds128(addr);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                       __uint_as_float(v.w));
+  }
+  // p: this warp's 8 keys x 16 heads (and 16 factors) in shared memory.
+  __device__ __forceinline__ void tile(uint32_t k_addr, uint32_t v_addr, int group, int lane,
+                                       float scale, uint32_t vis, const DecodeArgs& d, float* p) {
+    const int t = lane & 7, hg = lane >> 3;
+    const uint32_t box = (uint32_t)d.box_rows * 128u;
+    const uint32_t krow = k_addr + box_row(group * 8 + t, d.box_rows, d.box_shift, S::kSubs);
+    float s[4] = {};
+#pragma unroll 4
+    for (int c = 0; c < D / 4; ++c) {
+      const float4 kx = lds4(krow + (uint32_t)(c >> 3) * box + (uint32_t)(((c & 7) ^ t) << 4));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 qx = lds4(q_addr + (uint32_t)((hg * 4 + i) * S::kQRow + c * 16));
+        s[i] = fmaf(qx.x, kx.x, s[i]);
+        s[i] = fmaf(qx.y, kx.y, s[i]);
+        s[i] = fmaf(qx.z, kx.z, s[i]);
+        s[i] = fmaf(qx.w, kx.w, s[i]);
+      }
+    }
+    const bool seen = (vis >> t) & 1u;
+    float top[4];
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[i] = seen ? s[i] * scale : -INFINITY;
+      top[i] = s[i];
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1)
+        top[i] = fmaxf(top[i], __shfl_xor_sync(kFullMask, top[i], o));
+      top[i] = fmaxf(top[i], m[i]);
+      moved |= top[i] != m[i];
+    }
+    moved = __any_sync(kFullMask, moved);
+    __syncwarp();                                // the last tile's p has been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float base = top[i] == -INFINITY ? 0.f : top[i];
+      if (moved) {
+        const float keep = top[i] == -INFINITY ? 0.f : exp2_approx(m[i] - top[i]);
+        l[i] *= keep;
+        if (t == 0) p[128 + hg * 4 + i] = keep;
+        m[i] = top[i];
+      }
+      const float e = exp2_approx(s[i] - base);
+      l[i] += e;
+      p[t * 16 + hg * 4 + i] = e;
+    }
+    __syncwarp();
+    if (moved) {
+#pragma unroll
+      for (int h = 0; h < 16; ++h) {
+        const float keep = p[128 + h];
+#pragma unroll
+        for (int w = 0; w < kW; ++w) acc[h * kW + w] *= keep;
+      }
+    }
+    const uint32_t p_addr = smem_addr(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (!((vis >> j) & 1u)) continue;          // not seen: its value may be anything
+      const uint32_t vrow = v_addr + box_row(group * 8 + j, d.box_rows, d.box_shift, S::kSubs);
+      float vx[kW];
+      if constexpr (kW == 4) {
+        const float4 v4 = lds4(vrow + (uint32_t)(lane >> 3) * box + (uint32_t)(((lane & 7) ^ j) << 4));
+        vx[0] = v4.x; vx[1] = v4.y; vx[2] = v4.z; vx[3] = v4.w;
+      } else {
+        const uint32_t at = vrow + (uint32_t)(lane >> 4) * box +
+                            (uint32_t)((((lane >> 1) & 7) ^ j) << 4) + (uint32_t)(lane & 1) * 8;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(at));
+      }
+#pragma unroll
+      for (int h = 0; h < 16; h += 4) {
+        const float4 e = lds4(p_addr + (uint32_t)(j * 16 + h) * 4);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          acc[(h + 0) * kW + w] = fmaf(e.x, vx[w], acc[(h + 0) * kW + w]);
+          acc[(h + 1) * kW + w] = fmaf(e.y, vx[w], acc[(h + 1) * kW + w]);
+          acc[(h + 2) * kW + w] = fmaf(e.z, vx[w], acc[(h + 2) * kW + w]);
+          acc[(h + 3) * kW + w] = fmaf(e.w, vx[w], acc[(h + 3) * kW + w]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void merge(const float* ms, const float* ls, const float* o, int lane,
+                                        float* p) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = (lane >> 3) * 4 + i;
+      const float mo = ms[h], top = fmaxf(m[i], mo);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = exp2_approx(m[i] - base), g = exp2_approx(mo - base);
+      l[i] = l[i] * f + ((lane & 7) == 0 ? ls[h] * g : 0.f);
+      m[i] = top;
+      if ((lane & 7) == 0) {
+        p[h] = f;
+        p[16 + h] = g;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < S::kAcc; ++i)
+      acc[i] = acc[i] * p[i / kW] + o[i * 32 + lane] * p[16 + i / kW];
+  }
+  __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t = l[i];
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(kFullMask, t, o);
+      if ((lane & 7) == 0) {
+        ms[(lane >> 3) * 4 + i] = m[i];
+        ls[(lane >> 3) * 4 + i] = t;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<uint32_t*>(p) = pack_bf16(a, b);
+}
+__device__ __forceinline__ void store_pair(float* p, float a, float b) {
+  *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+
+// 1 / (l + e^(sink - m)) in the scale of m, for a row with running maximum m
+// and sum l: out = o * that.
+__device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, float l) {
+  float f = 1.f;
+  if (a.sink_logits != nullptr) {
+    const float z = __ldg(a.sink_logits + head) * kLog2e;
+    const float top = fmaxf(m, z), base = top == -INFINITY ? 0.f : top;
+    f = exp2_approx(m - base);
+    l = l * f + exp2_approx(z - base);
+  }
+  return l == 0.f ? 0.f : f / l;
+}
+
+template <typename Tok, int D, int kMT>
+__global__ void __launch_bounds__(32 * (1 + kGroups * kMT))
+attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs d) {
+  using S = Shape<Tok, D, kMT>;
+  constexpr int kThreads = 32 * (1 + kGroups * kMT), kConsumers = kThreads - 32;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  unsigned char* q_smem = ring + (size_t)S::kStages * 2 * S::kHalf;
+  float* merge = reinterpret_cast<float*>(q_smem + kQSlots * 16 * kMT * S::kQRow);
+  float* p_smem = merge + (size_t)kMT * 2 * S::kAcc * 32;            // float32: p per warp
+  constexpr int kPFloats = sizeof(Tok) == 4 ? 144 : 0;
+  DecodeShared<kMT>& sh =
+      *reinterpret_cast<DecodeShared<kMT>*>(p_smem + kGroups * kMT * kPFloats);
+  const AttnArgs& a = d.a;
+  const int warp = __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], kGroups * kMT);
+    }
+    for (int s = 0; s < kQSlots; ++s) {
+      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.q_empty[s], kGroups * kMT);
+    }
+    fence_mbar_init();
+  }
+  pdl_wait();
+
+  // Prefix sums of the sequences' tiles: each thread sums a run of them, then
+  // the runs are scanned.
+  {
+    const int per = (d.num_seqs + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, d.num_seqs), b1 = min(b0 + per, d.num_seqs);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int n = sequence_len(d, b);
+      int lo, st, ft, tiles;
+      tiles_of<S::kTile>(a, n, &lo, &st, &ft, &tiles);
+      if (blockIdx.x == 0 && __ldg(a.seqs.seq_lens + d.seq0 + b) > n)
+        atomicAdd(&a.status[kStatusBadPages], 1ull);
+      mine += (long long)tiles * d.units_per_seq;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(kFullMask, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    long long run = incl - mine;
+    for (int w = 0; w < warp; ++w) run += sh.scan[w];
+    for (int b = b0; b < b1; ++b) {
+      int lo, st, ft, tiles;
+      tiles_of<S::kTile>(a, sequence_len(d, b), &lo, &st, &ft, &tiles);
+      sh.prefix[b] = run;
+      run += (long long)tiles * d.units_per_seq;
+    }
+    if (b1 == d.num_seqs && b0 < b1) sh.prefix[d.num_seqs] = run;
+    __syncthreads();
+  }
+  const long long total = sh.prefix[d.num_seqs];
+  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);
+  const long long t0 = per * blockIdx.x, t1 = min(t0 + per, total);
+  if (t0 >= t1) return;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      bool ok = true;
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, q_phase = 0;
+      const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+      for (long long t = t0; t < t1 && ok;) {
+        long long first;
+        const Unit u = locate<Tok, D, kMT>(d, sh, t, &first);
+        const int i0 = (int)(t - first), i1 = (int)min((long long)u.tiles, t1 - first);
+        t = first + i1;
+        if (!mbar_wait(&sh.q_empty[slot], q_phase ^ 1u)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sh.q_full[slot], (uint32_t)(u.rows * D * sizeof(Tok)));
+        const Tok* q = static_cast<const Tok*>(a.q) + (int64_t)(d.seq0 + u.b) * a.q_token +
+                       (int64_t)u.head0 * a.q_head;
+        for (int r = 0; r < u.rows; ++r)
+          bulk_copy_g2s(q_smem + (size_t)(slot * 16 * kMT + r) * S::kQRow, q + r * a.q_head,
+                        D * sizeof(Tok), &sh.q_full[slot], keep);
+        if (++slot == kQSlots) {
+          slot = 0;
+          q_phase ^= 1u;
+        }
+        const int* table = a.seqs.page_table + (int64_t)(d.seq0 + u.b) * a.seqs.table_stride;
+        for (int i = i0; i < i1; ++i) {
+          const int j0 = (i < u.sink_tiles ? i : u.first_tile + i - u.sink_tiles) * S::kTile;
+          if (!mbar_wait(&sh.empty[stage], phase ^ 1u)) { ok = false; break; }
+          unsigned char* dst = ring + (size_t)stage * 2 * S::kHalf;
+          // Boxes with a key that is seen.
+          uint32_t boxes = 0;
+          for (int x = 0; x < S::kTile; x += d.box_rows) {
+            const int k0 = j0 + x, k1 = min(k0 + d.box_rows, u.len);
+            if (k0 < k1 && (k1 > u.lo || k0 < a.sinks)) boxes |= 1u << (x >> d.box_shift);
+          }
+          const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
+          if (boxes == 0) {
+            mbar_arrive(&sh.full[stage]);
+          } else {
+            mbar_arrive_expect_tx(&sh.full[stage], 2u * __popc(boxes) * box_bytes);
+            for (uint32_t left = boxes; left; left &= left - 1) {
+              const int x = (__ffs(left) - 1) << d.box_shift, key = j0 + x;
+              // An id out of range reads as zeros (the copy's fill).
+              const int id = __ldg(table + (key >> a.cache.page_shift));
+              if ((unsigned)id >= (uint64_t)a.cache.num_pages)
+                atomicAdd(&a.status[kStatusBadPages], 1ull);
+              const int s0 = key & (a.cache.page_size - 1);
+              unsigned char* at = dst + (size_t)x * D * sizeof(Tok);
+              tma_load_5d(at, &maps.k, 0, s0, 0, u.kvh, id, &sh.full[stage], once);
+              tma_load_5d(at + S::kHalf, &maps.v, 0, s0, 0, u.kvh, id, &sh.full[stage], once);
+            }
+          }
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+    }
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  // A wait that gives up is recorded; the warp then goes on without waiting,
+  // so that every warp still reaches every barrier and the workspace's
+  // counters end as they should.
+  const int cw = warp - 1, group = cw % kGroups, mt = cw / kGroups;
+  const int bar = 1 + mt;                                   // the four warps of 16 heads
+  float* buf = merge + (size_t)mt * 2 * S::kAcc * 32;
+  float* p_warp = p_smem + cw * kPFloats;
+  const float scale = a.scale * kLog2e;
+  Consumer<Tok, D> c;
+  bool ok = true;
+  int stage = 0, slot = 0;
+  uint32_t phase = 0, q_phase = 0;
+  for (long long t = t0; t < t1;) {
+    long long first;
+    const Unit u = locate<Tok, D, kMT>(d, sh, t, &first);
+    const int i0 = (int)(t - first), i1 = (int)min((long long)u.tiles, t1 - first);
+    t = first + i1;
+    ok = ok && mbar_wait_warp(&sh.q_full[slot], q_phase);
+    c.start(smem_addr(q_smem) + (uint32_t)((slot * kMT + mt) * 16 * S::kQRow), lane);
+    if constexpr (sizeof(Tok) == 2) {                       // the queries are in registers now
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_empty[slot]);
+    }
+    for (int i = i0; i < i1; ++i) {
+      const int j0 = (i < u.sink_tiles ? i : u.first_tile + i - u.sink_tiles) * S::kTile;
+      uint32_t vis = 0xffffffffu;
+      if (!(j0 + S::kTile <= u.len && (j0 >= u.lo || j0 + S::kTile <= a.sinks))) {
+        const int key = j0 + group * S::kPer + lane;
+        vis = __ballot_sync(kFullMask, lane < S::kPer && key < u.len &&
+                                           (key >= u.lo || key < a.sinks));
+      }
+      ok = ok && mbar_wait_warp(&sh.full[stage], phase);
+      const uint32_t at = smem_addr(ring) + (uint32_t)stage * 2 * S::kHalf;
+      c.tile(at, at + S::kHalf, group, lane, scale, vis, d, p_warp);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.empty[stage]);
+      if (++stage == S::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if constexpr (sizeof(Tok) == 4) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_empty[slot]);
+    }
+    if (++slot == kQSlots) {
+      slot = 0;
+      q_phase ^= 1u;
+    }
+
+    // The four groups' (m, l, o), joined in two rounds: 2 into 0 and 3 into
+    // 1, then 1 into 0.
+#pragma unroll
+    for (int half = 2; half >= 1; half >>= 1) {
+      float* mine = buf + (size_t)(group & (half - 1)) * S::kAcc * 32;
+      float* ms = sh.merge_m[mt][group & (half - 1)];
+      float* ls = sh.merge_l[mt][group & (half - 1)];
+      if (group >= half && group < 2 * half) {
+        c.stats(ms, ls, lane);
+#pragma unroll
+        for (int i = 0; i < S::kAcc; ++i) mine[i * 32 + lane] = c.acc[i];
+      }
+      bar_sync(bar, 32 * kGroups);
+      if (group < half) c.merge(ms, ls, mine, lane, p_warp);
+      bar_sync(bar, 32 * kGroups);
+    }
+    const bool whole = i0 == 0 && i1 == u.tiles;
+    if (group == 0) {
+      float* ms = sh.merge_m[mt][0];
+      float* ls = sh.merge_l[mt][0];
+      c.stats(ms, ls, lane);
+      __syncwarp();
+      if (whole) {
+        Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
+#pragma unroll
+        for (int i = 0; i < S::kAcc; i += 2) {
+          const int r = Consumer<Tok, D>::row(i, lane), rr = mt * 16 + r;
+          if (rr < u.rows) {
+            const float inv = finish(a, u.head0 + rr, ms[r], ls[r]);
+            store_pair(out + (int64_t)rr * D + Consumer<Tok, D>::col(i, lane), c.acc[i] * inv,
+                       c.acc[i + 1] * inv);
+          }
+        }
+      } else {
+        unsigned char* piece = d.pieces + (size_t)(2 * blockIdx.x + (i0 == 0 ? 1 : 0)) * kPieceBytes;
+        float* o = reinterpret_cast<float*>(piece);
+        float* st = o + kRowsMax * 128;
+#pragma unroll
+        for (int i = 0; i < S::kAcc; i += 2) {
+          const int rr = mt * 16 + Consumer<Tok, D>::row(i, lane);
+          if (rr < u.rows)
+            *reinterpret_cast<float2*>(o + rr * D + Consumer<Tok, D>::col(i, lane)) =
+                make_float2(c.acc[i], c.acc[i + 1]);
+        }
+        if (lane < 16 && mt * 16 + lane < u.rows) {
+          st[mt * 16 + lane] = ms[lane];
+          st[kRowsMax + mt * 16 + lane] = ls[lane];
+        }
+        __threadfence();
+      }
+    }
+    if (!whole) {
+      // The unit's CTAs are those that own its tiles' runs; the first owns
+      // the counter. The last to arrive joins.
+      const int c_first = (int)(first / per), c_last = (int)((first + u.tiles - 1) / per);
+      bar_sync(1 + kMT, kConsumers);
+      if (cw == 0 && lane == 0)
+        sh.last = atomicInc(d.counters + c_first, (unsigned)(c_last - c_first)) ==
+                  (unsigned)(c_last - c_first);
+      bar_sync(1 + kMT, kConsumers);
+      if (sh.last) {
+        __threadfence();
+        const int n = c_last - c_first + 1;
+        Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
+        for (int r = cw; r < u.rows; r += kGroups * kMT) {
+          auto piece = [&](int k) {
+            return reinterpret_cast<const float*>(
+                d.pieces + (size_t)(2 * (c_first + k) + (k == 0 ? 1 : 0)) * kPieceBytes);
+          };
+          float m = -INFINITY;
+          for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(piece(k) + kRowsMax * 128 + r));
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
+          const float base = m == -INFINITY ? 0.f : m;
+          float l = 0.f, o[D / 32] = {};
+#pragma unroll 4
+          for (int k = 0; k < n; ++k) {
+            const float* pk = piece(k);
+            const float f = exp2_approx(__ldcg(pk + kRowsMax * 128 + r) - base);
+            l = fmaf(__ldcg(pk + kRowsMax * 128 + kRowsMax + r), f, l);
+            if constexpr (D == 128) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(pk + r * D) + lane);
+              o[0] = fmaf(x.x, f, o[0]);
+              o[1] = fmaf(x.y, f, o[1]);
+              o[2] = fmaf(x.z, f, o[2]);
+              o[3] = fmaf(x.w, f, o[3]);
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(pk + r * D) + lane);
+              o[0] = fmaf(x.x, f, o[0]);
+              o[1] = fmaf(x.y, f, o[1]);
+            }
+          }
+          const float inv = finish(a, u.head0 + r, m, l);
+#pragma unroll
+          for (int w = 0; w < D / 32; w += 2)
+            store_pair(out + (int64_t)r * D + lane * (D / 32) + w, o[w] * inv, o[w + 1] * inv);
+        }
+      }
+    }
+    // ms and ls of group 0 are read before the next unit's rounds write them.
+    bar_sync(bar, 32 * kGroups);
+  }
+  if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+}
+
+// The keys (or values) as (128 bytes, slot, 128-byte column of the row, head,
+// page), copied box_rows slots of one head of one page at a time: each column
+// lands as box_rows rows of 128 bytes, swizzled. A dimension of one element
+// needs no stride; 16 stands in.
+bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, CUtensorMap* map) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (enc == nullptr) return false;
+  const bool bf16 = c.token_dtype == kTokenBF16;
+  const cuuint64_t es = bf16 ? 2 : 4, sub = 128 / es, subs = c.head_dim / sub;
+  const int64_t page = values ? c.v_page : c.k_page, head = values ? c.v_head : c.k_head,
+                slot = values ? c.v_slot : c.k_slot;
+  const cuuint64_t dims[5] = {sub, (cuuint64_t)c.page_size, subs, (cuuint64_t)c.kv_heads,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)slot * es, 128,
+                                 c.kv_heads > 1 ? (cuuint64_t)head * es : 16,
+                                 c.num_pages > 1 ? (cuuint64_t)page * es : 16};
+  const cuuint32_t box[5] = {(cuuint32_t)sub, (cuuint32_t)box_rows, (cuuint32_t)subs, 1, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5,
+             values ? c.v : c.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int num_sms() {
+  static int cached[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return 152;
+  if (cached[dev] == 0) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev] = n > 0 ? n : 152;
+  }
+  return cached[dev];
+}
+
+template <typename Tok, int D, int kMT>
+cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  using S = Shape<Tok, D, kMT>;
+  DecodeArgs d = {};
+  d.a = a;
+  d.head_blocks = (a.group + 16 * kMT - 1) / (16 * kMT);
+  d.units_per_seq = a.cache.kv_heads * d.head_blocks;
+  d.box_rows = std::min(a.cache.page_size, S::kTile);
+  while ((1 << d.box_shift) < d.box_rows) ++d.box_shift;
+  d.counters = static_cast<unsigned int*>(workspace);
+  d.pieces = static_cast<unsigned char*>(workspace) + kCounterBytes;
+  DecodeMaps maps;
+  if (!kv_tensor_map(a.cache, false, d.box_rows, &maps.k) ||
+      !kv_tensor_map(a.cache, true, d.box_rows, &maps.v))
+    return cudaErrorInvalidValue;
+  constexpr size_t smem = 1024 + (size_t)S::kStages * 2 * S::kHalf +
+                          (size_t)kQSlots * 16 * kMT * S::kQRow +
+                          (size_t)kMT * 2 * S::kAcc * 32 * 4 +
+                          (sizeof(Tok) == 4 ? (size_t)kGroups * kMT * 144 * 4 : 0) +
+                          sizeof(DecodeShared<kMT>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t err = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    err = cudaFuncSetAttribute(attention_decode_kernel<Tok, D, kMT>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (err != cudaSuccess) return err;
+  // No more CTAs than runs of kMinTiles tiles at the longest lengths the page
+  // tables could hold.
+  const int64_t room = ((int64_t)a.seqs.max_pages << a.cache.page_shift) / S::kTile + 2;
+  for (int b = 0; b < a.seqs.num_seqs; b += kMaxSeqs) {
+    d.seq0 = b;
+    d.num_seqs = std::min(kMaxSeqs, a.seqs.num_seqs - b);
+    const int64_t most = ((int64_t)d.num_seqs * d.units_per_seq * room + kMinTiles - 1) / kMinTiles;
+    const int grid = (int)std::min<int64_t>(std::min(num_sms(), kMaxCtas), most);
+    err = launch_after_previous(attention_decode_kernel<Tok, D, kMT>, dim3((unsigned)grid),
+                                dim3(32 * (1 + kGroups * kMT)), smem, stream, maps, d);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+template <typename Tok, int D>
+cudaError_t launch_heads(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  if (a.group <= 16) return launch<Tok, D, 1>(a, workspace, stream);
+  if (a.group <= 32) return launch<Tok, D, 2>(a, workspace, stream);
+  return launch<Tok, D, 4>(a, workspace, stream);
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes() { return kCounterBytes + 2 * (size_t)kMaxCtas * kPieceBytes; }
+
+cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  if (a.cache.token_dtype == kTokenBF16)
+    return a.cache.head_dim == 64 ? launch_heads<__nv_bfloat16, 64>(a, workspace, stream)
+                                  : launch_heads<__nv_bfloat16, 128>(a, workspace, stream);
+  return a.cache.head_dim == 64 ? launch_heads<float, 64>(a, workspace, stream)
+                                : launch_heads<float, 128>(a, workspace, stream);
+}
+
+}  // namespace mxfp4el
