@@ -124,7 +124,7 @@ int mxfp4el_append_kv(const void* q, int64_t q_token_stride, int64_t q_head_stri
  * mxfp4el_attention_decode -- one new token of each sequence: row b of q
  * (num_seqs, num_heads, head_dim; strides as above) over the keys of
  * sequence b, the token's own among them. seqs->q_offsets must be NULL.
- * window 0: no window (sinks is then not used). sink_logits is (num_heads)
+ * scale is positive. window 0: no window (sinks is then not used). sink_logits is (num_heads)
  * float32 or NULL. out is (num_seqs, num_heads, head_dim), dense.
  *
  * `workspace` is a device buffer of at least

@@ -22,7 +22,7 @@ LIB = os.path.join(LIB_DIR, "libmxfp4_expert_linear.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "gemv.cu", "gemm_tc.cu", "combine.cu", "static_scratch.cu",
            "router.cu", "swiglu.cu", "prepare.cu", "attn_api.cu", "kv_append.cu",
-           "attn_simt.cu", "attn_decode.cu"]
+           "attn_simt.cu", "attn_decode.cu", "attn_prefill.cu"]
 
 
 def nvcc() -> str:

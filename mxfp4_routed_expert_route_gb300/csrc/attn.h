@@ -2,6 +2,8 @@
 // units (include/mxfp4el_attention.h).
 #pragma once
 
+#include <cuda.h>
+
 #include "internal.h"
 
 namespace mxfp4el {
@@ -62,6 +64,14 @@ struct AttnArgs {
 // through the workspace (attn_decode.cu).
 cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream);
 size_t decode_workspace_bytes();
+size_t decode_counter_bytes();     // the prefill kernel's counters follow them
+
+// bf16 prompts on the tensor cores (attn_prefill.cu).
+cudaError_t launch_attention_prefill(const AttnArgs& a, void* workspace, cudaStream_t stream);
+
+bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, int box_subs,
+                   CUtensorMap* map);
+int attention_num_sms();
 
 // Any dtype, any number of new tokens, on the CUDA cores (attn_simt.cu).
 cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream);

@@ -108,7 +108,7 @@ int check_attention(const void* q, int64_t q_token, int64_t q_head, const mxfp4e
   int rc = check_cache(cache, &a->cache, &ks, &vs);
   if (rc != MXFP4EL_OK) return rc;
   if (T < 0 || heads <= 0 || heads % a->cache.kv_heads != 0 || window < 0 || sinks < 0 ||
-      !std::isfinite(scale))
+      !(scale > 0.f) || !std::isfinite(scale))
     return MXFP4EL_ERR_INVALID_ARGUMENT;
   if (T > kMaxTokens || heads > kMaxHeads || heads / a->cache.kv_heads > kMaxGroup)
     return MXFP4EL_ERR_TOO_LARGE;
@@ -247,9 +247,12 @@ extern "C" int mxfp4el_attention_prefill(const void* q, int64_t q_token_stride,
       check_attention(q, q_token_stride, q_head_stride, cache, seqs, scale, window, sinks,
                       sink_logits, out, T, num_heads, workspace, workspace_bytes, &a, &nothing);
   if (rc != MXFP4EL_OK || nothing) return rc;
-  return launch_attention_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MXFP4EL_OK
-             : MXFP4EL_ERR_CUDA;
+  // float32 has no tensor-core path that keeps its 24 bits.
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = a.cache.token_dtype == kTokenBF16
+                              ? launch_attention_prefill(a, workspace, s)
+                              : launch_attention_simt(a, s);
+  return err == cudaSuccess ? MXFP4EL_OK : MXFP4EL_ERR_CUDA;
 }
 
 extern "C" int mxfp4el_page_errors(void* stream, int64_t* count) {

@@ -52,7 +52,8 @@ constexpr int kQSlots = 2;
 
 // Bytes of a piece in the workspace: rows of o (128 floats), m and l.
 constexpr size_t kPieceBytes = (size_t)kRowsMax * 128 * 4 + 2 * kRowsMax * 4;
-constexpr size_t kCounterBytes = (size_t)kMaxCtas * 4;
+// The workspace: this kernel's counters, the prefill kernel's, the pieces.
+constexpr size_t kCounterBytes = (size_t)kMaxCtas * 4, kPiecesAt = kCounterBytes + 256;
 
 template <typename Tok, int D, int kMT = 1>
 struct Shape {
@@ -761,43 +762,6 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
 }
 
-// The keys (or values) as (128 bytes, slot, 128-byte column of the row, head,
-// page), copied box_rows slots of one head of one page at a time: each column
-// lands as box_rows rows of 128 bytes, swizzled. A dimension of one element
-// needs no stride; 16 stands in.
-bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, CUtensorMap* map) {
-  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-  if (enc == nullptr) return false;
-  const bool bf16 = c.token_dtype == kTokenBF16;
-  const cuuint64_t es = bf16 ? 2 : 4, sub = 128 / es, subs = c.head_dim / sub;
-  const int64_t page = values ? c.v_page : c.k_page, head = values ? c.v_head : c.k_head,
-                slot = values ? c.v_slot : c.k_slot;
-  const cuuint64_t dims[5] = {sub, (cuuint64_t)c.page_size, subs, (cuuint64_t)c.kv_heads,
-                              (cuuint64_t)c.num_pages};
-  const cuuint64_t strides[4] = {(cuuint64_t)slot * es, 128,
-                                 c.kv_heads > 1 ? (cuuint64_t)head * es : 16,
-                                 c.num_pages > 1 ? (cuuint64_t)page * es : 16};
-  const cuuint32_t box[5] = {(cuuint32_t)sub, (cuuint32_t)box_rows, (cuuint32_t)subs, 1, 1};
-  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
-  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5,
-             values ? c.v : c.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int num_sms() {
-  static int cached[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64) return 152;
-  if (cached[dev] == 0) {
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cached[dev] = n > 0 ? n : 152;
-  }
-  return cached[dev];
-}
-
 template <typename Tok, int D, int kMT>
 cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   using S = Shape<Tok, D, kMT>;
@@ -808,10 +772,10 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   d.box_rows = std::min(a.cache.page_size, S::kTile);
   while ((1 << d.box_shift) < d.box_rows) ++d.box_shift;
   d.counters = static_cast<unsigned int*>(workspace);
-  d.pieces = static_cast<unsigned char*>(workspace) + kCounterBytes;
+  d.pieces = static_cast<unsigned char*>(workspace) + kPiecesAt;
   DecodeMaps maps;
-  if (!kv_tensor_map(a.cache, false, d.box_rows, &maps.k) ||
-      !kv_tensor_map(a.cache, true, d.box_rows, &maps.v))
+  if (!kv_tensor_map(a.cache, false, d.box_rows, S::kSubs, &maps.k) ||
+      !kv_tensor_map(a.cache, true, d.box_rows, S::kSubs, &maps.v))
     return cudaErrorInvalidValue;
   constexpr size_t smem = 1024 + (size_t)S::kStages * 2 * S::kHalf +
                           (size_t)kQSlots * 16 * kMT * S::kQRow +
@@ -835,7 +799,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     d.seq0 = b;
     d.num_seqs = std::min(kMaxSeqs, a.seqs.num_seqs - b);
     const int64_t most = ((int64_t)d.num_seqs * d.units_per_seq * room + kMinTiles - 1) / kMinTiles;
-    const int grid = (int)std::min<int64_t>(std::min(num_sms(), kMaxCtas), most);
+    const int grid = (int)std::min<int64_t>(std::min(attention_num_sms(), kMaxCtas), most);
     err = launch_after_previous(attention_decode_kernel<Tok, D, kMT>, dim3((unsigned)grid),
                                 dim3(32 * (1 + kGroups * kMT)), smem, stream, maps, d);
     if (err != cudaSuccess) return err;
@@ -852,7 +816,46 @@ cudaError_t launch_heads(const AttnArgs& a, void* workspace, cudaStream_t stream
 
 }  // namespace
 
-size_t decode_workspace_bytes() { return kCounterBytes + 2 * (size_t)kMaxCtas * kPieceBytes; }
+// The keys (or values) as (128 bytes, slot, 128-byte column of the row, head,
+// page), copied box_rows slots and box_subs columns of one head of one page at a
+// time: each column lands as box_rows rows of 128 bytes, swizzled. A dimension of one element
+// needs no stride; 16 stands in.
+bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, int box_subs,
+                   CUtensorMap* map) {
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (enc == nullptr) return false;
+  const bool bf16 = c.token_dtype == kTokenBF16;
+  const cuuint64_t es = bf16 ? 2 : 4, sub = 128 / es, subs = c.head_dim / sub;
+  const int64_t page = values ? c.v_page : c.k_page, head = values ? c.v_head : c.k_head,
+                slot = values ? c.v_slot : c.k_slot;
+  const cuuint64_t dims[5] = {sub, (cuuint64_t)c.page_size, subs, (cuuint64_t)c.kv_heads,
+                              (cuuint64_t)c.num_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)slot * es, 128,
+                                 c.kv_heads > 1 ? (cuuint64_t)head * es : 16,
+                                 c.num_pages > 1 ? (cuuint64_t)page * es : 16};
+  const cuuint32_t box[5] = {(cuuint32_t)sub, (cuuint32_t)box_rows, (cuuint32_t)box_subs, 1, 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 5,
+             values ? c.v : c.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int attention_num_sms() {
+  static int cached[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return 152;
+  if (cached[dev] == 0) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev] = n > 0 ? n : 152;
+  }
+  return cached[dev];
+}
+
+size_t decode_counter_bytes() { return kCounterBytes; }
+size_t decode_workspace_bytes() { return kPiecesAt + 2 * (size_t)kMaxCtas * kPieceBytes; }
 
 cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   if (a.cache.token_dtype == kTokenBF16)

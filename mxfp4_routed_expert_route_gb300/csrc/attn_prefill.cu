@@ -1,0 +1,742 @@
+// attn_prefill.cu -- attention of prompts (or chunks behind a history) over
+// the paged cache on the tensor cores: tcgen05, tensor memory and tensor
+// copies. bf16 tokens.
+//
+// Rows. The query heads of one key head share its keys: a tile's 128 rows are
+// n = 128 / heads tokens times those heads (row i: token i / heads, head
+// i % heads), so a key or value is read once for all of them, short prompts
+// and short windows still fill tiles, and the causal edge cuts few of a
+// tile's scores. A unit of work is two such tiles (2 n tokens) of one key
+// head over every key that a row of it sees, in key tiles of 128:
+//
+//   S = Q K^T            two tiles' worth, into tensor memory (float32)
+//   P = 2^(c S - c m)    m: running row maximum, c = scale log2 e; bf16
+//   O += P V             P from tensor memory, V from shared memory
+//   l += sum P           out = O / l
+//
+// Bound: tensor throughput, 4 D operations per row and key, as long as the
+// powers keep up: the two tiles take turns, one in the tensor pipe while the
+// other's softmax runs.
+//
+// Warps of a CTA (one CTA per SM, units from a counter, the longest first):
+//   0-3, 4-7  softmax and epilogue of tile 0 and of tile 1: one thread per
+//             row, so row maxima and sums need no exchange between threads.
+//             O is rescaled only when a row's maximum grew by more than 8
+//             (2^8 fits every format here); the stale maximum is as good a
+//             base for the powers as the true one.
+//   8         takes units, copies queries, keys and values
+//   9         issues the matrix instructions
+//   10        values of key tiles that the mask cuts: rows that no query sees
+//             are zeroed (a masked score gives P = 0, but 0 times what a stale
+//             page holds need not be 0), and so are infinities and NaN.
+// A value that is not finite must reach the rows that see it and no other,
+// which a matrix product cannot do in a tile that the mask cuts: there it
+// counts as zero, and the epilogue computes the rows that may see it again,
+// one by one on the CUDA cores.
+//
+// P and the sum l: P is rounded to bf16 for the second product (a relative
+// error of 2^-8 at most, as the result's own rounding); l adds the float32
+// values.
+//
+// Every wait is bounded. A role whose wait gives up records it and goes on
+// without waiting, so that every role ends.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "attn.cuh"
+
+namespace mxfp4el {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRows = 128;              // query rows per tile
+constexpr int kKeys = 128;              // keys per tile
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kUnitRing = 2;
+constexpr int kUnitReaders = 2 + 8;     // MMA, cleaner, 8 softmax warps
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
+constexpr float kRescale = 8.f;
+
+template <int D>
+struct Shape {
+  static constexpr int kSubs = D / 64;                       // 128-byte columns of a row
+  static constexpr uint32_t kSub = 128 * 128;                // bytes: 128 rows of one column
+  static constexpr uint32_t kTileBytes = kSubs * kSub;
+  static constexpr int kStages = D == 128 ? 5 : 8;           // key and value tiles in flight
+};
+
+struct PrefillMaps {
+  CUtensorMap q;      // (64, head, column, token), box (64, group, 1, n)
+  CUtensorMap k, v;   // as the cache's maps, one column per box
+};
+
+struct PrefillArgs {
+  AttnArgs a;
+  int n;              // tokens per tile
+  int box_rows, box_shift;
+  long long units;    // slots x key heads
+  int slots;
+  unsigned int* counter;   // next unit; counter[1]: CTAs that are done
+};
+
+struct Unit {
+  int seq, kvh;       // seq < 0: the end
+  int row0, nt;       // first token row of the call, tokens (<= 2 n)
+  int pos0;           // position of the first token
+  int hi;             // keys below hi may be seen
+  int lo;             // first key of the first token's window
+  int start;          // first key of the first window tile
+  int sinks;          // keys below this are seen beside the window
+  int sink_tiles, tiles[2];     // key tiles for each row tile (tiles[1] >= tiles[0])
+};
+
+template <int D>
+struct __align__(16) PrefillShared {
+  uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages], raw[Shape<D>::kStages];
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t u_full[kUnitRing], u_empty[kUnitRing];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
+  Unit unit[kUnitRing];
+};
+
+// Key tile i of a unit: its first key, the keys below which a row may see it
+// (tiles of first keys end where the window's tiles begin) and the columns
+// that matter.
+struct KeyTile {
+  int j0, end, cols;
+  bool cut;           // the mask hides some of its keys from some of the unit's rows
+};
+__device__ __forceinline__ KeyTile key_tile(const Unit& u, int i, int window) {
+  KeyTile t;
+  const bool sink = i < u.sink_tiles;
+  t.j0 = sink ? i * kKeys : u.start + (i - u.sink_tiles) * kKeys;
+  t.end = sink ? min(u.sinks, u.start) : u.hi;
+  t.cols = min(kKeys, t.end - t.j0);
+  t.cut = sink || t.j0 + kKeys - 1 > u.pos0 || (window != 0 && t.j0 <= u.pos0 + u.nt - 1 - window);
+  return t;
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n"
+      " .reg .pred p;\n"
+      " .reg .b32 r;\n"
+      " elect.sync r|p, 0xffffffff;\n"
+      " selp.u32 %0, 1, 0, p;\n"
+      "}"
+      : "=r"(e));
+  return e != 0;
+}
+
+// Instruction descriptor of tcgen05.mma kind::f16, bf16 operands, float32
+// accumulator; b_rows_k: B's rows run along K (its columns are contiguous).
+__device__ __forceinline__ uint32_t mma_idesc(int n, bool b_rows_k) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows_k ? 1u << 16 : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+// Shared-memory descriptor, 128-byte swizzle: 8-row groups 1024 bytes apart.
+// For a B whose columns are contiguous, blocks of 64 columns are `lead` bytes
+// apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One row on the CUDA cores (see the top): its keys one after another.
+template <int D>
+__device__ __noinline__ void slow_row(const AttnArgs& a, const Unit& u, int token, int head) {
+  const __nv_bfloat16* q =
+      static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + token) * a.q_token + head * a.q_head;
+  const int pos = u.pos0 + token;
+  const float c = a.scale * kLog2e;
+  float m = -INFINITY, l = 0.f;
+  float o[D];
+  for (int d = 0; d < D; ++d) o[d] = 0.f;
+  for (int j = 0; j <= pos; ++j) {
+    if (!key_visible(j, pos, a.window, a.sinks)) {
+      j = max(j, pos - a.window);      // the next key is the window's first
+      continue;
+    }
+    const int64_t page = page_of(a.seqs, a.cache, u.seq, j >> a.cache.page_shift);
+    const int slot = j & (a.cache.page_size - 1);
+    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.cache.k) + page * a.cache.k_page +
+                             u.kvh * a.cache.k_head + slot * a.cache.k_slot;
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.cache.v) + page * a.cache.v_page +
+                             u.kvh * a.cache.v_head + slot * a.cache.v_slot;
+    float s = 0.f;
+    if (page >= 0)
+      for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+    s *= c;
+    const float top = fmaxf(m, s), base = top == -INFINITY ? 0.f : top;
+    const float keep = exp2_approx(m - base), p = exp2_approx(s - base);
+    m = top;
+    l = l * keep + p;
+    for (int d = 0; d < D; ++d)
+      o[d] = o[d] * keep + (page >= 0 ? p * __bfloat162float(v[d]) : 0.f);
+  }
+  float f = 1.f;
+  if (a.sink_logits != nullptr) {
+    const float z = __ldg(a.sink_logits + head) * kLog2e;
+    const float top = fmaxf(m, z), base = top == -INFINITY ? 0.f : top;
+    f = exp2_approx(m - base);
+    l = l * f + exp2_approx(z - base);
+  }
+  const float inv = f / l;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                       ((int64_t)(u.row0 + token) * a.heads + head) * D;
+  for (int d = 0; d < D; ++d) out[d] = __float2bfloat16_rn(l == 0.f ? 0.f : o[d] * inv);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p) {
+  using S = Shape<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* q_smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  unsigned char* ring = q_smem + 2 * S::kTileBytes;
+  PrefillShared<D>& sh =
+      *reinterpret_cast<PrefillShared<D>*>(ring + (size_t)S::kStages * S::kTileBytes);
+  const AttnArgs& a = p.a;
+  const int warp = __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+
+  pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.raw[s], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.s_full[t], 1);
+      mbar_init(&sh.p_full[t], 4);
+      mbar_init(&sh.o_full[t], 1);
+      mbar_init(&sh.o_empty[t], 4);
+    }
+    for (int r = 0; r < kUnitRing; ++r) {
+      mbar_init(&sh.u_full[r], 1);
+      mbar_init(&sh.u_empty[r], kUnitReaders);
+    }
+    mbar_init(&sh.drain, 32);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&sh.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem_base, 0);
+  pdl_wait();
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------ units and copies
+    const uint64_t keep = l2_evict_normal_policy();
+    int slot = 0, stage = 0;
+    uint32_t u_phase = 0, phase = 0, q_phase = 0;
+    unsigned next = 0;
+    if (lane == 0) next = atomicAdd(p.counter, 1u);
+    next = __shfl_sync(kFullMask, next, 0);
+    for (;;) {
+      const unsigned idx = next;
+      Unit u;
+      u.seq = -1;
+      if ((long long)idx < p.units) {
+        if (lane == 0) next = atomicAdd(p.counter, 1u);
+        next = __shfl_sync(kFullMask, next, 0);
+        u.kvh = (int)(idx % (unsigned)a.cache.kv_heads);
+        const int at = p.slots - 1 - (int)(idx / (unsigned)a.cache.kv_heads);
+        const int b = sequence_of_slot(a.seqs, at, a.T, 2 * p.n, lane);
+        const SeqRows r =
+            sequence_rows(a.seqs, b, a.T, a.cache.page_shift, a.status, lane == 0 && u.kvh == 0);
+        const int tile = a.seqs.q_offsets == nullptr ? 0 : at - (r.first / (2 * p.n) + b);
+        const int t0 = tile * 2 * p.n;
+        u.nt = min(2 * p.n, r.count - t0);
+        if (u.nt <= 0) continue;
+        u.seq = b;
+        u.row0 = r.first + t0;
+        u.pos0 = r.pos0 + t0;
+        u.hi = max(0, u.pos0 + u.nt);
+        u.lo = a.window ? max(0, u.pos0 - a.window + 1) : 0;
+        u.start = u.lo & ~(p.box_rows - 1);
+        u.sinks = a.sinks;
+        u.sink_tiles = (min(a.sinks, u.start) + kKeys - 1) / kKeys;
+        // Keys that the first row tile sees end at its last token.
+        const int hi0 = max(0, u.pos0 + min(u.nt, p.n));
+        u.tiles[1] = u.hi > 0 ? u.sink_tiles + (u.hi - u.start + kKeys - 1) / kKeys : 0;
+        u.tiles[0] = hi0 > 0 ? u.sink_tiles + (hi0 - u.start + kKeys - 1) / kKeys : 0;
+        if (u.nt <= p.n) u.tiles[1] = 0;
+      }
+      ok = ok && mbar_wait_warp(&sh.u_empty[slot], u_phase ^ 1u);
+      if (lane == 0) {
+        sh.unit[slot] = u;
+        sh.bad_lo[slot] = 0x7fffffff;
+        sh.bad_hi[slot] = -1;
+        mbar_arrive(&sh.u_full[slot]);
+      }
+      __syncwarp();
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+      if (u.seq < 0) break;
+      const int tiles = max(u.tiles[0], u.tiles[1]);
+      if (tiles == 0 || !ok) continue;
+
+      ok = ok && mbar_wait_warp(&sh.q_empty, q_phase ^ 1u);
+      q_phase ^= 1u;
+      const int row_tiles = u.nt > p.n ? 2 : 1;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&sh.q_full,
+                              (uint32_t)(row_tiles * S::kSubs * p.n * a.group * 128));
+        for (int t = 0; t < row_tiles; ++t)
+          for (int c = 0; c < S::kSubs; ++c)
+            tma_load_4d(q_smem + t * S::kTileBytes + c * S::kSub, &maps.q, 0, u.kvh * a.group, c,
+                        u.row0 + t * p.n, &sh.q_full, keep);
+      }
+      const int* table = a.seqs.page_table + (int64_t)u.seq * a.seqs.table_stride;
+      for (int i = 0; i < tiles && ok; ++i) {
+        const KeyTile kt = key_tile(u, i, a.window);
+        // Lane x copies box x, if a row sees a key of it.
+        const int key = kt.j0 + lane * p.box_rows;
+        const bool want = lane < (kKeys >> p.box_shift) && key < kt.end &&
+                          (i < u.sink_tiles || key + p.box_rows > u.lo || key < u.sinks);
+        int id = 0;
+        if (want) {
+          id = __ldg(table + (key >> a.cache.page_shift));
+          if ((unsigned)id >= (uint64_t)a.cache.num_pages)
+            atomicAdd(&a.status[kStatusBadPages], 1ull);
+        }
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kFullMask, want)) *
+                               (uint32_t)p.box_rows * 128u * S::kSubs;
+        for (int v = 0; v < 2; ++v) {
+          ok = ok && mbar_wait_warp(&sh.empty[stage], phase ^ 1u);
+          uint64_t* bar = v && kt.cut ? &sh.raw[stage] : &sh.full[stage];
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (want) {
+            unsigned char* dst = ring + (size_t)stage * S::kTileBytes + (size_t)lane * p.box_rows * 128;
+            for (int c = 0; c < S::kSubs; ++c)
+              tma_load_5d(dst + c * S::kSub, v ? &maps.v : &maps.k, 0,
+                          key & (a.cache.page_size - 1), c, u.kvh, id, bar, keep);
+          }
+          __syncwarp();
+          if (++stage == S::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    if (lane == 0) {
+      // The last CTA to take its end leaves the counters at zero.
+      if (atomicAdd(p.counter + 1, 1u) == gridDim.x - 1) {
+        p.counter[0] = 0;
+        p.counter[1] = 0;
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------ matrix instructions
+    // The whole warp waits; one lane, elected once, issues everything, so the
+    // products run in the order of issue and a commit covers all before it.
+    const bool leader = elect_one();
+    int slot = 0, stage = 0;
+    uint32_t u_phase = 0, phase = 0, q_phase = 0;
+    uint32_t p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+    const uint32_t q_addr = __shfl_sync(kFullMask, smem_addr(q_smem), 0);
+    const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
+    const uint32_t idesc_o = __shfl_sync(kFullMask, mma_idesc(D, true), 0);
+    for (;;) {
+      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const int seq = sh.unit[slot].seq;
+      if (seq < 0) break;
+      const Unit u = sh.unit[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+      const int tiles = max(u.tiles[0], u.tiles[1]);
+      if (tiles == 0) continue;
+      ok = ok && mbar_wait_warp(&sh.q_full, q_phase);
+      q_phase ^= 1u;
+      // S of both row tiles with the keys in stage `stage`.
+      auto scores = [&](int t, int cols) {
+        const uint32_t k_addr = ring_addr + (uint32_t)stage * S::kTileBytes;
+        const uint32_t idesc = __shfl_sync(kFullMask, mma_idesc((cols + 15) & ~15, false), 0);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = (uint32_t)(k / 4) * S::kSub + (uint32_t)(k % 4) * 32;
+            tc_mma_ss(tmem + (uint32_t)t * 128, smem_desc(q_addr + (uint32_t)t * S::kTileBytes + at, 16),
+                      smem_desc(k_addr + at, 16), idesc, k > 0 ? 1u : 0u);
+          }
+          tc_commit(&sh.s_full[t]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](int s) {
+        if (leader) tc_commit(&sh.empty[s]);
+      };
+      auto step = [&]() {
+        if (++stage == S::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      ok = ok && mbar_wait_warp(&sh.full[stage], phase);
+      tc_fence_after_sync();
+      int cols = key_tile(u, 0, a.window).cols;
+      for (int t = 0; t < 2; ++t)
+        if (u.tiles[t] > 0) scores(t, cols);
+      release(stage);
+      step();
+      for (int i = 0; i < tiles; ++i) {
+        const int v_stage = stage;
+        const uint32_t v_phase = phase;
+        step();                                   // now at the next tile's keys
+        const int next_cols = i + 1 < tiles ? key_tile(u, i + 1, a.window).cols : 0;
+        bool v_ready = false, k_ready = false;
+        const bool last1 = u.tiles[1] <= i;       // tile 1 takes no part in this key tile
+        for (int t = 0; t < 2; ++t) {
+          if (i >= u.tiles[t]) continue;
+          if (!v_ready) {
+            ok = ok && mbar_wait_warp(&sh.full[v_stage], v_phase);
+            v_ready = true;
+          }
+          if (i == 0) {                           // the last unit's O has been read
+            ok = ok && mbar_wait_warp(&sh.o_empty[t], o_phase[t] ^ 1u);
+            o_phase[t] ^= 1u;
+          }
+          ok = ok && mbar_wait_warp(&sh.p_full[t], p_phase[t]);
+          p_phase[t] ^= 1u;
+          tc_fence_after_sync();
+          const uint32_t v_addr = ring_addr + (uint32_t)v_stage * S::kTileBytes;
+          const int steps = (cols + 15) / 16;
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              if (k < steps)
+                tc_mma_ts(tmem + kOCol + (uint32_t)t * D, tmem + (uint32_t)t * 128 + k * 8,
+                          smem_desc(v_addr + (uint32_t)k * 2048, S::kSub), idesc_o,
+                          (i > 0 || k > 0) ? 1u : 0u);
+            if (t == 1 || last1) tc_commit(&sh.empty[v_stage]);
+            if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
+          }
+          __syncwarp();
+          if (i + 1 < u.tiles[t]) {
+            if (!k_ready) {
+              ok = ok && mbar_wait_warp(&sh.full[stage], phase);
+              tc_fence_after_sync();
+              k_ready = true;
+            }
+            scores(t, next_cols);
+          }
+        }
+        if (i + 1 < tiles) {
+          release(stage);
+          step();
+        }
+        cols = next_cols;
+        // All products with Q have been issued.
+        if ((i + 2 == tiles || tiles == 1) && leader) tc_commit(&sh.q_empty);
+        __syncwarp();
+      }
+    }
+    // TMEM is freed only after every product has finished.
+    tc_commit(&sh.drain);
+    mbar_wait(&sh.drain, 0);
+  } else if (warp == kCleanWarp) {
+    // ------------------------------------------------ values under the mask
+    int slot = 0, stage = 0;
+    uint32_t u_phase = 0;
+    uint32_t raw_phase = 0;                       // one bit per stage
+    for (;;) {
+      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const Unit u = sh.unit[slot];
+      if (u.seq < 0) break;
+      const int tiles = max(u.tiles[0], u.tiles[1]);
+      for (int i = 0; i < tiles; ++i) {
+        const KeyTile kt = key_tile(u, i, a.window);
+        const int v_stage = stage + 1 < S::kStages ? stage + 1 : 0;
+        if (kt.cut) {
+          ok = ok && mbar_wait_warp(&sh.raw[v_stage], (raw_phase >> v_stage) & 1u);
+          raw_phase ^= 1u << v_stage;
+          unsigned char* v = ring + (size_t)v_stage * S::kTileBytes;
+          int bad_lo = 0x7fffffff, bad_hi = -1;
+          for (int r = lane; r < ((kt.cols + 15) & ~15); r += 32) {
+            const int key = kt.j0 + r;
+            const bool seen = key < kt.end && (i < u.sink_tiles || key >= u.lo || key < u.sinks);
+#pragma unroll
+            for (int c = 0; c < 8 * S::kSubs; ++c) {
+              // Lanes start at different pieces of their rows: no bank conflicts.
+              uint4* at = reinterpret_cast<uint4*>(v + (c / 8) * S::kSub + r * 128 +
+                                                   ((c + lane) & 7) * 16);
+              if (!seen) {
+                *at = make_uint4(0, 0, 0, 0);
+              } else {
+                const uint4 x = *at;
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                if (bad) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    w[e] &= ((w[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                            ((w[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                  *at = make_uint4(w[0], w[1], w[2], w[3]);
+                  bad_lo = min(bad_lo, key);
+                  bad_hi = max(bad_hi, key);
+                }
+              }
+            }
+          }
+          bad_lo = __reduce_min_sync(kFullMask, bad_lo);
+          bad_hi = __reduce_max_sync(kFullMask, bad_hi);
+          if (lane == 0 && bad_hi >= 0) {
+            sh.bad_lo[slot] = min(sh.bad_lo[slot], bad_lo);
+            sh.bad_hi[slot] = max(sh.bad_hi[slot], bad_hi);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[v_stage]);
+        }
+        stage = stage + 2 < S::kStages ? stage + 2 : stage + 2 - S::kStages;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------ softmax and epilogue
+    const int t = warp >> 2;                      // row tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + (uint32_t)t * 128;
+    const uint32_t o_addr = tmem + lanes + kOCol + (uint32_t)t * D;
+    const int tok = t * p.n + row / a.group, head = row % a.group;
+    const bool in_tile = row < p.n * a.group;
+    const int tok_first = t * p.n + (row - lane) / a.group;                  // of the warp's rows
+    const int tok_last = t * p.n + min((row - lane + 31) / a.group, p.n - 1);
+    const float c = a.scale * kLog2e;
+    int slot = 0;
+    uint32_t u_phase = 0, s_phase = 0, o_phase = 0;
+    for (;;) {
+      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const Unit u = sh.unit[slot];
+      if (u.seq < 0) break;
+      const int tiles = u.tiles[t];
+      const int pos = u.pos0 + min(tok, u.nt - 1);
+      const int pos_first = u.pos0 + min(tok_first, u.nt - 1);
+      const int pos_last = u.pos0 + min(tok_last, u.nt - 1);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < tiles; ++i) {
+        const KeyTile kt = key_tile(u, i, a.window);
+        const bool cut = i < u.sink_tiles || kt.j0 + kKeys - 1 > pos_first ||
+                         (a.window != 0 && kt.j0 <= pos_last - a.window);
+        ok = ok && mbar_wait_warp(&sh.s_full[t], s_phase);
+        s_phase ^= 1u;
+        tc_fence_after_sync();
+        float s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s + 32 * q);
+        tmem_wait_ld();
+        if (cut) {
+          const int last = min(pos, kt.end - 1) - kt.j0;
+          const int first = a.window ? pos - a.window + 1 - kt.j0 : 0;
+          const int sinks = a.window ? u.sinks - kt.j0 : 0;
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            s[j] = j <= last && (j >= first || j < sinks) ? s[j] : -INFINITY;
+        }
+        float top = max3(m, s[0], s[1]), top1 = s[2];
+#pragma unroll
+        for (int j = 3; j + 3 < 128; j += 4) {
+          top = max3(top, s[j], s[j + 1]);
+          top1 = max3(top1, s[j + 2], s[j + 3]);
+        }
+        top = max3(top, top1, s[127]);
+        if (i == 0) {
+          m = top;
+        } else if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
+          // O's last product is done: S was issued after it.
+          const float keep = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
+          const bool fresh = m == -INFINITY;
+          l *= keep;
+          m = top;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_wait_ld();
+            uint32_t w[2][16];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j / 16][j % 16] = __float_as_uint(fresh ? 0.f : o[j] * keep);
+            tmem_st16(o_addr + 32 * q, w[0]);
+            tmem_st16(o_addr + 32 * q + 16, w[1]);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = ffma2(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]),
+                                   make_float2(c, c), make_float2(base, base));
+            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum = fadd2(sum, e);
+            w[j] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(s_addr + 16 * q, w);
+        }
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+
+      const bool write = in_tile && tok < u.nt;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                           ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D;
+      if (tiles > 0) {
+        float total = l, f = 1.f;
+        if (a.sink_logits != nullptr) {
+          const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
+          const float mc = m * c, top = fmaxf(mc, z), base = top == -INFINITY ? 0.f : top;
+          f = exp2_approx(mc - base);
+          total = l * f + exp2_approx(z - base);
+        }
+        const float inv = l == 0.f ? 0.f : f / total;
+        ok = ok && mbar_wait_warp(&sh.o_full[t], o_phase);
+        o_phase ^= 1u;
+        tc_fence_after_sync();
+        const int bad_lo = *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]);
+        const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
+        const bool again = bad_lo <= min(bad_hi, pos) &&
+                           (a.window == 0 || bad_hi > pos - a.window || bad_lo < a.sinks);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          tmem_ld32(o_addr + 32 * q, o);
+          tmem_wait_ld();
+          if (write && !again) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = l == 0.f ? 0u : pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
+              *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+        if (again && write) slow_row<D>(a, u, tok, u.kvh * a.group + head);
+      } else if (write) {
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+    }
+  }
+  if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
+  using S = Shape<D>;
+  PrefillArgs p = {};
+  p.a = a;
+  p.n = kRows / a.group;
+  p.box_rows = std::min(a.cache.page_size, kKeys);
+  while ((1 << p.box_shift) < p.box_rows) ++p.box_shift;
+  const int64_t slots = query_tile_slots(a.seqs, a.T, 2 * p.n);
+  p.slots = (int)slots;
+  p.units = slots * a.cache.kv_heads;
+  p.counter = static_cast<unsigned int*>(counters);
+  PrefillMaps maps;
+  if (!kv_tensor_map(a.cache, false, p.box_rows, 1, &maps.k) ||
+      !kv_tensor_map(a.cache, true, p.box_rows, 1, &maps.v))
+    return cudaErrorInvalidValue;
+  {
+    auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {64, (cuuint64_t)a.heads, (cuuint64_t)S::kSubs, (cuuint64_t)a.T};
+    const cuuint64_t strides[3] = {a.heads > 1 ? (cuuint64_t)a.q_head * 2 : 16, 128,
+                                   a.T > 1 ? (cuuint64_t)a.q_token * 2 : 16};
+    const cuuint32_t box[4] = {64, (cuuint32_t)a.group, 1, (cuuint32_t)p.n};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    if (enc(&maps.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a.q), dims, strides,
+            box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  constexpr size_t smem =
+      1024 + (size_t)(2 + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t err = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    err = cudaFuncSetAttribute(attention_prefill_kernel<D>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (err != cudaSuccess) return err;
+  const int grid = (int)std::min<int64_t>(attention_num_sms(), p.units);
+  return launch_after_previous(attention_prefill_kernel<D>, dim3((unsigned)grid), dim3(kThreads),
+                               smem, stream, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prefill(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  void* counters = static_cast<unsigned char*>(workspace) + decode_counter_bytes();
+  return a.cache.head_dim == 64 ? launch<64>(a, counters, stream) : launch<128>(a, counters, stream);
+}
+
+}  // namespace mxfp4el
