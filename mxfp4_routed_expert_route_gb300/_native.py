@@ -114,6 +114,8 @@ class LibraryNotBuilt(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load the CUDA library once; raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

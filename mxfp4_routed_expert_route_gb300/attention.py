@@ -24,8 +24,10 @@ __all__ = ["PagedKVCache", "PagedSequences", "append_kv", "paged_attention_decod
 _DTYPES = {torch.float32: _native.DTYPE_F32, torch.bfloat16: _native.DTYPE_BF16}
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+# The current stream's handle of a device by index: the tuple-free form of
+# torch.cuda.current_stream(device).cuda_stream, which costs 2 us a call.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 class PagedKVCache:
@@ -60,6 +62,7 @@ class PagedKVCache:
             k_pages.data_ptr(), v_pages.data_ptr(), pages, heads, page, dim,
             *k_pages.stride()[:3], *v_pages.stride()[:3], _DTYPES[k_pages.dtype])
         self._address = ctypes.addressof(self._c)
+        self._index = k_pages.device.index
 
     @classmethod
     def empty(cls, num_pages: int, num_kv_heads: int, page_size: int, head_dim: int,
@@ -107,23 +110,40 @@ class PagedSequences:
 
 
 def _check_rows(name: str, t: torch.Tensor, cache: PagedKVCache, heads: int | None = None):
+    """The shape and strides of a (tokens, heads, head_dim) tensor."""
+    shape, stride = t.shape, t.stride()
     if t.dtype != cache.dtype:
         raise TypeError(f"{name} must have the cache's dtype {cache.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be (tokens, heads, {cache.head_dim})")
-    if t.stride(2) != 1:
+    if stride[2] != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
+    return shape, stride
 
 
 def _check_out(name: str, out: torch.Tensor | None, q: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return torch.empty_like(q) if q.is_contiguous() else \
+            torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
             or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of q's shape, dtype and device")
     return out
+
+
+def _call(name: str, cache: PagedKVCache, args: tuple) -> None:
+    """One library call on the cache's device, the current stream last."""
+    f = getattr(_native.load(), name)
+    index = cache._index
+    if _current_device() == index:
+        rc = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
+    if rc:
+        _native.check(rc, name)
 
 
 def append_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVCache,
@@ -141,11 +161,11 @@ def append_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVC
     (head_dim) in the cache's dtype weigh an RMS norm of each head's row.
     See mxfp4el_append_kv in the C header.
     """
-    _check_rows("q", q, cache)
-    _check_rows("k", k, cache, cache.num_kv_heads)
-    _check_rows("v", v, cache, cache.num_kv_heads)
-    T = q.shape[0]
-    if k.shape[0] != T or v.shape[0] != T:
+    shape, qs = _check_rows("q", q, cache)
+    kshape, ks = _check_rows("k", k, cache, cache.num_kv_heads)
+    vshape, vs = _check_rows("v", v, cache, cache.num_kv_heads)
+    T = shape[0]
+    if kshape[0] != T or vshape[0] != T:
         raise ValueError("q, k and v must have the same number of tokens")
     if seqs.device != cache.device:
         raise ValueError(f"the sequences are on {seqs.device}, the cache on {cache.device}")
@@ -165,19 +185,13 @@ def append_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVC
         if rotary % 16 or not 0 < rotary <= cache.head_dim:
             raise ValueError("rotary_dim must be a multiple of 16 up to head_dim")
     q_out = _check_out("q_out", q_out, q)
-    if T == 0:
-        return q_out
-    lib = _native.load()
-    with torch.cuda.device(cache.device):
-        rc = lib.mxfp4el_append_kv(
-            q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
-            v.data_ptr(), v.stride(0), v.stride(1),
-            q_norm.data_ptr() if q_norm is not None else None,
-            k_norm.data_ptr() if k_norm is not None else None, eps,
-            cos_sin.data_ptr() if cos_sin is not None else None, positions, rotary,
-            1 if interleaved else 0, cache._address, seqs._address, q_out.data_ptr(), T,
-            q.shape[1], _stream(cache.device))
-    _native.check(rc, "append_kv")
+    if T:
+        _call("mxfp4el_append_kv", cache, (
+            q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            None if q_norm is None else q_norm.data_ptr(),
+            None if k_norm is None else k_norm.data_ptr(), eps,
+            None if cos_sin is None else cos_sin.data_ptr(), positions, rotary,
+            1 if interleaved else 0, cache._address, seqs._address, q_out.data_ptr(), T, shape[1]))
     return q_out
 
 
@@ -195,23 +209,27 @@ def attention_workspace(device=None) -> torch.Tensor:
 _workspaces: dict[tuple[int, int], torch.Tensor] = {}
 
 
-def _workspace_of(device: torch.device, stream: int) -> torch.Tensor:
-    ws = _workspaces.get((device.index, stream))
+def _workspace_of(cache: PagedKVCache) -> torch.Tensor:
+    key = (cache._index, _raw_stream(cache._index))
+    ws = _workspaces.get(key)
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("pass a workspace (attention_workspace) while a graph is captured, "
                                "or make a first call on this stream before the capture")
-        ws = _workspaces[(device.index, stream)] = attention_workspace(device)
+        with torch.cuda.device(cache.device):
+            ws = _workspaces[key] = attention_workspace(cache.device)
     return ws
 
 
-def _attention(what, q, cache, seqs, scale, window, sinks, sink_logits, out, workspace):
-    _check_rows("q", q, cache)
-    T, heads, dim = q.shape
+def _attention(name, q, cache, seqs, scale, window, sinks, sink_logits, out, workspace):
+    shape, qs = _check_rows("q", q, cache)
+    T, heads, dim = shape
     if heads == 0 or heads % cache.num_kv_heads:
         raise ValueError("the number of query heads must be a multiple of the cache's heads")
     if seqs.device != cache.device:
         raise ValueError(f"the sequences are on {seqs.device}, the cache on {cache.device}")
+    if seqs.q_offsets is None and seqs.num_seqs != T:
+        raise ValueError("without q_offsets there is one token per sequence")
     window = 0 if window is None else window
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
@@ -220,27 +238,14 @@ def _attention(what, q, cache, seqs, scale, window, sinks, sink_logits, out, wor
             or sink_logits.shape != (heads,) or not sink_logits.is_contiguous()):
         raise ValueError("sink_logits must be a (heads,) float32 tensor on the cache's device")
     out = _check_out("out", out, q)
-    if T == 0:
-        return out
-    lib = _native.load()
-    if scale is None:
-        scale = dim ** -0.5
-    with torch.cuda.device(cache.device):
-        stream = _stream(cache.device)
-        if workspace is None:
-            workspace = _workspace_of(cache.device, stream)
-        logits = sink_logits.data_ptr() if sink_logits is not None else None
-        if what == "paged_attention_decode":
-            rc = lib.mxfp4el_attention_decode(
-                q.data_ptr(), q.stride(0), q.stride(1), cache._address, seqs._address, scale,
-                window, sinks, logits, out.data_ptr(), heads, workspace.data_ptr(),
-                workspace.numel(), stream)
-        else:
-            rc = lib.mxfp4el_attention_prefill(
-                q.data_ptr(), q.stride(0), q.stride(1), cache._address, seqs._address, scale,
-                window, sinks, logits, out.data_ptr(), T, heads, workspace.data_ptr(),
-                workspace.numel(), stream)
-    _native.check(rc, what)
+    if T:
+        ws = _workspace_of(cache) if workspace is None else workspace
+        rows = (heads,) if name == "mxfp4el_attention_decode" else (T, heads)
+        _call(name, cache, (
+            q.data_ptr(), qs[0], qs[1], cache._address, seqs._address,
+            dim ** -0.5 if scale is None else scale, window, sinks,
+            None if sink_logits is None else sink_logits.data_ptr(), out.data_ptr(), *rows,
+            ws.data_ptr(), ws.numel()))
     return out
 
 
@@ -263,9 +268,7 @@ def paged_attention_decode(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSequ
     if seqs.q_offsets is not None:
         raise ValueError("decode takes one token per sequence: leave q_offsets out, or use "
                          "paged_attention_prefill")
-    if q.dim() == 3 and q.shape[0] != seqs.num_seqs:
-        raise ValueError("q must have one row per sequence")
-    return _attention("paged_attention_decode", q, cache, seqs, scale, window, sinks, sink_logits,
+    return _attention("mxfp4el_attention_decode", q, cache, seqs, scale, window, sinks, sink_logits,
                       out, workspace)
 
 
@@ -281,9 +284,7 @@ def paged_attention_prefill(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSeq
     the cache, behind any history. Arguments otherwise as
     :func:`paged_attention_decode`.
     """
-    if seqs.q_offsets is None and q.dim() == 3 and q.shape[0] != seqs.num_seqs:
-        raise ValueError("without q_offsets there is one token per sequence")
-    return _attention("paged_attention_prefill", q, cache, seqs, scale, window, sinks,
+    return _attention("mxfp4el_attention_prefill", q, cache, seqs, scale, window, sinks,
                       sink_logits, out, workspace)
 
 
@@ -294,6 +295,7 @@ def page_errors(device=None) -> int:
         "cuda", torch.cuda.current_device())
     n = ctypes.c_int64(0)
     with torch.cuda.device(dev):
-        _native.check(_native.load().mxfp4el_page_errors(_stream(dev), ctypes.byref(n)),
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        _native.check(_native.load().mxfp4el_page_errors(stream, ctypes.byref(n)),
                       "mxfp4el_page_errors")
     return int(n.value)

@@ -16,31 +16,34 @@
 // rotary_dim pair up among themselves). head_dim / 16 lanes make a row, so a
 // warp takes 32 / (head_dim / 16) rows at a time, of one token: the cosines
 // and sines of the token stay in the lanes' registers for all of its rows.
+#include <algorithm>
+
 #include "attn.cuh"
 
 namespace mxfp4el {
 namespace {
 
 constexpr int kAppendWarps = 4;
+constexpr int kFlight = 4;
+constexpr int kAppendBlocks = 4;        // per SM
+constexpr int kFillWarps = 152 * 32;
 
-template <typename Tok> struct Chunk8;   // 8 elements <-> 8 floats, 16-byte accesses
+template <typename Tok> struct Chunk8;   // 8 elements <-> 4 pairs of floats, 16-byte accesses
 
 template <> struct Chunk8<__nv_bfloat16> {
   uint4 raw;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+  __device__ __forceinline__ void unpack(float2 (&x)[4]) const {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+      x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
-  __device__ __forceinline__ void pack(const float (&x)[8]) {
+  __device__ __forceinline__ void pack(const float2 (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     raw = make_uint4(w[0], w[1], w[2], w[3]);
@@ -54,20 +57,18 @@ template <> struct Chunk8<float> {
     raw[0] = __ldg(reinterpret_cast<const uint4*>(p));
     raw[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   }
-  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+  __device__ __forceinline__ void unpack(float2 (&x)[4]) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      x[4 * i] = __uint_as_float(raw[i].x);
-      x[4 * i + 1] = __uint_as_float(raw[i].y);
-      x[4 * i + 2] = __uint_as_float(raw[i].z);
-      x[4 * i + 3] = __uint_as_float(raw[i].w);
+      x[2 * i] = make_float2(__uint_as_float(raw[i].x), __uint_as_float(raw[i].y));
+      x[2 * i + 1] = make_float2(__uint_as_float(raw[i].z), __uint_as_float(raw[i].w));
     }
   }
-  __device__ __forceinline__ void pack(const float (&x)[8]) {
+  __device__ __forceinline__ void pack(const float2 (&x)[4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      raw[i] = make_uint4(__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
-                          __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3]));
+      raw[i] = make_uint4(__float_as_uint(x[2 * i].x), __float_as_uint(x[2 * i].y),
+                          __float_as_uint(x[2 * i + 1].x), __float_as_uint(x[2 * i + 1].y));
   }
   __device__ __forceinline__ void store(float* p) const {
     reinterpret_cast<uint4*>(p)[0] = raw[0];
@@ -75,36 +76,126 @@ template <> struct Chunk8<float> {
   }
 };
 
-// The pair (x, y) of chunks turned in place. Half style: element i of x with
-// element i of y by (c[i], s[i]). Interleaved: elements 2i and 2i + 1 of x by
-// (c[i], s[i]), of y by (c[4 + i], s[4 + i]).
+// The pair (x, y) of chunks turned in place, two elements at a time. Half
+// style: element i of x with element i of y by (c[i], s[i]). Interleaved:
+// elements 2i and 2i + 1 of x by (c[i], s[i]), of y by (c[4 + i], s[4 + i]).
 template <bool kInter>
-__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&c)[8],
-                                     const float (&s)[8]) {
+__device__ __forceinline__ void turn(float2 (&x)[4], float2 (&y)[4], const float2 (&c)[4],
+                                     const float2 (&s)[4]) {
   if constexpr (kInter) {
+    auto one = [](float2& v, float ci, float si) {
+      v = ffma2(v, make_float2(ci, ci),
+                fmul2(make_float2(v.y, v.x), make_float2(-si, si)));
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1], e = y[2 * i], f = y[2 * i + 1];
-      x[2 * i] = a * c[i] - b * s[i];
-      x[2 * i + 1] = b * c[i] + a * s[i];
-      y[2 * i] = e * c[4 + i] - f * s[4 + i];
-      y[2 * i + 1] = f * c[4 + i] + e * s[4 + i];
+    for (int i = 0; i < 2; ++i) {
+      one(x[2 * i], c[i].x, s[i].x);
+      one(x[2 * i + 1], c[i].y, s[i].y);
+      one(y[2 * i], c[2 + i].x, s[2 + i].x);
+      one(y[2 * i + 1], c[2 + i].y, s[2 + i].y);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = x[i], b = y[i];
-      x[i] = a * c[i] - b * s[i];
-      y[i] = b * c[i] + a * s[i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = x[i], b = y[i];
+      x[i] = ffma2(a, c[i], fmul2(b, make_float2(-s[i].x, -s[i].y)));
+      y[i] = ffma2(b, c[i], fmul2(a, s[i]));
     }
   }
 }
 
+// What a warp knows about its token.
+struct TokenPlace {
+  int64_t page;
+  int slot;
+  bool rotate;   // its position has a row of angles (or there are none)
+  bool store;    // its key and value have a place
+};
+
+// The warp's steps of one kind of rows: kRows rows at a time, kInFlight steps'
+// loads issued together. src and dst are the token's rows. Returns the step at
+// which the warp goes on with the next kind.
+enum class Rows { kQuery, kKey, kValue };
+template <Rows kKind, typename Tok, int D, bool kInter>
+__device__ __forceinline__ int rows_of_kind(const Tok* src, int64_t src_head, Tok* dst,
+                                            int64_t dst_head, const Tok* norm, float eps, int rows,
+                                            int step, int slices, int c0, int c1, bool turns,
+                                            const float2 (&cs)[4], const float2 (&sn)[4],
+                                            const TokenPlace& place, int lane) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  constexpr int kInFlight = sizeof(Tok) == 2 ? kFlight : kFlight / 2;
+  const int steps = (rows + kRows - 1) / kRows;
+  float2 n0[4], n1[4];
+  if (kKind != Rows::kValue && norm != nullptr && step < steps) {
+    Chunk8<Tok> a, b;
+    a.load(norm + 8 * c0);
+    b.load(norm + 8 * c1);
+    a.unpack(n0);
+    b.unpack(n1);
+  }
+  src += (int64_t)min(step * kRows + lane / kLanes, rows - 1) * src_head;
+  for (; step < steps; step += slices * kInFlight) {
+    Chunk8<Tok> u[kInFlight], w[kInFlight];
+    const int h0 = step * kRows + lane / kLanes;
+    const Tok* from = src;
+#pragma unroll
+    for (int f = 0; f < kInFlight; ++f) {
+      if (h0 + f * slices * kRows < rows) {
+        u[f].load(from + 8 * c0);
+        w[f].load(from + 8 * c1);
+      }
+      from += (int64_t)slices * kRows * src_head;
+    }
+    src = from;
+#pragma unroll
+    for (int f = 0; f < kInFlight; ++f) {
+      if (f > 0 && step + f * slices >= steps) return step + f * slices - steps;
+      const int h = h0 + f * slices * kRows;
+      if constexpr (kKind != Rows::kValue) {
+        float2 x[4], y[4];
+        u[f].unpack(x);
+        w[f].unpack(y);
+        if (norm != nullptr) {
+          // The row's mean square over its lanes (all lanes of the warp take
+          // part in the shuffles).
+          float2 sq = fmul2(x[0], x[0]);
+#pragma unroll
+          for (int i = 1; i < 4; ++i) sq = ffma2(x[i], x[i], sq);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sq = ffma2(y[i], y[i], sq);
+          float sum = sq.x + sq.y;
+#pragma unroll
+          for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+          const float inv = rsqrtf(sum * (1.0f / D) + eps);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = fmul2(fmul2(x[i], make_float2(inv, inv)), n0[i]);
+            y[i] = fmul2(fmul2(y[i], make_float2(inv, inv)), n1[i]);
+          }
+        }
+        if (turns && place.rotate) turn<kInter>(x, y, cs, sn);
+        if (kKind == Rows::kQuery && !place.rotate) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = y[i] = make_float2(0.f, 0.f);
+        }
+        u[f].pack(x);
+        w[f].pack(y);
+      }
+      if (h < rows && (kKind == Rows::kQuery || place.store)) {
+        u[f].store(dst + h * dst_head + 8 * c0);
+        w[f].store(dst + h * dst_head + 8 * c1);
+      }
+    }
+  }
+  return step - steps;
+}
+
 template <typename Tok, int D, bool kInter>
-__global__ void __launch_bounds__(kAppendWarps * 32)
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks)
 append_kv_kernel(const AppendArgs a, int slices) {
   constexpr int kLanes = D / 16;          // lanes of a row
-  constexpr int kRows = 32 / kLanes;      // rows a warp holds at a time
+  pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
   const int t = (int)(unit / slices), slice = (int)(unit - (int64_t)t * slices);
@@ -120,14 +211,16 @@ append_kv_kernel(const AppendArgs a, int slices) {
   if (!past)
     pos = __ldg(a.seqs.seq_lens + seq) - first_row(a.seqs, seq + 1, a.T) + t;
   const bool pos_ok = pos >= 0 && (pos >> a.cache.page_shift) < a.seqs.max_pages;
-  const bool turn_ok = a.rotary_dim == 0 || (pos_ok && pos < a.max_positions);
-  int64_t page = -1;
-  if (pos_ok) page = page_of(a.seqs, a.cache, seq, pos >> a.cache.page_shift);
-  const bool store_ok = turn_ok && page >= 0;
-  if (!past && !store_ok && slice == 0 && lane == 0) atomicAdd(&a.status[kStatusBadPages], 1ull);
-  const int slot = pos & (a.cache.page_size - 1);
+  TokenPlace place;
+  place.rotate = !past && (a.rotary_dim == 0 || (pos_ok && pos < a.max_positions));
+  place.page = -1;
+  if (pos_ok) place.page = page_of(a.seqs, a.cache, seq, pos >> a.cache.page_shift);
+  place.store = place.rotate && place.page >= 0;
+  place.slot = pos & (a.cache.page_size - 1);
+  if (!past && !place.store && slice == 0 && lane == 0)
+    atomicAdd(&a.status[kStatusBadPages], 1ull);
 
-  // This lane's two chunks, and their cosines and sines.
+  // This lane's two chunks, and the cosines and sines of its pairs.
   const int j = lane % kLanes, rot = a.rotary_dim / 16;      // chunk pairs that turn
   const bool turns = j < rot;
   int c0, c1;
@@ -138,94 +231,48 @@ append_kv_kernel(const AppendArgs a, int slices) {
     c0 = turns ? j : 2 * rot + 2 * (j - rot);
     c1 = turns ? j + rot : c0 + 1;
   }
-  float cs[8], sn[8];
-  if (turns && turn_ok) {
-    const float* row = a.cos_sin + (int64_t)pos * a.rotary_dim + 8 * j;
+  float2 cs[4] = {}, sn[4] = {};
+  if (turns && place.rotate) {
+    const float4* row = reinterpret_cast<const float4*>(a.cos_sin + (int64_t)pos * a.rotary_dim) + 2 * j;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      cs[i] = __ldg(row + i);
-      sn[i] = __ldg(row + a.rotary_dim / 2 + i);
+    for (int i = 0; i < 2; ++i) {
+      const float4 c = __ldg(row + i), s = __ldg(row + a.rotary_dim / 8 + i);
+      cs[2 * i] = make_float2(c.x, c.y);
+      cs[2 * i + 1] = make_float2(c.z, c.w);
+      sn[2 * i] = make_float2(s.x, s.y);
+      sn[2 * i + 1] = make_float2(s.z, s.w);
     }
   }
 
-  const int rows = a.heads + 2 * a.cache.kv_heads;
-  for (int h = slice * kRows + lane / kLanes; h < (rows + kRows - 1) / kRows * kRows;
-       h += slices * kRows) {
-    const bool live = h < rows;
-    const bool is_q = h < a.heads, is_k = !is_q && h < a.heads + a.cache.kv_heads;
-    const Tok* src;
-    Tok* dst;
-    const Tok* norm = nullptr;
-    if (is_q) {
-      src = static_cast<const Tok*>(a.q) + t * a.q_token + h * a.q_head;
-      dst = static_cast<Tok*>(a.q_out) + ((int64_t)t * a.heads + h) * D;
-      norm = static_cast<const Tok*>(a.q_norm);
-    } else if (is_k) {
-      const int kh = h - a.heads;
-      src = static_cast<const Tok*>(a.k) + t * a.k_token + kh * a.k_head;
-      dst = static_cast<Tok*>(a.cache.k) + page * a.cache.k_page + kh * a.cache.k_head +
-            slot * a.cache.k_slot;
-      norm = static_cast<const Tok*>(a.k_norm);
-    } else {
-      const int vh = min(h, rows - 1) - a.heads - a.cache.kv_heads;
-      src = static_cast<const Tok*>(a.v) + t * a.v_token + vh * a.v_head;
-      dst = static_cast<Tok*>(a.cache.v) + page * a.cache.v_page + vh * a.cache.v_head +
-            slot * a.cache.v_slot;
-    }
-    Chunk8<Tok> u, w;
-    u.load(src + 8 * c0);
-    w.load(src + 8 * c1);
-    float x[8], y[8];
-    u.unpack(x);
-    w.unpack(y);
-    // The row's mean square over its lanes. Every lane of the warp takes part
-    // in the shuffles; rows without a norm drop the result.
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += x[i] * x[i] + y[i] * y[i];
-#pragma unroll
-    for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
-    if (is_q || is_k) {
-      if (norm != nullptr) {
-        const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-        Chunk8<Tok> n0, n1;
-        n0.load(norm + 8 * c0);
-        n1.load(norm + 8 * c1);
-        float f[8], g[8];
-        n0.unpack(f);
-        n1.unpack(g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = x[i] * inv * f[i];
-          y[i] = y[i] * inv * g[i];
-        }
-      }
-      if (turns && turn_ok) turn<kInter>(x, y, cs, sn);
-      if (is_q && (past || !turn_ok)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
-      }
-      u.pack(x);
-      w.pack(y);
-    }
-    if (live && (is_q || store_ok)) {
-      u.store(dst + 8 * c0);
-      w.store(dst + 8 * c1);
-    }
-  }
+  // The token's steps are its query rows', then its keys', then its values'.
+  const KvCacheView& kv = a.cache;
+  int step = rows_of_kind<Rows::kQuery, Tok, D, kInter>(
+      static_cast<const Tok*>(a.q) + t * a.q_token, a.q_head,
+      static_cast<Tok*>(a.q_out) + (int64_t)t * a.heads * D, D, static_cast<const Tok*>(a.q_norm),
+      a.eps, a.heads, slice, slices, c0, c1, turns, cs, sn, place, lane);
+  step = rows_of_kind<Rows::kKey, Tok, D, kInter>(
+      static_cast<const Tok*>(a.k) + t * a.k_token, a.k_head,
+      static_cast<Tok*>(kv.k) + place.page * kv.k_page + place.slot * kv.k_slot, kv.k_head,
+      static_cast<const Tok*>(a.k_norm), a.eps, kv.kv_heads, step, slices, c0, c1, turns, cs, sn,
+      place, lane);
+  rows_of_kind<Rows::kValue, Tok, D, kInter>(
+      static_cast<const Tok*>(a.v) + t * a.v_token, a.v_head,
+      static_cast<Tok*>(kv.v) + place.page * kv.v_page + place.slot * kv.v_slot, kv.v_head,
+      nullptr, 0.f, kv.kv_heads, step, slices, c0, c1, turns, cs, sn, place, lane);
 }
 
 template <typename Tok, int D, bool kInter>
 cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
   constexpr int kRows = 32 / (D / 16);
-  const int rows = a.heads + 2 * a.cache.kv_heads;
-  const int slices = (rows + kRows - 1) / kRows;
+  const int steps = (a.heads + kRows - 1) / kRows + 2 * ((a.cache.kv_heads + kRows - 1) / kRows);
+  // Few tokens: a warp for every step, for the shortest path. Many: as few
+  // warps per token as still fill the GPU (kFillWarps), since each of them
+  // looks its token up anew, a chain of four or five loads.
+  const int slices = (int)std::min<int64_t>(steps, (kFillWarps + a.T - 1) / a.T);
   const int64_t warps = (int64_t)a.T * slices;
   const int64_t blocks = (warps + kAppendWarps - 1) / kAppendWarps;
-  append_kv_kernel<Tok, D, kInter><<<(unsigned)blocks, kAppendWarps * 32, 0, stream>>>(a, slices);
-  const cudaError_t err = cudaGetLastError();
-  if (err == cudaSuccess) note_launch();
-  return err;
+  return launch_after_previous(append_kv_kernel<Tok, D, kInter>, dim3((unsigned)blocks),
+                               dim3(kAppendWarps * 32), 0, stream, a, slices);
 }
 
 template <typename Tok, int D>
