@@ -31,8 +31,8 @@
 //             page holds need not be 0), and so are infinities and NaN.
 // A value that is not finite must reach the rows that see it and no other,
 // which a matrix product cannot do in a tile that the mask cuts: there it
-// counts as zero, and the epilogue computes the rows that may see it again,
-// one by one on the CUDA cores.
+// counts as zero, and warp 10 computes the rows that may see it by itself, on
+// the CUDA cores; the epilogue leaves them out.
 //
 // P and the sum l: P is rounded to bf16 for the second product (a relative
 // error of 2^-8 at most, as the result's own rounding); l adds the float32
@@ -160,37 +160,71 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One row on the CUDA cores (see the top): its keys one after another.
+// Whether the row at position pos may see a key of [bad_lo, bad_hi].
+__device__ __forceinline__ bool may_see(const AttnArgs& a, int pos, int bad_lo, int bad_hi) {
+  return bad_lo <= min(bad_hi, pos) &&
+         (a.window == 0 || bad_hi > pos - a.window || bad_lo < a.sinks);
+}
+
+// One row on the CUDA cores (see the top) by one warp: lane i holds elements
+// i, i + 32, ... of the row; four keys at a time.
 template <int D>
-__device__ __noinline__ void slow_row(const AttnArgs& a, const Unit& u, int token, int head) {
-  const __nv_bfloat16* q =
-      static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + token) * a.q_token + head * a.q_head;
+__device__ __forceinline__ void slow_row(const AttnArgs& a, const Unit& u, int token, int head,
+                                         int lane) {
+  constexpr int kE = D / 32;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
+                           (int64_t)(u.row0 + token) * a.q_token + head * a.q_head + lane;
   const int pos = u.pos0 + token;
-  const float c = a.scale * kLog2e;
+  float x[kE], o[kE] = {};
+#pragma unroll
+  for (int e = 0; e < kE; ++e) x[e] = __bfloat162float(q[32 * e]) * (a.scale * kLog2e);
   float m = -INFINITY, l = 0.f;
-  float o[D];
-  for (int d = 0; d < D; ++d) o[d] = 0.f;
-  for (int j = 0; j <= pos; ++j) {
-    if (!key_visible(j, pos, a.window, a.sinks)) {
-      j = max(j, pos - a.window);      // the next key is the window's first
+#pragma unroll 1
+  for (int j0 = 0; j0 <= pos; j0 += 4) {
+    if (a.window != 0 && j0 >= a.sinks && j0 + 3 <= pos - a.window) {
+      j0 = ((pos - a.window + 1) & ~3) - 4;        // on to the window's first keys
       continue;
     }
-    const int64_t page = page_of(a.seqs, a.cache, u.seq, j >> a.cache.page_shift);
-    const int slot = j & (a.cache.page_size - 1);
-    const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.cache.k) + page * a.cache.k_page +
-                             u.kvh * a.cache.k_head + slot * a.cache.k_slot;
-    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.cache.v) + page * a.cache.v_page +
-                             u.kvh * a.cache.v_head + slot * a.cache.v_slot;
-    float s = 0.f;
-    if (page >= 0)
-      for (int d = 0; d < D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
-    s *= c;
-    const float top = fmaxf(m, s), base = top == -INFINITY ? 0.f : top;
-    const float keep = exp2_approx(m - base), p = exp2_approx(s - base);
+    float s[4];
+    int64_t at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = j0 + i;
+      at[i] = -1;
+      s[i] = -INFINITY;
+      if (j <= pos && key_visible(j, pos, a.window, a.sinks)) {
+        const int64_t page = page_of(a.seqs, a.cache, u.seq, j >> a.cache.page_shift);
+        const int slot = j & (a.cache.page_size - 1);
+        s[i] = 0.f;
+        if (page >= 0) {
+          const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.cache.k) +
+                                   page * a.cache.k_page + u.kvh * a.cache.k_head +
+                                   slot * a.cache.k_slot + lane;
+          at[i] = page * a.cache.v_page + u.kvh * a.cache.v_head + slot * a.cache.v_slot + lane;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) s[i] = fmaf(x[e], __bfloat162float(k[32 * e]), s[i]);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) s[i] += __shfl_xor_sync(kFullMask, s[i], off);
+      }
+    }
+    const float top = fmaxf(m, fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2_approx(m - base);
     m = top;
-    l = l * keep + p;
-    for (int d = 0; d < D; ++d)
-      o[d] = o[d] * keep + (page >= 0 ? p * __bfloat162float(v[d]) : 0.f);
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] *= keep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float p = exp2_approx(s[i] - base);
+      if (j0 + i <= pos && key_visible(j0 + i, pos, a.window, a.sinks)) l += p;
+      if (at[i] >= 0) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e)
+          o[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.v)[at[i] + 32 * e]),
+                      o[e]);
+      }
+    }
   }
   float f = 1.f;
   if (a.sink_logits != nullptr) {
@@ -199,10 +233,11 @@ __device__ __noinline__ void slow_row(const AttnArgs& a, const Unit& u, int toke
     f = exp2_approx(m - base);
     l = l * f + exp2_approx(z - base);
   }
-  const float inv = f / l;
+  const float inv = l == 0.f ? 0.f : f / l;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                       ((int64_t)(u.row0 + token) * a.heads + head) * D;
-  for (int d = 0; d < D; ++d) out[d] = __float2bfloat16_rn(l == 0.f ? 0.f : o[d] * inv);
+                       ((int64_t)(u.row0 + token) * a.heads + head) * D + lane;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) out[32 * e] = __float2bfloat16_rn(o[e] * inv);
 }
 
 template <int D>
@@ -250,6 +285,152 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   pdl_wait();
   bool ok = true;
 
+  // The softmax warps hold a row of 128 scores each: they take registers that
+  // the other warps give up (256 x 216 + 128 x 72 = 384 x 168).
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------ softmax and epilogue
+    const int t = warp >> 2;                      // row tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + (uint32_t)t * 128;
+    const uint32_t o_addr = tmem + lanes + kOCol + (uint32_t)t * D;
+    const int tok = t * p.n + row / a.group, head = row % a.group;
+    const bool in_tile = row < p.n * a.group;
+    const int tok_first = t * p.n + (row - lane) / a.group;                  // of the warp's rows
+    const int tok_last = t * p.n + min((row - lane + 31) / a.group, p.n - 1);
+    const float c = a.scale * kLog2e;
+    int slot = 0;
+    uint32_t u_phase = 0, s_phase = 0, o_phase = 0;
+    for (;;) {
+      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const Unit u = sh.unit[slot];
+      if (u.seq < 0) break;
+      const int tiles = u.tiles[t];
+      const int pos = u.pos0 + min(tok, u.nt - 1);
+      const int pos_first = u.pos0 + min(tok_first, u.nt - 1);
+      const int pos_last = u.pos0 + min(tok_last, u.nt - 1);
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < tiles; ++i) {
+        const KeyTile kt = key_tile(u, i, a.window);
+        const bool cut = i < u.sink_tiles || kt.j0 + kKeys - 1 > pos_first ||
+                         (a.window != 0 && kt.j0 <= pos_last - a.window);
+        ok = ok && mbar_wait_warp(&sh.s_full[t], s_phase);
+        s_phase ^= 1u;
+        tc_fence_after_sync();
+        float s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s + 32 * q);
+        tmem_wait_ld();
+        if (cut) {
+          const int last = min(pos, kt.end - 1) - kt.j0;
+          const int first = a.window ? pos - a.window + 1 - kt.j0 : 0;
+          const int sinks = a.window ? u.sinks - kt.j0 : 0;
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            s[j] = j <= last && (j >= first || j < sinks) ? s[j] : -INFINITY;
+        }
+        float tops[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < 124; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[j + 2 * e], s[j + 2 * e + 1]);
+        tops[0] = max3(tops[0], s[124], s[125]);
+        tops[1] = max3(tops[1], s[126], s[127]);
+        const float top = fmaxf(m, max3(tops[0], tops[1], fmaxf(tops[2], tops[3])));
+        if (i == 0) {
+          m = top;
+        } else if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
+          // O's last product is done: S was issued after it.
+          const float keep = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
+          const bool fresh = m == -INFINITY;
+          l *= keep;
+          m = top;
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            float o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_wait_ld();
+            uint32_t w[2][16];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j / 16][j % 16] = __float_as_uint(fresh ? 0.f : o[j] * keep);
+            tmem_st16(o_addr + 32 * q, w[0]);
+            tmem_st16(o_addr + 32 * q + 16, w[1]);
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : -m * c;
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = ffma2(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]),
+                                   make_float2(c, c), make_float2(base, base));
+            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            sum = fadd2(sum, e);
+            w[j] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(s_addr + 16 * q, w);
+        }
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_full[t]);
+      }
+
+      const bool write = in_tile && tok < u.nt;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                           ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D;
+      if (tiles > 0) {
+        float total = l, f = 1.f;
+        if (a.sink_logits != nullptr) {
+          const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
+          const float mc = m * c, top = fmaxf(mc, z), base = top == -INFINITY ? 0.f : top;
+          f = exp2_approx(mc - base);
+          total = l * f + exp2_approx(z - base);
+        }
+        const float inv = l == 0.f ? 0.f : f / total;
+        ok = ok && mbar_wait_warp(&sh.o_full[t], o_phase);
+        o_phase ^= 1u;
+        tc_fence_after_sync();
+        const int bad_lo = *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]);
+        const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
+        const bool again = may_see(a, pos, bad_lo, bad_hi);
+#pragma unroll
+        for (int q = 0; q < D / 32; ++q) {
+          float o[32];
+          tmem_ld32(o_addr + 32 * q, o);
+          tmem_wait_ld();
+          if (write && !again) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = l == 0.f ? 0u : pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
+              *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+      } else if (write) {
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(0, 0, 0, 0);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == kLoadWarp) {
     // ------------------------------------------------ units and copies
     const uint64_t keep = l2_evict_normal_policy();
@@ -480,6 +661,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       const Unit u = sh.unit[slot];
       if (u.seq < 0) break;
       const int tiles = max(u.tiles[0], u.tiles[1]);
+      int unit_lo = 0x7fffffff, unit_hi = -1;
       for (int i = 0; i < tiles; ++i) {
         const KeyTile kt = key_tile(u, i, a.window);
         const int v_stage = stage + 1 < S::kStages ? stage + 1 : 0;
@@ -519,9 +701,11 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           }
           bad_lo = __reduce_min_sync(kFullMask, bad_lo);
           bad_hi = __reduce_max_sync(kFullMask, bad_hi);
+          unit_lo = min(unit_lo, bad_lo);
+          unit_hi = max(unit_hi, bad_hi);
           if (lane == 0 && bad_hi >= 0) {
-            sh.bad_lo[slot] = min(sh.bad_lo[slot], bad_lo);
-            sh.bad_hi[slot] = max(sh.bad_hi[slot], bad_hi);
+            sh.bad_lo[slot] = unit_lo;
+            sh.bad_hi[slot] = unit_hi;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -529,147 +713,11 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         }
         stage = stage + 2 < S::kStages ? stage + 2 : stage + 2 - S::kStages;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
-      if (++slot == kUnitRing) {
-        slot = 0;
-        u_phase ^= 1u;
-      }
-    }
-  } else if (warp < 8) {
-    // ------------------------------------------------ softmax and epilogue
-    const int t = warp >> 2;                      // row tile
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + (uint32_t)t * 128;
-    const uint32_t o_addr = tmem + lanes + kOCol + (uint32_t)t * D;
-    const int tok = t * p.n + row / a.group, head = row % a.group;
-    const bool in_tile = row < p.n * a.group;
-    const int tok_first = t * p.n + (row - lane) / a.group;                  // of the warp's rows
-    const int tok_last = t * p.n + min((row - lane + 31) / a.group, p.n - 1);
-    const float c = a.scale * kLog2e;
-    int slot = 0;
-    uint32_t u_phase = 0, s_phase = 0, o_phase = 0;
-    for (;;) {
-      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
-      if (!ok) break;
-      const Unit u = sh.unit[slot];
-      if (u.seq < 0) break;
-      const int tiles = u.tiles[t];
-      const int pos = u.pos0 + min(tok, u.nt - 1);
-      const int pos_first = u.pos0 + min(tok_first, u.nt - 1);
-      const int pos_last = u.pos0 + min(tok_last, u.nt - 1);
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; i < tiles; ++i) {
-        const KeyTile kt = key_tile(u, i, a.window);
-        const bool cut = i < u.sink_tiles || kt.j0 + kKeys - 1 > pos_first ||
-                         (a.window != 0 && kt.j0 <= pos_last - a.window);
-        ok = ok && mbar_wait_warp(&sh.s_full[t], s_phase);
-        s_phase ^= 1u;
-        tc_fence_after_sync();
-        float s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s + 32 * q);
-        tmem_wait_ld();
-        if (cut) {
-          const int last = min(pos, kt.end - 1) - kt.j0;
-          const int first = a.window ? pos - a.window + 1 - kt.j0 : 0;
-          const int sinks = a.window ? u.sinks - kt.j0 : 0;
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            s[j] = j <= last && (j >= first || j < sinks) ? s[j] : -INFINITY;
-        }
-        float top = max3(m, s[0], s[1]), top1 = s[2];
-#pragma unroll
-        for (int j = 3; j + 3 < 128; j += 4) {
-          top = max3(top, s[j], s[j + 1]);
-          top1 = max3(top1, s[j + 2], s[j + 3]);
-        }
-        top = max3(top, top1, s[127]);
-        if (i == 0) {
-          m = top;
-        } else if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
-          // O's last product is done: S was issued after it.
-          const float keep = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
-          const bool fresh = m == -INFINITY;
-          l *= keep;
-          m = top;
-#pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
-            float o[32];
-            tmem_ld32(o_addr + 32 * q, o);
-            tmem_wait_ld();
-            uint32_t w[2][16];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j / 16][j % 16] = __float_as_uint(fresh ? 0.f : o[j] * keep);
-            tmem_st16(o_addr + 32 * q, w[0]);
-            tmem_st16(o_addr + 32 * q + 16, w[1]);
-          }
-        }
-        const float base = m == -INFINITY ? 0.f : -m * c;
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float2 x = ffma2(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]),
-                                   make_float2(c, c), make_float2(base, base));
-            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            sum = fadd2(sum, e);
-            w[j] = pack_bf16(e.x, e.y);
-          }
-          tmem_st16(s_addr + 16 * q, w);
-        }
-        l += sum.x + sum.y;
-        tmem_wait_st();
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[t]);
-      }
-
-      const bool write = in_tile && tok < u.nt;
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                           ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D;
-      if (tiles > 0) {
-        float total = l, f = 1.f;
-        if (a.sink_logits != nullptr) {
-          const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
-          const float mc = m * c, top = fmaxf(mc, z), base = top == -INFINITY ? 0.f : top;
-          f = exp2_approx(mc - base);
-          total = l * f + exp2_approx(z - base);
-        }
-        const float inv = l == 0.f ? 0.f : f / total;
-        ok = ok && mbar_wait_warp(&sh.o_full[t], o_phase);
-        o_phase ^= 1u;
-        tc_fence_after_sync();
-        const int bad_lo = *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]);
-        const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
-        const bool again = bad_lo <= min(bad_hi, pos) &&
-                           (a.window == 0 || bad_hi > pos - a.window || bad_lo < a.sinks);
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          tmem_ld32(o_addr + 32 * q, o);
-          tmem_wait_ld();
-          if (write && !again) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = l == 0.f ? 0u : pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-        }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.o_empty[t]);
-        if (again && write) slow_row<D>(a, u, tok, u.kvh * a.group + head);
-      } else if (write) {
-        for (int j = 0; j < D / 8; ++j)
-          *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(0, 0, 0, 0);
+      if (unit_hi >= 0) {
+#pragma unroll 1
+        for (int r = 0; r < u.nt * a.group; ++r)
+          if (may_see(a, u.pos0 + r / a.group, unit_lo, unit_hi))
+            slow_row<D>(a, u, r / a.group, u.kvh * a.group + r % a.group, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
@@ -678,6 +726,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         u_phase ^= 1u;
       }
     }
+  }
   }
   if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   tc_fence_before_sync();
