@@ -51,12 +51,13 @@
 namespace mxfp4el {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kSoftmaxWarps = 16;
 constexpr int kRows = 128;              // query rows per tile
 constexpr int kKeys = 128;              // keys per tile
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kCleanWarp = 10;
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kCleanWarp = 18;
 constexpr int kUnitRing = 2;
-constexpr int kUnitReaders = 2 + 8;     // MMA, cleaner, 8 softmax warps
+constexpr int kUnitReaders = 2 + kSoftmaxWarps;     // MMA, cleaner, softmax
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
 constexpr float kRescale = 8.f;
@@ -66,7 +67,7 @@ struct Shape {
   static constexpr int kSubs = D / 64;                       // 128-byte columns of a row
   static constexpr uint32_t kSub = 128 * 128;                // bytes: 128 rows of one column
   static constexpr uint32_t kTileBytes = kSubs * kSub;
-  static constexpr int kStages = D == 128 ? 5 : 8;           // key and value tiles in flight
+  static constexpr int kStages = D == 128 ? 4 : 8;           // key and value tiles in flight
 };
 
 struct PrefillMaps {
@@ -104,6 +105,7 @@ struct __align__(16) PrefillShared {
   uint32_t tmem_base;
   int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
   Unit unit[kUnitRing];
+  float row_max[2][2][kRows], row_sum[2][2][kRows];   // [tile][half of the keys]
 };
 
 // Key tile i of a unit: its first key, the keys below which a row may see it
@@ -150,6 +152,9 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -263,9 +268,9 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
     mbar_init(&sh.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
-      mbar_init(&sh.p_full[t], 4);
+      mbar_init(&sh.p_full[t], kSoftmaxWarps / 2);
       mbar_init(&sh.o_full[t], 1);
-      mbar_init(&sh.o_empty[t], 4);
+      mbar_init(&sh.o_empty[t], kSoftmaxWarps / 2);
     }
     for (int r = 0; r < kUnitRing; ++r) {
       mbar_init(&sh.u_full[r], 1);
@@ -285,16 +290,16 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   pdl_wait();
   bool ok = true;
 
-  // The softmax warps hold a row of 128 scores each: they take registers that
-  // the other warps give up (256 x 216 + 128 x 72 = 384 x 168).
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  // The softmax threads hold 64 scores each: they take registers that the
+  // other warps give up (512 x 104 + 128 x 64 = 640 x 96).
+  if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ------------------------------------------------ softmax and epilogue
-    const int t = warp >> 2;                      // row tile
+    const int t = warp >> 3, half = (warp >> 2) & 1;         // row tile, half of the keys
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + (uint32_t)t * 128;
-    const uint32_t o_addr = tmem + lanes + kOCol + (uint32_t)t * D;
+    const uint32_t o_addr = tmem + lanes + kOCol + (uint32_t)(t * D + half * (D / 2));
     const int tok = t * p.n + row / a.group, head = row % a.group;
     const bool in_tile = row < p.n * a.group;
     const int tok_first = t * p.n + (row - lane) / a.group;                  // of the warp's rows
@@ -319,26 +324,34 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         ok = ok && mbar_wait_warp(&sh.s_full[t], s_phase);
         s_phase ^= 1u;
         tc_fence_after_sync();
-        float s[128];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, s + 32 * q);
+        float s[64];
+        tmem_ld32(s_addr + 64 * half, s);
+        tmem_ld32(s_addr + 64 * half + 32, s + 32);
         tmem_wait_ld();
         if (cut) {
-          const int last = min(pos, kt.end - 1) - kt.j0;
-          const int first = a.window ? pos - a.window + 1 - kt.j0 : 0;
-          const int sinks = a.window ? u.sinks - kt.j0 : 0;
+          const int j0 = kt.j0 + 64 * half;
+          const int last = min(pos, kt.end - 1) - j0;
+          const int first = a.window ? pos - a.window + 1 - j0 : 0;
+          const int sinks = a.window ? u.sinks - j0 : 0;
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
+          for (int j = 0; j < 64; ++j)
             s[j] = j <= last && (j >= first || j < sinks) ? s[j] : -INFINITY;
         }
         float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < 124; j += 8)
+        for (int j = 4; j < 60; j += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[j + 2 * e], s[j + 2 * e + 1]);
-        tops[0] = max3(tops[0], s[124], s[125]);
-        tops[1] = max3(tops[1], s[126], s[127]);
-        const float top = fmaxf(m, max3(tops[0], tops[1], fmaxf(tops[2], tops[3])));
+        tops[0] = max3(tops[0], s[60], s[61]);
+        tops[1] = max3(tops[1], s[62], s[63]);
+        const float mine = max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
+        // The other half's maximum. Past the barrier both halves hold their
+        // scores in registers, so P may overwrite them.
+        sh.row_max[t][half][row] = mine;
+        tc_fence_before_sync();
+        bar_sync(1 + t, 256);
+        tc_fence_after_sync();
+        const float top = max3(m, mine, sh.row_max[t][half ^ 1][row]);
         if (i == 0) {
           m = top;
         } else if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
@@ -348,7 +361,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           l *= keep;
           m = top;
 #pragma unroll
-          for (int q = 0; q < D / 32; ++q) {
+          for (int q = 0; q < D / 64; ++q) {
             float o[32];
             tmem_ld32(o_addr + 32 * q, o);
             tmem_wait_ld();
@@ -362,7 +375,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         const float base = m == -INFINITY ? 0.f : -m * c;
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -372,7 +385,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
             sum = fadd2(sum, e);
             w[j] = pack_bf16(e.x, e.y);
           }
-          tmem_st16(s_addr + 16 * q, w);
+          tmem_st16(s_addr + 32 * half + 16 * q, w);
         }
         l += sum.x + sum.y;
         tmem_wait_st();
@@ -383,8 +396,12 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
 
       const bool write = in_tile && tok < u.nt;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                           ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D;
+                           ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D +
+                           half * (D / 2);
       if (tiles > 0) {
+        sh.row_sum[t][half][row] = l;
+        bar_sync(1 + t, 256);
+        l += sh.row_sum[t][half ^ 1][row];
         float total = l, f = 1.f;
         if (a.sink_logits != nullptr) {
           const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
@@ -400,7 +417,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
         const bool again = may_see(a, pos, bad_lo, bad_hi);
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = 0; q < D / 64; ++q) {
           float o[32];
           tmem_ld32(o_addr + 32 * q, o);
           tmem_wait_ld();
@@ -419,7 +436,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.o_empty[t]);
       } else if (write) {
-        for (int j = 0; j < D / 8; ++j)
+        for (int j = 0; j < D / 16; ++j)
           *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(0, 0, 0, 0);
       }
       __syncwarp();
@@ -430,7 +447,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == kLoadWarp) {
     // ------------------------------------------------ units and copies
     const uint64_t keep = l2_evict_normal_policy();
