@@ -55,9 +55,10 @@ constexpr int kThreads = 640;
 constexpr int kSoftmaxWarps = 16;
 constexpr int kRows = 128;              // query rows per tile
 constexpr int kKeys = 128;              // keys per tile
-constexpr int kLoadWarp = 16, kMmaWarp = 17, kCleanWarp = 18;
-constexpr int kUnitRing = 2;
-constexpr int kUnitReaders = 2 + kSoftmaxWarps;     // MMA, cleaner, softmax
+constexpr int kLoadWarp = 16, kMmaWarp = 17, kCleanWarp = 18, kUnitWarp = 19;
+constexpr int kUnitRing = 4;
+constexpr int kUnitReaders = 3 + kSoftmaxWarps;     // copies, MMA, values, softmax
+constexpr int kFewSeqs = 30;            // sequences that the unit warp keeps in its lanes
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
 constexpr float kRescale = 8.f;
@@ -68,6 +69,7 @@ struct Shape {
   static constexpr uint32_t kSub = 128 * 128;                // bytes: 128 rows of one column
   static constexpr uint32_t kTileBytes = kSubs * kSub;
   static constexpr int kStages = D == 128 ? 4 : 8;           // key and value tiles in flight
+  static constexpr int kQSlots = D == 128 ? 1 : 2;           // units' queries, as far as they fit
 };
 
 struct PrefillMaps {
@@ -98,13 +100,14 @@ struct Unit {
 template <int D>
 struct __align__(16) PrefillShared {
   uint64_t full[Shape<D>::kStages], empty[Shape<D>::kStages], raw[Shape<D>::kStages];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[Shape<D>::kQSlots], q_empty[Shape<D>::kQSlots];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
   uint32_t tmem_base;
   int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
   Unit unit[kUnitRing];
+  int first_ids[kUnitRing][16];              // pages of the unit's first key tile
   float row_max[2][2][kRows], row_sum[2][2][kRows];   // [tile][half of the keys]
 };
 
@@ -140,7 +143,7 @@ __device__ __forceinline__ bool elect_one() {
 
 // Instruction descriptor of tcgen05.mma kind::f16, bf16 operands, float32
 // accumulator; b_rows_k: B's rows run along K (its columns are contiguous).
-__device__ __forceinline__ uint32_t mma_idesc(int n, bool b_rows_k) {
+__device__ __forceinline__ constexpr uint32_t mma_idesc(int n, bool b_rows_k) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows_k ? 1u << 16 : 0u) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
@@ -152,8 +155,27 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// The lowest n bits (n may be negative, or past 32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// bar_sync that tells every thread whether any brought `p`.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
+  uint32_t any;
+  asm volatile(
+      "{\n"
+      " .reg .pred p, q;\n"
+      " setp.ne.u32 p, %3, 0;\n"
+      " bar.red.or.pred q, %1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n"
+      "}"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(p ? 1u : 0u)
+      : "memory");
+  return any != 0;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -163,6 +185,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Whether lane's box of a key tile, whose first key is `key`, holds a key that
+// a row sees.
+__device__ __forceinline__ bool box_wanted(const Unit& u, const KeyTile& kt, int i, int key,
+                                           int lane, const PrefillArgs& p) {
+  return lane < (kKeys >> p.box_shift) && key < kt.end &&
+         (i < u.sink_tiles || key + p.box_rows > u.lo || key < u.sinks);
+}
+// The key's page; an id out of range is counted (and copied as zeros).
+__device__ __forceinline__ int page_id(const PrefillArgs& p, const Unit& u, int key) {
+  const AttnArgs& a = p.a;
+  const int id = __ldg(a.seqs.page_table + (int64_t)u.seq * a.seqs.table_stride +
+                       (key >> a.cache.page_shift));
+  if ((unsigned)id >= (uint64_t)a.cache.num_pages) atomicAdd(&a.status[kStatusBadPages], 1ull);
+  return id;
 }
 
 // Whether the row at position pos may see a key of [bad_lo, bad_hi].
@@ -251,7 +289,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   using S = Shape<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* q_smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  unsigned char* ring = q_smem + 2 * S::kTileBytes;
+  unsigned char* ring = q_smem + S::kQSlots * 2 * S::kTileBytes;
   PrefillShared<D>& sh =
       *reinterpret_cast<PrefillShared<D>*>(ring + (size_t)S::kStages * S::kTileBytes);
   const AttnArgs& a = p.a;
@@ -264,8 +302,10 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       mbar_init(&sh.empty[s], 1);
       mbar_init(&sh.raw[s], 1);
     }
-    mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
+    for (int s = 0; s < S::kQSlots; ++s) {
+      mbar_init(&sh.q_full[s], 1);
+      mbar_init(&sh.q_empty[s], 1);
+    }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh.s_full[t], 1);
       mbar_init(&sh.p_full[t], kSoftmaxWarps / 2);
@@ -276,7 +316,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       mbar_init(&sh.u_full[r], 1);
       mbar_init(&sh.u_empty[r], kUnitReaders);
     }
-    mbar_init(&sh.drain, 32);
+    mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -316,26 +356,42 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       const int pos = u.pos0 + min(tok, u.nt - 1);
       const int pos_first = u.pos0 + min(tok_first, u.nt - 1);
       const int pos_last = u.pos0 + min(tok_last, u.nt - 1);
-      float m = -INFINITY, l = 0.f;
+      // Key tiles [whole0, whole1) are seen whole by every row of the warp.
+      const int whole0 = u.sink_tiles +
+                         (a.window ? (max(0, pos_last - a.window + 1 - u.start) + kKeys - 1) / kKeys : 0);
+      const int whole1 = u.sink_tiles + max(0, pos_first + 1 - u.start) / kKeys;
+      float m = -INFINITY, l = 0.f, mc = 0.f;     // mc: -m c, or 0 while m is -infinity
+
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i) {
-        const KeyTile kt = key_tile(u, i, a.window);
-        const bool cut = i < u.sink_tiles || kt.j0 + kKeys - 1 > pos_first ||
-                         (a.window != 0 && kt.j0 <= pos_last - a.window);
-        ok = ok && mbar_wait_warp(&sh.s_full[t], s_phase);
+        if (ok) ok = mbar_wait_warp(&sh.s_full[t], s_phase);
         s_phase ^= 1u;
         tc_fence_after_sync();
         float s[64];
         tmem_ld32(s_addr + 64 * half, s);
         tmem_ld32(s_addr + 64 * half + 32, s + 32);
         tmem_wait_ld();
-        if (cut) {
-          const int j0 = kt.j0 + 64 * half;
-          const int last = min(pos, kt.end - 1) - j0;
-          const int first = a.window ? pos - a.window + 1 - j0 : 0;
-          const int sinks = a.window ? u.sinks - j0 : 0;
+        // Of this warp's two blocks of 32 keys: `live` has a key that one of
+        // its rows sees, `used` takes part in the second product (P of keys
+        // that no row of the warp sees is zero).
+        bool live0 = true, live1 = true, used0 = true, used1 = true;
+        if (i < whole0 || i >= whole1) {
+          const KeyTile kt = key_tile(u, i, a.window);
+          // Bit j of `seen`: the row sees key j0 + j.
+          auto mask = [&](float* x, int q) {
+            const int j0 = kt.j0 + 64 * half + 32 * q;
+            uint32_t seen = low_bits(min(pos, kt.end - 1) - j0 + 1);
+            if (a.window != 0)
+              seen &= ~low_bits(pos - a.window + 1 - j0) | low_bits(u.sinks - j0);
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            s[j] = j <= last && (j >= first || j < sinks) ? s[j] : -INFINITY;
+            for (int j = 0; j < 32; ++j)
+              if (!((seen >> j) & 1u)) x[j] = -INFINITY;
+            return __any_sync(kFullMask, seen != 0) != 0;
+          };
+          live0 = mask(s, 0);
+          live1 = mask(s + 32, 1);
+          used0 = 64 * half < kt.cols;
+          used1 = 64 * half + 32 < kt.cols;
         }
         float tops[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -352,42 +408,50 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         bar_sync(1 + t, 256);
         tc_fence_after_sync();
         const float top = max3(m, mine, sh.row_max[t][half ^ 1][row]);
-        if (i == 0) {
-          m = top;
-        } else if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
-          // O's last product is done: S was issued after it.
-          const float keep = m == -INFINITY ? 0.f : exp2_approx((m - top) * c);
+        if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
+          // A maximum grew by more than kRescale (or was -infinity): O and l
+          // move to the new base. O's last product is done: S was issued after
+          // it.
           const bool fresh = m == -INFINITY;
+          const float keep = fresh ? 0.f : exp2_approx((m - top) * c);
           l *= keep;
           m = top;
+          mc = m == -INFINITY ? 0.f : -m * c;
+          if (i > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 2; q += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + q, o);
+              tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            float o[32];
-            tmem_ld32(o_addr + 32 * q, o);
-            tmem_wait_ld();
-            uint32_t w[2][16];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j / 16][j % 16] = __float_as_uint(fresh ? 0.f : o[j] * keep);
-            tmem_st16(o_addr + 32 * q, w[0]);
-            tmem_st16(o_addr + 32 * q + 16, w[1]);
+              for (int j = 0; j < 16; ++j)
+                o[j] = __float_as_uint(fresh ? 0.f : __uint_as_float(o[j]) * keep);
+              tmem_st16(o_addr + q, o);
+            }
           }
         }
-        const float base = m == -INFINITY ? 0.f : -m * c;
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        // P of a block of 32 keys, and its part of the sum. Each step's
+        // instructions are independent of each other.
+        auto powers = [&](float* x, int q) {
           uint32_t w[16];
+          const float2 c2 = make_float2(c, c), b2 = make_float2(mc, mc);
+          float2 sum[4] = {};
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 x = ffma2(make_float2(s[32 * q + 2 * j], s[32 * q + 2 * j + 1]),
-                                   make_float2(c, c), make_float2(base, base));
-            const float2 e = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-            sum = fadd2(sum, e);
+            float2 e = ffma2(make_float2(x[2 * j], x[2 * j + 1]), c2, b2);
+            e = make_float2(exp2_approx(e.x), exp2_approx(e.y));
             w[j] = pack_bf16(e.x, e.y);
+            sum[j & 3] = fadd2(sum[j & 3], e);
           }
           tmem_st16(s_addr + 32 * half + 16 * q, w);
-        }
-        l += sum.x + sum.y;
+          const float2 z = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
+          l += z.x + z.y;
+        };
+        const uint32_t zero[16] = {};
+        if (live0) powers(s, 0);
+        else if (used0) tmem_st16(s_addr + 32 * half, zero);
+        if (live1) powers(s + 32, 1);
+        else if (used1) tmem_st16(s_addr + 32 * half + 16, zero);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -405,8 +469,8 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         float total = l, f = 1.f;
         if (a.sink_logits != nullptr) {
           const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
-          const float mc = m * c, top = fmaxf(mc, z), base = top == -INFINITY ? 0.f : top;
-          f = exp2_approx(mc - base);
+          const float ms = m * c, top = fmaxf(ms, z), base = top == -INFINITY ? 0.f : top;
+          f = exp2_approx(ms - base);
           total = l * f + exp2_approx(z - base);
         }
         const float inv = l == 0.f ? 0.f : f / total;
@@ -448,31 +512,42 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------ units and copies
-    const uint64_t keep = l2_evict_normal_policy();
-    int slot = 0, stage = 0;
-    uint32_t u_phase = 0, phase = 0, q_phase = 0;
-    unsigned next = 0;
-    if (lane == 0) next = atomicAdd(p.counter, 1u);
-    next = __shfl_sync(kFullMask, next, 0);
+  if (warp == kUnitWarp) {
+    // ------------------------------------------------ units
+    // Takes units and works out what they hold, some units ahead of the other
+    // warps: the lookups are chains of loads. The offsets and lengths of a few
+    // sequences stay in the lanes.
+    const int n2 = 2 * p.n, seqs = a.seqs.num_seqs;
+    const bool few = a.seqs.q_offsets != nullptr && seqs <= kFewSeqs;
+    SeqRows mine = {a.T, 0, 0, 0};
+    if (few && lane <= seqs)
+      mine = sequence_rows(a.seqs, lane, a.T, a.cache.page_shift, a.status, blockIdx.x == 0);
+    int slot = 0;
+    uint32_t u_phase = 0;
+    long long idx = blockIdx.x;
     for (;;) {
-      const unsigned idx = next;
       Unit u;
       u.seq = -1;
-      if ((long long)idx < p.units) {
-        if (lane == 0) next = atomicAdd(p.counter, 1u);
-        next = __shfl_sync(kFullMask, next, 0);
-        u.kvh = (int)(idx % (unsigned)a.cache.kv_heads);
-        const int at = p.slots - 1 - (int)(idx / (unsigned)a.cache.kv_heads);
-        const int b = sequence_of_slot(a.seqs, at, a.T, 2 * p.n, lane);
-        const SeqRows r =
-            sequence_rows(a.seqs, b, a.T, a.cache.page_shift, a.status, lane == 0 && u.kvh == 0);
-        const int tile = a.seqs.q_offsets == nullptr ? 0 : at - (r.first / (2 * p.n) + b);
-        const int t0 = tile * 2 * p.n;
-        u.nt = min(2 * p.n, r.count - t0);
-        if (u.nt <= 0) continue;
+      unsigned taken = 0;
+      if (idx < p.units) {
+        if (lane == 0) taken = atomicAdd(p.counter, 1u);   // used after this unit
+        u.kvh = (int)(idx % a.cache.kv_heads);
+        const int at = p.slots - 1 - (int)(idx / a.cache.kv_heads);
+        int b;
+        SeqRows r;
+        if (few) {
+          b = __popc(__ballot_sync(kFullMask, lane <= seqs && mine.first / n2 + lane <= at)) - 1;
+          r.first = __shfl_sync(kFullMask, mine.first, b);
+          r.count = __shfl_sync(kFullMask, mine.count, b);
+          r.pos0 = __shfl_sync(kFullMask, mine.pos0, b);
+        } else {
+          b = sequence_of_slot(a.seqs, at, a.T, n2, lane);
+          r = sequence_rows(a.seqs, b, a.T, a.cache.page_shift, a.status, lane == 0 && u.kvh == 0);
+        }
+        const int tile = a.seqs.q_offsets == nullptr ? 0 : at - (r.first / n2 + b);
+        const int t0 = tile * n2;
         u.seq = b;
+        u.nt = min(n2, r.count - t0);
         u.row0 = r.first + t0;
         u.pos0 = r.pos0 + t0;
         u.hi = max(0, u.pos0 + u.nt);
@@ -486,45 +561,84 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         u.tiles[0] = hi0 > 0 ? u.sink_tiles + (hi0 - u.start + kKeys - 1) / kKeys : 0;
         if (u.nt <= p.n) u.tiles[1] = 0;
       }
-      ok = ok && mbar_wait_warp(&sh.u_empty[slot], u_phase ^ 1u);
-      if (lane == 0) {
-        sh.unit[slot] = u;
-        sh.bad_lo[slot] = 0x7fffffff;
-        sh.bad_hi[slot] = -1;
-        mbar_arrive(&sh.u_full[slot]);
+      if (u.seq < 0 || u.nt > 0) {
+        int id = 0;
+        const bool keys = u.seq >= 0 && max(u.tiles[0], u.tiles[1]) > 0;
+        if (keys) {
+          const KeyTile kt = key_tile(u, 0, a.window);
+          const int key = kt.j0 + lane * p.box_rows;
+          if (box_wanted(u, kt, 0, key, lane, p)) id = page_id(p, u, key);
+        }
+        ok = ok && mbar_wait_warp(&sh.u_empty[slot], u_phase ^ 1u);
+        if (lane < 16) sh.first_ids[slot][lane] = id;
+        if (lane == 0) {
+          sh.unit[slot] = u;
+          sh.bad_lo[slot] = 0x7fffffff;
+          sh.bad_hi[slot] = -1;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.u_full[slot]);
+        if (++slot == kUnitRing) {
+          slot = 0;
+          u_phase ^= 1u;
+        }
       }
+      if (u.seq < 0) break;
+      idx = (long long)gridDim.x + __shfl_sync(kFullMask, taken, 0);
+    }
+    if (lane == 0) {
+      // The last CTA to take its end leaves the counters at zero.
+      if (atomicAdd(p.counter + 1, 1u) == gridDim.x - 1) {
+        p.counter[0] = 0;
+        p.counter[1] = 0;
+      }
+    }
+  } else if (warp == kLoadWarp) {
+    // ------------------------------------------------ copies
+    const uint64_t keep = l2_evict_normal_policy();
+    int slot = 0, stage = 0, q_slot = 0;
+    uint32_t u_phase = 0, phase = 0, q_phase = 0;
+    for (;;) {
+      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const Unit u = sh.unit[slot];
+      int id = lane < 16 ? sh.first_ids[slot][lane] : 0;
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
       if (++slot == kUnitRing) {
         slot = 0;
         u_phase ^= 1u;
       }
       if (u.seq < 0) break;
       const int tiles = max(u.tiles[0], u.tiles[1]);
-      if (tiles == 0 || !ok) continue;
+      if (tiles == 0) continue;
 
-      ok = ok && mbar_wait_warp(&sh.q_empty, q_phase ^ 1u);
-      q_phase ^= 1u;
+      ok = ok && mbar_wait_warp(&sh.q_empty[q_slot], q_phase ^ 1u);
       const int row_tiles = u.nt > p.n ? 2 : 1;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&sh.q_full,
+        mbar_arrive_expect_tx(&sh.q_full[q_slot],
                               (uint32_t)(row_tiles * S::kSubs * p.n * a.group * 128));
         for (int t = 0; t < row_tiles; ++t)
           for (int c = 0; c < S::kSubs; ++c)
-            tma_load_4d(q_smem + t * S::kTileBytes + c * S::kSub, &maps.q, 0, u.kvh * a.group, c,
-                        u.row0 + t * p.n, &sh.q_full, keep);
+            tma_load_4d(q_smem + (q_slot * 2 + t) * S::kTileBytes + c * S::kSub, &maps.q, 0,
+                        u.kvh * a.group, c, u.row0 + t * p.n, &sh.q_full[q_slot], keep);
       }
-      const int* table = a.seqs.page_table + (int64_t)u.seq * a.seqs.table_stride;
+      __syncwarp();
+      if (++q_slot == S::kQSlots) {
+        q_slot = 0;
+        q_phase ^= 1u;
+      }
       for (int i = 0; i < tiles && ok; ++i) {
         const KeyTile kt = key_tile(u, i, a.window);
-        // Lane x copies box x, if a row sees a key of it.
+        // Lane x copies box x, if a row sees a key of it; the next tile's
+        // pages are looked up meanwhile.
         const int key = kt.j0 + lane * p.box_rows;
-        const bool want = lane < (kKeys >> p.box_shift) && key < kt.end &&
-                          (i < u.sink_tiles || key + p.box_rows > u.lo || key < u.sinks);
-        int id = 0;
-        if (want) {
-          id = __ldg(table + (key >> a.cache.page_shift));
-          if ((unsigned)id >= (uint64_t)a.cache.num_pages)
-            atomicAdd(&a.status[kStatusBadPages], 1ull);
+        const bool want = box_wanted(u, kt, i, key, lane, p);
+        int next_id = 0;
+        if (i + 1 < tiles) {
+          const KeyTile nt = key_tile(u, i + 1, a.window);
+          const int next_key = nt.j0 + lane * p.box_rows;
+          if (box_wanted(u, nt, i + 1, next_key, lane, p)) next_id = page_id(p, u, next_key);
         }
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(kFullMask, want)) *
                                (uint32_t)p.box_rows * 128u * S::kSubs;
@@ -545,128 +659,117 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
             phase ^= 1u;
           }
         }
-      }
-    }
-    if (lane == 0) {
-      // The last CTA to take its end leaves the counters at zero.
-      if (atomicAdd(p.counter + 1, 1u) == gridDim.x - 1) {
-        p.counter[0] = 0;
-        p.counter[1] = 0;
+        id = next_id;
       }
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ matrix instructions
-    // The whole warp waits; one lane, elected once, issues everything, so the
-    // products run in the order of issue and a commit covers all before it.
-    const bool leader = elect_one();
-    int slot = 0, stage = 0;
-    uint32_t u_phase = 0, phase = 0, q_phase = 0;
-    uint32_t p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
-    const uint32_t q_addr = __shfl_sync(kFullMask, smem_addr(q_smem), 0);
-    const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
-    const uint32_t idesc_o = __shfl_sync(kFullMask, mma_idesc(D, true), 0);
-    for (;;) {
-      ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
-      if (!ok) break;
-      const int seq = sh.unit[slot].seq;
-      if (seq < 0) break;
-      const Unit u = sh.unit[slot];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
-      if (++slot == kUnitRing) {
-        slot = 0;
-        u_phase ^= 1u;
-      }
-      const int tiles = max(u.tiles[0], u.tiles[1]);
-      if (tiles == 0) continue;
-      ok = ok && mbar_wait_warp(&sh.q_full, q_phase);
-      q_phase ^= 1u;
-      // S of both row tiles with the keys in stage `stage`.
-      auto scores = [&](int t, int cols) {
-        const uint32_t k_addr = ring_addr + (uint32_t)stage * S::kTileBytes;
-        const uint32_t idesc = __shfl_sync(kFullMask, mma_idesc((cols + 15) & ~15, false), 0);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (uint32_t)(k / 4) * S::kSub + (uint32_t)(k % 4) * 32;
-            tc_mma_ss(tmem + (uint32_t)t * 128, smem_desc(q_addr + (uint32_t)t * S::kTileBytes + at, 16),
-                      smem_desc(k_addr + at, 16), idesc, k > 0 ? 1u : 0u);
-          }
-          tc_commit(&sh.s_full[t]);
-        }
-        __syncwarp();
-      };
-      auto release = [&](int s) {
-        if (leader) tc_commit(&sh.empty[s]);
-      };
+    // One elected thread waits and issues, so the products run in the order of
+    // issue and a commit covers all before it. Per key tile and row tile it
+    // issues O += P V and the next S back to back: the copies both need are
+    // waited for before P, because a gap between instructions idles the
+    // tensor pipe (its queue holds little).
+    if (elect_one()) {
+      int slot = 0, stage = 0, q_slot = 0;
+      uint32_t u_phase = 0, phase = 0, q_phase = 0;
+      uint32_t p_phase = 0, o_phase = 0;          // bit t: row tile t
+      const uint32_t q_base = smem_addr(q_smem), ring_addr = smem_addr(ring);
+      constexpr uint32_t kIdescO = mma_idesc(D, true);
       auto step = [&]() {
         if (++stage == S::kStages) {
           stage = 0;
           phase ^= 1u;
         }
       };
-      ok = ok && mbar_wait_warp(&sh.full[stage], phase);
-      tc_fence_after_sync();
-      int cols = key_tile(u, 0, a.window).cols;
-      for (int t = 0; t < 2; ++t)
-        if (u.tiles[t] > 0) scores(t, cols);
-      release(stage);
-      step();
-      for (int i = 0; i < tiles; ++i) {
-        const int v_stage = stage;
-        const uint32_t v_phase = phase;
-        step();                                   // now at the next tile's keys
-        const int next_cols = i + 1 < tiles ? key_tile(u, i + 1, a.window).cols : 0;
-        bool v_ready = false, k_ready = false;
-        const bool last1 = u.tiles[1] <= i;       // tile 1 takes no part in this key tile
-        for (int t = 0; t < 2; ++t) {
-          if (i >= u.tiles[t]) continue;
-          if (!v_ready) {
-            ok = ok && mbar_wait_warp(&sh.full[v_stage], v_phase);
-            v_ready = true;
-          }
-          if (i == 0) {                           // the last unit's O has been read
-            ok = ok && mbar_wait_warp(&sh.o_empty[t], o_phase[t] ^ 1u);
-            o_phase[t] ^= 1u;
-          }
-          ok = ok && mbar_wait_warp(&sh.p_full[t], p_phase[t]);
-          p_phase[t] ^= 1u;
-          tc_fence_after_sync();
-          const uint32_t v_addr = ring_addr + (uint32_t)v_stage * S::kTileBytes;
-          const int steps = (cols + 15) / 16;
-          if (leader) {
+      for (;;) {
+        ok = ok && mbar_wait(&sh.u_full[slot], u_phase);
+        if (!ok) break;
+        const Unit u = sh.unit[slot];
+        mbar_arrive(&sh.u_empty[slot]);
+        if (++slot == kUnitRing) {
+          slot = 0;
+          u_phase ^= 1u;
+        }
+        if (u.seq < 0) break;
+        const int tiles = max(u.tiles[0], u.tiles[1]);
+        if (tiles == 0) continue;
+        const uint32_t q_addr = q_base + (uint32_t)q_slot * 2 * S::kTileBytes;
+        // S of row tile t with the keys in stage k_stage.
+        auto scores = [&](int t, int k_stage, int cols) {
+          const uint64_t qd = smem_desc(q_addr + (uint32_t)t * S::kTileBytes, 16);
+          const uint64_t kd = smem_desc(ring_addr + (uint32_t)k_stage * S::kTileBytes, 16);
+          const uint32_t idesc = mma_idesc((cols + 15) & ~15, false);
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              if (k < steps)
-                tc_mma_ts(tmem + kOCol + (uint32_t)t * D, tmem + (uint32_t)t * 128 + k * 8,
-                          smem_desc(v_addr + (uint32_t)k * 2048, S::kSub), idesc_o,
-                          (i > 0 || k > 0) ? 1u : 0u);
-            if (t == 1 || last1) tc_commit(&sh.empty[v_stage]);
-            if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t at = ((uint32_t)(k / 4) * S::kSub + (uint32_t)(k % 4) * 32) >> 4;
+            tc_mma_ss(tmem + (uint32_t)t * 128, qd + at, kd + at, idesc, k > 0 ? 1u : 0u);
           }
-          __syncwarp();
-          if (i + 1 < u.tiles[t]) {
-            if (!k_ready) {
-              ok = ok && mbar_wait_warp(&sh.full[stage], phase);
-              tc_fence_after_sync();
-              k_ready = true;
+          tc_commit(&sh.s_full[t]);
+        };
+        ok = ok && mbar_wait(&sh.q_full[q_slot], q_phase);
+        ok = ok && mbar_wait(&sh.full[stage], phase);
+        tc_fence_after_sync();
+        int cols = key_tile(u, 0, a.window).cols;
+        if (u.tiles[0] > 0) scores(0, stage, cols);
+        if (u.tiles[1] > 0) scores(1, stage, cols);
+        tc_commit(&sh.empty[stage]);
+        if (tiles == 1) tc_commit(&sh.q_empty[q_slot]);
+        step();
+        for (int i = 0; i < tiles; ++i) {
+          const int v_stage = stage;
+          const uint32_t v_phase = phase;
+          step();                                   // now at the next tile's keys
+          const bool more = i + 1 < tiles;
+          const int next_cols = more ? key_tile(u, i + 1, a.window).cols : 0;
+          const int steps = (cols + 15) / 16;
+          const uint64_t vd = smem_desc(ring_addr + (uint32_t)v_stage * S::kTileBytes, S::kSub);
+          ok = ok && mbar_wait(&sh.full[v_stage], v_phase);
+          if (more) ok = ok && mbar_wait(&sh.full[stage], phase);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (i >= u.tiles[t]) continue;
+            if (i == 0) {                           // the last unit's O has been read
+              ok = ok && mbar_wait(&sh.o_empty[t], ((o_phase >> t) & 1u) ^ 1u);
+              o_phase ^= 1u << t;
             }
-            scores(t, next_cols);
+            ok = ok && mbar_wait(&sh.p_full[t], (p_phase >> t) & 1u);
+            p_phase ^= 1u << t;
+            tc_fence_after_sync();
+            const uint32_t o_tmem = tmem + kOCol + (uint32_t)t * D, p_tmem = tmem + (uint32_t)t * 128;
+            if (steps == kKeys / 16) {
+#pragma unroll
+              for (int k = 0; k < kKeys / 16; ++k)
+                tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
+                          (i > 0 || k > 0) ? 1u : 0u);
+            } else {
+              for (int k = 0; k < steps; ++k)
+                tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
+                          (i > 0 || k > 0) ? 1u : 0u);
+            }
+            if (t == 1 || u.tiles[1] <= i) tc_commit(&sh.empty[v_stage]);
+            if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
+            else scores(t, stage, next_cols);
           }
+          if (more) {
+            tc_commit(&sh.empty[stage]);
+            // All products with Q have been issued.
+            if (i + 2 == tiles) tc_commit(&sh.q_empty[q_slot]);
+            step();
+          }
+          cols = next_cols;
         }
-        if (i + 1 < tiles) {
-          release(stage);
-          step();
+        if (++q_slot == S::kQSlots) {
+          q_slot = 0;
+          q_phase ^= 1u;
         }
-        cols = next_cols;
-        // All products with Q have been issued.
-        if ((i + 2 == tiles || tiles == 1) && leader) tc_commit(&sh.q_empty);
-        __syncwarp();
       }
+      // TMEM is freed only after every product has finished.
+      tc_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
+      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+      ok = true;
     }
-    // TMEM is freed only after every product has finished.
-    tc_commit(&sh.drain);
-    mbar_wait(&sh.drain, 0);
+    __syncwarp();
   } else if (warp == kCleanWarp) {
     // ------------------------------------------------ values under the mask
     int slot = 0, stage = 0;
@@ -782,7 +885,7 @@ cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   constexpr size_t smem =
-      1024 + (size_t)(2 + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
+      1024 + (size_t)(2 * S::kQSlots + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::once_flag once[64];
   int dev = 0;
