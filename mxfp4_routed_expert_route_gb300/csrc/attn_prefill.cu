@@ -58,6 +58,10 @@ constexpr int kKeys = 128;              // keys per tile
 constexpr int kLoadWarp = 16, kMmaWarp = 17, kCleanWarp = 18, kUnitWarp = 19;
 constexpr int kUnitRing = 4;
 constexpr int kUnitReaders = 3 + kSoftmaxWarps;     // copies, MMA, values, softmax
+// A CTA takes its next unit while at most one unit, or units of at most this
+// many key tiles, are ahead: short units are taken early enough to hide the
+// lookup, long ones late enough to spread the last of them over the CTAs.
+constexpr int kAheadTiles = 8;
 constexpr int kFewSeqs = 30;            // sequences that the unit warp keeps in its lanes
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
@@ -515,38 +519,67 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   if (warp == kUnitWarp) {
     // ------------------------------------------------ units
     // Takes units and works out what they hold, some units ahead of the other
-    // warps: the lookups are chains of loads. The offsets and lengths of a few
-    // sequences stay in the lanes.
+    // warps: the lookups are chains of loads. With few sequences their rows
+    // stay in the lanes, and the units are taken from the longest sequence
+    // down; else from the last one up. Inside a sequence the last tokens, which
+    // see the most keys, come first.
     const int n2 = 2 * p.n, seqs = a.seqs.num_seqs;
-    const bool few = a.seqs.q_offsets != nullptr && seqs <= kFewSeqs;
-    SeqRows mine = {a.T, 0, 0, 0};
-    if (few && lane <= seqs)
-      mine = sequence_rows(a.seqs, lane, a.T, a.cache.page_shift, a.status, blockIdx.x == 0);
-    int slot = 0;
-    uint32_t u_phase = 0;
+    const bool few = seqs <= kFewSeqs;
+    SeqRows mine = {a.T, 0, 0, 0};                // lane r: the sequence of rank r
+    int mine_seq = 0, before = 0, mine_tiles = 0; // query tiles of the sequences before it
+    long long units = p.units;
+    if (few) {
+      SeqRows r = mine;
+      if (lane <= seqs)
+        r = sequence_rows(a.seqs, lane, a.T, a.cache.page_shift, a.status, blockIdx.x == 0);
+      int rank = 0;
+      for (int b = 0; b <= seqs; ++b) {
+        const int len = __shfl_sync(kFullMask, r.len, b);
+        rank += len > r.len || (len == r.len && b < lane) ? 1 : 0;
+      }
+      for (int b = 0; b <= seqs; ++b)
+        if (__shfl_sync(kFullMask, rank, b) == lane) mine_seq = b;
+      mine.first = __shfl_sync(kFullMask, r.first, mine_seq);
+      mine.count = __shfl_sync(kFullMask, r.count, mine_seq);
+      mine.pos0 = __shfl_sync(kFullMask, r.pos0, mine_seq);
+      mine_tiles = lane <= seqs ? (mine.count + n2 - 1) / n2 : 0;
+      int incl = mine_tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += up;
+      }
+      before = incl - mine_tiles;
+      units = (long long)__shfl_sync(kFullMask, incl, 31) * a.cache.kv_heads;
+    }
+    // Units published and not yet released, and their key tiles (lane s: ring
+    // slot s's).
+    int published = 0, released = 0, ahead = 0, slot_tiles = 0;
     long long idx = blockIdx.x;
     for (;;) {
       Unit u;
       u.seq = -1;
-      unsigned taken = 0;
-      if (idx < p.units) {
-        if (lane == 0) taken = atomicAdd(p.counter, 1u);   // used after this unit
+      if (idx < units) {
         u.kvh = (int)(idx % a.cache.kv_heads);
-        const int at = p.slots - 1 - (int)(idx / a.cache.kv_heads);
-        int b;
+        const int s = (int)(idx / a.cache.kv_heads);
+        int tile;
         SeqRows r;
         if (few) {
-          b = __popc(__ballot_sync(kFullMask, lane <= seqs && mine.first / n2 + lane <= at)) - 1;
-          r.first = __shfl_sync(kFullMask, mine.first, b);
-          r.count = __shfl_sync(kFullMask, mine.count, b);
-          r.pos0 = __shfl_sync(kFullMask, mine.pos0, b);
+          const int rank = __popc(__ballot_sync(kFullMask, lane <= seqs && before <= s)) - 1;
+          u.seq = __shfl_sync(kFullMask, mine_seq, rank);
+          r.first = __shfl_sync(kFullMask, mine.first, rank);
+          r.count = __shfl_sync(kFullMask, mine.count, rank);
+          r.pos0 = __shfl_sync(kFullMask, mine.pos0, rank);
+          tile = __shfl_sync(kFullMask, mine_tiles, rank) - 1 -
+                 (s - __shfl_sync(kFullMask, before, rank));
         } else {
-          b = sequence_of_slot(a.seqs, at, a.T, n2, lane);
-          r = sequence_rows(a.seqs, b, a.T, a.cache.page_shift, a.status, lane == 0 && u.kvh == 0);
+          const int at = p.slots - 1 - s;
+          u.seq = sequence_of_slot(a.seqs, at, a.T, n2, lane);
+          r = sequence_rows(a.seqs, u.seq, a.T, a.cache.page_shift, a.status,
+                            lane == 0 && u.kvh == 0);
+          tile = a.seqs.q_offsets == nullptr ? 0 : at - (r.first / n2 + u.seq);
         }
-        const int tile = a.seqs.q_offsets == nullptr ? 0 : at - (r.first / n2 + b);
         const int t0 = tile * n2;
-        u.seq = b;
         u.nt = min(n2, r.count - t0);
         u.row0 = r.first + t0;
         u.pos0 = r.pos0 + t0;
@@ -562,14 +595,22 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         if (u.nt <= p.n) u.tiles[1] = 0;
       }
       if (u.seq < 0 || u.nt > 0) {
+        const int tiles = u.seq < 0 ? 0 : max(u.tiles[0], u.tiles[1]);
         int id = 0;
-        const bool keys = u.seq >= 0 && max(u.tiles[0], u.tiles[1]) > 0;
-        if (keys) {
+        if (tiles > 0) {
           const KeyTile kt = key_tile(u, 0, a.window);
           const int key = kt.j0 + lane * p.box_rows;
           if (box_wanted(u, kt, 0, key, lane, p)) id = page_id(p, u, key);
         }
-        ok = ok && mbar_wait_warp(&sh.u_empty[slot], u_phase ^ 1u);
+        const int slot = published % kUnitRing;
+        while (published - released >= kUnitRing) {
+          if (ok) ok = mbar_wait_warp(&sh.u_empty[released % kUnitRing],
+                                      (uint32_t)(released / kUnitRing) & 1u);
+          ahead -= __shfl_sync(kFullMask, slot_tiles, released % kUnitRing);
+          ++released;
+        }
+        if (lane == slot) slot_tiles = tiles;
+        ahead += tiles;
         if (lane < 16) sh.first_ids[slot][lane] = id;
         if (lane == 0) {
           sh.unit[slot] = u;
@@ -578,12 +619,17 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.u_full[slot]);
-        if (++slot == kUnitRing) {
-          slot = 0;
-          u_phase ^= 1u;
-        }
+        ++published;
       }
       if (u.seq < 0) break;
+      while (published - released >= 2 && ahead > kAheadTiles) {
+        if (ok) ok = mbar_wait_warp(&sh.u_empty[released % kUnitRing],
+                                    (uint32_t)(released / kUnitRing) & 1u);
+        ahead -= __shfl_sync(kFullMask, slot_tiles, released % kUnitRing);
+        ++released;
+      }
+      unsigned taken = 0;
+      if (lane == 0) taken = atomicAdd(p.counter, 1u);
       idx = (long long)gridDim.x + __shfl_sync(kFullMask, taken, 0);
     }
     if (lane == 0) {
