@@ -72,7 +72,7 @@ struct Shape {
   static constexpr int kSubs = D / 64;                       // 128-byte columns of a row
   static constexpr uint32_t kSub = 128 * 128;                // bytes: 128 rows of one column
   static constexpr uint32_t kTileBytes = kSubs * kSub;
-  static constexpr int kStages = D == 128 ? 4 : 8;           // key and value tiles in flight
+  static constexpr int kStages = D == 128 ? 5 : 8;           // key and value tiles in flight
   static constexpr int kQSlots = D == 128 ? 1 : 2;           // units' queries, as far as they fit
 };
 
@@ -112,7 +112,7 @@ struct __align__(16) PrefillShared {
   int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
   Unit unit[kUnitRing];
   int first_ids[kUnitRing][16];              // pages of the unit's first key tile
-  float row_max[2][2][kRows], row_sum[2][2][kRows];   // [tile][half of the keys]
+  float row_max[2][2][kRows];                // [tile][half of the keys]; at the end the sums
 };
 
 // Key tile i of a unit: its first key, the keys below which a row may see it
@@ -291,8 +291,14 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p) {
   using S = Shape<D>;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* q_smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  // Tiles start on 1024-byte boundaries (the swizzle's), and there is no room
+  // to move up to one.
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  if ((smem_addr(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicAdd(&p.a.status[kStatusWaitTimeouts], 1ull);
+    return;
+  }
+  unsigned char* q_smem = smem_raw;
   unsigned char* ring = q_smem + S::kQSlots * 2 * S::kTileBytes;
   PrefillShared<D>& sh =
       *reinterpret_cast<PrefillShared<D>*>(ring + (size_t)S::kStages * S::kTileBytes);
@@ -467,9 +473,11 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
                            ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D +
                            half * (D / 2);
       if (tiles > 0) {
-        sh.row_sum[t][half][row] = l;
+        bar_sync(1 + t, 256);                      // the last tile's maxima have been read
+        sh.row_max[t][half][row] = l;
         bar_sync(1 + t, 256);
-        l += sh.row_sum[t][half ^ 1][row];
+        l += sh.row_max[t][half ^ 1][row];
+        bar_sync(1 + t, 256);                      // before the next unit's maxima
         float total = l, f = 1.f;
         if (a.sink_logits != nullptr) {
           const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
@@ -710,112 +718,127 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ matrix instructions
-    // One elected thread waits and issues, so the products run in the order of
-    // issue and a commit covers all before it. Per key tile and row tile it
-    // issues O += P V and the next S back to back: the copies both need are
-    // waited for before P, because a gap between instructions idles the
-    // tensor pipe (its queue holds little).
-    if (elect_one()) {
-      int slot = 0, stage = 0, q_slot = 0;
-      uint32_t u_phase = 0, phase = 0, q_phase = 0;
-      uint32_t p_phase = 0, o_phase = 0;          // bit t: row tile t
-      const uint32_t q_base = smem_addr(q_smem), ring_addr = smem_addr(ring);
-      constexpr uint32_t kIdescO = mma_idesc(D, true);
-      auto step = [&]() {
-        if (++stage == S::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      };
-      for (;;) {
-        ok = ok && mbar_wait(&sh.u_full[slot], u_phase);
-        if (!ok) break;
-        const Unit u = sh.unit[slot];
-        mbar_arrive(&sh.u_empty[slot]);
-        if (++slot == kUnitRing) {
-          slot = 0;
-          u_phase ^= 1u;
-        }
-        if (u.seq < 0) break;
-        const int tiles = max(u.tiles[0], u.tiles[1]);
-        if (tiles == 0) continue;
-        const uint32_t q_addr = q_base + (uint32_t)q_slot * 2 * S::kTileBytes;
-        // S of row tile t with the keys in stage k_stage.
-        auto scores = [&](int t, int k_stage, int cols) {
-          const uint64_t qd = smem_desc(q_addr + (uint32_t)t * S::kTileBytes, 16);
-          const uint64_t kd = smem_desc(ring_addr + (uint32_t)k_stage * S::kTileBytes, 16);
-          const uint32_t idesc = mma_idesc((cols + 15) & ~15, false);
+    // The whole warp runs the loop, on values the compiler can tell are the
+    // same in every lane (they come through shuffles and votes), so that the
+    // instructions' operands stay in uniform registers; one elected lane
+    // issues. (A loop that one lane ran alone moved every operand over for
+    // each instruction, 140 cycles apiece.) elect.sync elects the same lane
+    // every time, so the products run in the order of issue and a commit
+    // covers all before it. Per key tile and row tile it issues O += P V and
+    // the next S back to back: the copies both need are waited for before P.
+    int slot = 0, stage = 0, q_slot = 0;
+    uint32_t u_phase = 0, phase = 0, q_phase = 0;
+    uint32_t p_phase = 0, o_phase = 0;            // bit t: row tile t
+    const uint32_t q_base = __shfl_sync(kFullMask, smem_addr(q_smem), 0);
+    const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
+    constexpr uint32_t kIdescO = mma_idesc(D, true);
+    auto step = [&]() {
+      if (++stage == S::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    // S of row tile t with the keys in stage k_stage.
+    auto scores = [&](int t, uint32_t q_addr, int k_stage, uint32_t idesc) {
+      const uint64_t qd = smem_desc(q_addr + (uint32_t)t * S::kTileBytes, 16);
+      const uint64_t kd = smem_desc(ring_addr + (uint32_t)k_stage * S::kTileBytes, 16);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = ((uint32_t)(k / 4) * S::kSub + (uint32_t)(k % 4) * 32) >> 4;
-            tc_mma_ss(tmem + (uint32_t)t * 128, qd + at, kd + at, idesc, k > 0 ? 1u : 0u);
-          }
-          tc_commit(&sh.s_full[t]);
-        };
-        ok = ok && mbar_wait(&sh.q_full[q_slot], q_phase);
-        ok = ok && mbar_wait(&sh.full[stage], phase);
-        tc_fence_after_sync();
-        int cols = key_tile(u, 0, a.window).cols;
-        if (u.tiles[0] > 0) scores(0, stage, cols);
-        if (u.tiles[1] > 0) scores(1, stage, cols);
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = ((uint32_t)(k / 4) * S::kSub + (uint32_t)(k % 4) * 32) >> 4;
+        tc_mma_ss(tmem + (uint32_t)t * 128, qd + at, kd + at, idesc, k > 0 ? 1u : 0u);
+      }
+      tc_commit(&sh.s_full[t]);
+    };
+    while (ok) {
+      ok = mbar_wait_warp(&sh.u_full[slot], u_phase);
+      if (!ok) break;
+      const Unit v = sh.unit[slot];
+      Unit u;
+      u.seq = __shfl_sync(kFullMask, v.seq, 0);
+      u.nt = __shfl_sync(kFullMask, v.nt, 0);
+      u.pos0 = __shfl_sync(kFullMask, v.pos0, 0);
+      u.hi = __shfl_sync(kFullMask, v.hi, 0);
+      u.start = __shfl_sync(kFullMask, v.start, 0);
+      u.sinks = __shfl_sync(kFullMask, v.sinks, 0);
+      u.sink_tiles = __shfl_sync(kFullMask, v.sink_tiles, 0);
+      u.tiles[0] = __shfl_sync(kFullMask, v.tiles[0], 0);
+      u.tiles[1] = __shfl_sync(kFullMask, v.tiles[1], 0);
+      if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
+      if (++slot == kUnitRing) {
+        slot = 0;
+        u_phase ^= 1u;
+      }
+      if (u.seq < 0) break;
+      const int tiles = max(u.tiles[0], u.tiles[1]);
+      if (tiles == 0) continue;
+      const uint32_t q_addr = q_base + (uint32_t)q_slot * 2 * S::kTileBytes;
+      if (ok) ok = mbar_wait_warp(&sh.q_full[q_slot], q_phase);
+      if (ok) ok = mbar_wait_warp(&sh.full[stage], phase);
+      tc_fence_after_sync();
+      int cols = key_tile(u, 0, a.window).cols;
+      if (elect_one()) {
+        const uint32_t idesc = mma_idesc((cols + 15) & ~15, false);
+        if (u.tiles[0] > 0) scores(0, q_addr, stage, idesc);
+        if (u.tiles[1] > 0) scores(1, q_addr, stage, idesc);
         tc_commit(&sh.empty[stage]);
         if (tiles == 1) tc_commit(&sh.q_empty[q_slot]);
-        step();
-        for (int i = 0; i < tiles; ++i) {
-          const int v_stage = stage;
-          const uint32_t v_phase = phase;
-          step();                                   // now at the next tile's keys
-          const bool more = i + 1 < tiles;
-          const int next_cols = more ? key_tile(u, i + 1, a.window).cols : 0;
-          const int steps = (cols + 15) / 16;
-          const uint64_t vd = smem_desc(ring_addr + (uint32_t)v_stage * S::kTileBytes, S::kSub);
-          ok = ok && mbar_wait(&sh.full[v_stage], v_phase);
-          if (more) ok = ok && mbar_wait(&sh.full[stage], phase);
+      }
+      __syncwarp();
+      step();
+      for (int i = 0; i < tiles; ++i) {
+        const int v_stage = stage;
+        const uint32_t v_phase = phase;
+        step();                                     // now at the next tile's keys
+        const bool more = i + 1 < tiles;
+        const int next_cols = more ? key_tile(u, i + 1, a.window).cols : 0;
+        const int steps = (cols + 15) / 16;
+        const uint32_t idesc = mma_idesc((next_cols + 15) & ~15, false);
+        if (ok) ok = mbar_wait_warp(&sh.full[v_stage], v_phase);
+        if (ok && more) ok = mbar_wait_warp(&sh.full[stage], phase);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (i >= u.tiles[t]) continue;
+        for (int t = 0; t < 2; ++t) {
+          if (i < u.tiles[t]) {
             if (i == 0) {                           // the last unit's O has been read
-              ok = ok && mbar_wait(&sh.o_empty[t], ((o_phase >> t) & 1u) ^ 1u);
+              if (ok) ok = mbar_wait_warp(&sh.o_empty[t], ((o_phase >> t) & 1u) ^ 1u);
               o_phase ^= 1u << t;
             }
-            ok = ok && mbar_wait(&sh.p_full[t], (p_phase >> t) & 1u);
+            if (ok) ok = mbar_wait_warp(&sh.p_full[t], (p_phase >> t) & 1u);
             p_phase ^= 1u << t;
             tc_fence_after_sync();
             const uint32_t o_tmem = tmem + kOCol + (uint32_t)t * D, p_tmem = tmem + (uint32_t)t * 128;
-            if (steps == kKeys / 16) {
+            const uint64_t vd = smem_desc(ring_addr + (uint32_t)v_stage * S::kTileBytes, S::kSub);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < kKeys / 16; ++k)
-                tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
-                          (i > 0 || k > 0) ? 1u : 0u);
-            } else {
-              for (int k = 0; k < steps; ++k)
-                tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
-                          (i > 0 || k > 0) ? 1u : 0u);
+                if (k < steps)
+                  tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
+                            (i > 0 || k > 0) ? 1u : 0u);
+              if (t == 1 || u.tiles[1] <= i) tc_commit(&sh.empty[v_stage]);
+              if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
+              else scores(t, q_addr, stage, idesc);
             }
-            if (t == 1 || u.tiles[1] <= i) tc_commit(&sh.empty[v_stage]);
-            if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
-            else scores(t, stage, next_cols);
+            __syncwarp();
           }
-          if (more) {
+        }
+        if (more) {
+          if (elect_one()) {
             tc_commit(&sh.empty[stage]);
             // All products with Q have been issued.
             if (i + 2 == tiles) tc_commit(&sh.q_empty[q_slot]);
-            step();
           }
-          cols = next_cols;
+          __syncwarp();
+          step();
         }
-        if (++q_slot == S::kQSlots) {
-          q_slot = 0;
-          q_phase ^= 1u;
-        }
+        cols = next_cols;
       }
-      // TMEM is freed only after every product has finished.
-      tc_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0);
-      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
-      ok = true;
+      if (++q_slot == S::kQSlots) {
+        q_slot = 0;
+        q_phase ^= 1u;
+      }
     }
-    __syncwarp();
+    // TMEM is freed only after every product has finished.
+    if (elect_one()) tc_commit(&sh.drain);
+    mbar_wait(&sh.drain, 0);
   } else if (warp == kCleanWarp) {
     // ------------------------------------------------ values under the mask
     int slot = 0, stage = 0;
@@ -931,7 +954,7 @@ cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
       return cudaErrorInvalidValue;
   }
   constexpr size_t smem =
-      1024 + (size_t)(2 * S::kQSlots + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
+      (size_t)(2 * S::kQSlots + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::once_flag once[64];
   int dev = 0;
