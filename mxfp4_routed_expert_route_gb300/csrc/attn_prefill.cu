@@ -112,7 +112,8 @@ struct __align__(16) PrefillShared {
   int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
   Unit unit[kUnitRing];
   int first_ids[kUnitRing][16];              // pages of the unit's first key tile
-  float row_max[2][2][kRows];                // [tile][half of the keys]; at the end the sums
+  float row_max[2][2][kRows];                // [tile][half of the keys]
+  float row_sum[D == 64 ? 2 : 1][2][D == 64 ? kRows : 1];
 };
 
 // Key tile i of a unit: its first key, the keys below which a row may see it
@@ -384,33 +385,44 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         // Of this warp's two blocks of 32 keys: `live` has a key that one of
         // its rows sees, `used` takes part in the second product (P of keys
         // that no row of the warp sees is zero).
-        bool live0 = true, live1 = true, used0 = true, used1 = true;
+        bool live[2] = {true, true}, used[2] = {true, true};
         if (i < whole0 || i >= whole1) {
           const KeyTile kt = key_tile(u, i, a.window);
-          // Bit j of `seen`: the row sees key j0 + j.
-          auto mask = [&](float* x, int q) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
             const int j0 = kt.j0 + 64 * half + 32 * q;
-            uint32_t seen = low_bits(min(pos, kt.end - 1) - j0 + 1);
-            if (a.window != 0)
-              seen &= ~low_bits(pos - a.window + 1 - j0) | low_bits(u.sinks - j0);
+            used[q] = 64 * half + 32 * q < kt.cols;
+            live[q] = j0 <= min(pos_last, kt.end - 1) &&
+                      (i < u.sink_tiles || a.window == 0 || j0 + 31 > pos_first - a.window ||
+                       j0 < u.sinks);
+            const bool all = j0 + 31 <= min(pos_first, kt.end - 1) &&
+                             (a.window == 0 || j0 > pos_last - a.window || j0 + 32 <= u.sinks);
+            if (live[q] && !all) {
+              // Bit j of `seen`: the row sees key j0 + j.
+              uint32_t seen = low_bits(min(pos, kt.end - 1) - j0 + 1);
+              if (a.window != 0)
+                seen &= ~low_bits(pos - a.window + 1 - j0) | low_bits(u.sinks - j0);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!((seen >> j) & 1u)) x[j] = -INFINITY;
-            return __any_sync(kFullMask, seen != 0) != 0;
-          };
-          live0 = mask(s, 0);
-          live1 = mask(s + 32, 1);
-          used0 = 64 * half < kt.cols;
-          used1 = 64 * half + 32 < kt.cols;
+              for (int j = 0; j < 32; ++j)
+                if (!((seen >> j) & 1u)) s[32 * q + j] = -INFINITY;
+            }
+          }
         }
-        float tops[4] = {s[0], s[1], s[2], s[3]};
+        float mine = -INFINITY;
 #pragma unroll
-        for (int j = 4; j < 60; j += 8)
+        for (int q = 0; q < 2; ++q) {
+          if (live[q]) {
+            const float* x = s + 32 * q;
+            float tops[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], s[j + 2 * e], s[j + 2 * e + 1]);
-        tops[0] = max3(tops[0], s[60], s[61]);
-        tops[1] = max3(tops[1], s[62], s[63]);
-        const float mine = max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
+            for (int j = 4; j < 28; j += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], x[j + 2 * e], x[j + 2 * e + 1]);
+            tops[0] = max3(tops[0], x[28], x[29]);
+            tops[1] = max3(tops[1], x[30], x[31]);
+            mine = max3(mine, max3(tops[0], tops[1], tops[2]), tops[3]);
+          }
+        }
         // The other half's maximum. Past the barrier both halves hold their
         // scores in registers, so P may overwrite them.
         sh.row_max[t][half][row] = mine;
@@ -457,11 +469,15 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           const float2 z = fadd2(fadd2(sum[0], sum[1]), fadd2(sum[2], sum[3]));
           l += z.x + z.y;
         };
-        const uint32_t zero[16] = {};
-        if (live0) powers(s, 0);
-        else if (used0) tmem_st16(s_addr + 32 * half, zero);
-        if (live1) powers(s + 32, 1);
-        else if (used1) tmem_st16(s_addr + 32 * half + 16, zero);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (live[q]) {
+            powers(s + 32 * q, q);
+          } else if (used[q]) {
+            const uint32_t zero[16] = {};
+            tmem_st16(s_addr + 32 * half + 16 * q, zero);
+          }
+        }
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -473,11 +489,16 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
                            ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D +
                            half * (D / 2);
       if (tiles > 0) {
-        bar_sync(1 + t, 256);                      // the last tile's maxima have been read
-        sh.row_max[t][half][row] = l;
+        // The halves' sums, in an array of their own where there is room, else
+        // after the last tile's maxima have been read and before the next
+        // unit's are written.
+        float(*sums)[kRows] = D == 64 ? reinterpret_cast<float(*)[kRows]>(sh.row_sum[D == 64 ? t : 0])
+                                      : sh.row_max[t];
+        if (D != 64) bar_sync(1 + t, 256);
+        sums[half][row] = l;
         bar_sync(1 + t, 256);
-        l += sh.row_max[t][half ^ 1][row];
-        bar_sync(1 + t, 256);                      // before the next unit's maxima
+        l += sums[half ^ 1][row];
+        if (D != 64) bar_sync(1 + t, 256);
         float total = l, f = 1.f;
         if (a.sink_logits != nullptr) {
           const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
