@@ -55,7 +55,7 @@ constexpr size_t kPieceBytes = (size_t)kRowsMax * 128 * 4 + 2 * kRowsMax * 4;
 // The workspace: this kernel's counters, the prefill kernel's, the pieces.
 constexpr size_t kCounterBytes = (size_t)kMaxCtas * 4, kPiecesAt = kCounterBytes + 256;
 
-template <typename Tok, int D, int kMT = 1>
+template <typename Tok, int D, int kMT = 1, int kH = 16>
 struct Shape {
   static constexpr int kTile = sizeof(Tok) == 2 ? 64 : 32;          // keys per tile
   static constexpr int kPer = kTile / kGroups;                      // keys per consumer warp
@@ -67,7 +67,7 @@ struct Shape {
   static constexpr int kStages =
       (kMT == 1 ? 5 : kMT == 2 ? 4 : sizeof(Tok) == 2 ? 3 : 2) * 32768 / (2 * (int)kHalf);
   static constexpr int kQRow = D * (int)sizeof(Tok) + 16;           // padded row in shared memory
-  static constexpr int kAcc = 16 * D / 32;                          // result elements per lane
+  static constexpr int kAcc = kH * D / 32;                          // result elements per lane
 };
 
 struct Unit {
@@ -176,11 +176,11 @@ __device__ __forceinline__ uint32_t box_row(int j, int box_rows, int box_shift, 
 
 // One warp: 16 query heads x the warp's share of each tile's keys.
 // Result element i of a lane: row row(i), column col(i).
-template <typename Tok, int D>
+template <typename Tok, int D, int kH>
 struct Consumer;
 
 template <int D>
-struct Consumer<__nv_bfloat16, D> {
+struct Consumer<__nv_bfloat16, D, 16> {
   using S = Shape<__nv_bfloat16, D>;
   uint32_t q[D / 16][4];
   float m[2], l[2];          // rows lane / 4 and lane / 4 + 8; l: this lane's keys only
@@ -306,20 +306,22 @@ struct Consumer<__nv_bfloat16, D> {
   }
 };
 
-template <int D>
-struct Consumer<float, D> {
-  using S = Shape<float, D>;
+// kH of the 16 heads that the warp's buffers have room for.
+template <int D, int kH>
+struct Consumer<float, D, kH> {
+  using S = Shape<float, D, 1, kH>;
+  static constexpr int kL = kH / 4;    // heads per lane in the scores
   static constexpr int kW = D / 32;    // result columns per lane
   uint32_t q_addr;
-  float m[4], l[4];          // heads 4 (lane / 8) ..; l: this lane's key (lane % 8) only
-  float acc[S::kAcc];        // [16 heads][kW]
+  float m[kL], l[kL];        // heads kL (lane / 8) ..; l: this lane's key (lane % 8) only
+  float acc[S::kAcc];        // [kH heads][kW]
 
   static __device__ __forceinline__ int row(int i, int) { return i / kW; }
   static __device__ __forceinline__ int col(int i, int lane) { return lane * kW + i % kW; }
   __device__ __forceinline__ void start(uint32_t q_smem, int) {
     q_addr = q_smem;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kL; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
     }
@@ -337,24 +339,33 @@ struct Consumer<float, D> {
     const int t = lane & 7, hg = lane >> 3;
     const uint32_t box = (uint32_t)d.box_rows * 128u;
     const uint32_t krow = k_addr + box_row(group * 8 + t, d.box_rows, d.box_shift, S::kSubs);
-    float s[4] = {};
-#pragma unroll 4
-    for (int c = 0; c < D / 4; ++c) {
-      const float4 kx = lds4(krow + (uint32_t)(c >> 3) * box + (uint32_t)(((c & 7) ^ t) << 4));
+    // Two sums per head, over 128 bytes of the row at a time: the reads of a
+    // step are in flight together.
+    float s[kL] = {}, s1[kL] = {};
+#pragma unroll(kL == 1 ? 2 : 1)
+    for (int c = 0; c < S::kSubs; ++c) {
+      const uint32_t at = krow + (uint32_t)c * box;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 qx = lds4(q_addr + (uint32_t)((hg * 4 + i) * S::kQRow + c * 16));
-        s[i] = fmaf(qx.x, kx.x, s[i]);
-        s[i] = fmaf(qx.y, kx.y, s[i]);
-        s[i] = fmaf(qx.z, kx.z, s[i]);
-        s[i] = fmaf(qx.w, kx.w, s[i]);
+      for (int k = 0; k < 8; ++k) {
+        const float4 kx = lds4(at + (uint32_t)((k ^ t) << 4));
+#pragma unroll
+        for (int i = 0; i < kL; ++i) {
+          const float4 qx = lds4(q_addr + (uint32_t)((hg * kL + i) * S::kQRow + c * 128 + k * 16));
+          float& z = k & 1 ? s1[i] : s[i];
+          z = fmaf(qx.x, kx.x, z);
+          z = fmaf(qx.y, kx.y, z);
+          z = fmaf(qx.z, kx.z, z);
+          z = fmaf(qx.w, kx.w, z);
+        }
       }
     }
+#pragma unroll
+    for (int i = 0; i < kL; ++i) s[i] += s1[i];
     const bool seen = (vis >> t) & 1u;
-    float top[4];
+    float top[kL];
     bool moved = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kL; ++i) {
       s[i] = seen ? s[i] * scale : -INFINITY;
       top[i] = s[i];
 #pragma unroll
@@ -366,31 +377,31 @@ struct Consumer<float, D> {
     moved = __any_sync(kFullMask, moved);
     __syncwarp();                                // the last tile's p has been read
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kL; ++i) {
       const float base = top[i] == -INFINITY ? 0.f : top[i];
       if (moved) {
         const float keep = top[i] == -INFINITY ? 0.f : exp2_approx(m[i] - top[i]);
         l[i] *= keep;
-        if (t == 0) p[128 + hg * 4 + i] = keep;
+        if (t == 0) p[128 + hg * kL + i] = keep;
         m[i] = top[i];
       }
       const float e = exp2_approx(s[i] - base);
       l[i] += e;
-      p[t * 16 + hg * 4 + i] = e;
+      p[t * 16 + hg * kL + i] = e;
     }
     __syncwarp();
     if (moved) {
 #pragma unroll
-      for (int h = 0; h < 16; ++h) {
+      for (int h = 0; h < kH; ++h) {
         const float keep = p[128 + h];
 #pragma unroll
         for (int w = 0; w < kW; ++w) acc[h * kW + w] *= keep;
       }
     }
     const uint32_t p_addr = smem_addr(p);
+    const bool whole = (vis & 0xffu) == 0xffu;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      if (!((vis >> j) & 1u)) continue;          // not seen: its value may be anything
       const uint32_t vrow = v_addr + box_row(group * 8 + j, d.box_rows, d.box_shift, S::kSubs);
       float vx[kW];
       if constexpr (kW == 4) {
@@ -401,8 +412,12 @@ struct Consumer<float, D> {
                             (uint32_t)((((lane >> 1) & 7) ^ j) << 4) + (uint32_t)(lane & 1) * 8;
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vx[0]), "=f"(vx[1]) : "r"(at));
       }
+      if (!whole && !((vis >> j) & 1u)) {        // not seen: its value may be anything
 #pragma unroll
-      for (int h = 0; h < 16; h += 4) {
+        for (int w = 0; w < kW; ++w) vx[w] = 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < kH; h += 4) {
         const float4 e = lds4(p_addr + (uint32_t)(j * 16 + h) * 4);
 #pragma unroll
         for (int w = 0; w < kW; ++w) {
@@ -418,8 +433,8 @@ struct Consumer<float, D> {
                                         float* p) {
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int h = (lane >> 3) * 4 + i;
+    for (int i = 0; i < kL; ++i) {
+      const int h = (lane >> 3) * kL + i;
       const float mo = ms[h], top = fmaxf(m[i], mo);
       const float base = top == -INFINITY ? 0.f : top;
       const float f = exp2_approx(m[i] - base), g = exp2_approx(mo - base);
@@ -437,13 +452,13 @@ struct Consumer<float, D> {
   }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kL; ++i) {
       float t = l[i];
 #pragma unroll
       for (int o = 4; o >= 1; o >>= 1) t += __shfl_xor_sync(kFullMask, t, o);
       if ((lane & 7) == 0) {
-        ms[(lane >> 3) * 4 + i] = m[i];
-        ls[(lane >> 3) * 4 + i] = t;
+        ms[(lane >> 3) * kL + i] = m[i];
+        ls[(lane >> 3) * kL + i] = t;
       }
     }
   }
@@ -473,10 +488,10 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, fl
   return l == 0.f ? 0.f : f / l;
 }
 
-template <typename Tok, int D, int kMT>
+template <typename Tok, int D, int kMT, int kH>
 __global__ void __launch_bounds__(32 * (1 + kGroups * kMT))
 attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs d) {
-  using S = Shape<Tok, D, kMT>;
+  using S = Shape<Tok, D, kMT, kH>;
   constexpr int kThreads = 32 * (1 + kGroups * kMT), kConsumers = kThreads - 32;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -612,7 +627,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   float* buf = merge + (size_t)mt * 2 * S::kAcc * 32;
   float* p_warp = p_smem + cw * kPFloats;
   const float scale = a.scale * kLog2e;
-  Consumer<Tok, D> c;
+  Consumer<Tok, D, kH> c;
   bool ok = true;
   int stage = 0, slot = 0;
   uint32_t phase = 0, q_phase = 0;
@@ -683,10 +698,10 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
 #pragma unroll
         for (int i = 0; i < S::kAcc; i += 2) {
-          const int r = Consumer<Tok, D>::row(i, lane), rr = mt * 16 + r;
+          const int r = Consumer<Tok, D, kH>::row(i, lane), rr = mt * 16 + r;
           if (rr < u.rows) {
             const float inv = finish(a, u.head0 + rr, ms[r], ls[r]);
-            store_pair(out + (int64_t)rr * D + Consumer<Tok, D>::col(i, lane), c.acc[i] * inv,
+            store_pair(out + (int64_t)rr * D + Consumer<Tok, D, kH>::col(i, lane), c.acc[i] * inv,
                        c.acc[i + 1] * inv);
           }
         }
@@ -696,9 +711,9 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         float* st = o + kRowsMax * 128;
 #pragma unroll
         for (int i = 0; i < S::kAcc; i += 2) {
-          const int rr = mt * 16 + Consumer<Tok, D>::row(i, lane);
+          const int rr = mt * 16 + Consumer<Tok, D, kH>::row(i, lane);
           if (rr < u.rows)
-            *reinterpret_cast<float2*>(o + rr * D + Consumer<Tok, D>::col(i, lane)) =
+            *reinterpret_cast<float2*>(o + rr * D + Consumer<Tok, D, kH>::col(i, lane)) =
                 make_float2(c.acc[i], c.acc[i + 1]);
         }
         if (lane < 16 && mt * 16 + lane < u.rows) {
@@ -762,9 +777,9 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
 }
 
-template <typename Tok, int D, int kMT>
+template <typename Tok, int D, int kMT, int kH = 16>
 cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
-  using S = Shape<Tok, D, kMT>;
+  using S = Shape<Tok, D, kMT, kH>;
   DecodeArgs d = {};
   d.a = a;
   d.head_blocks = (a.group + 16 * kMT - 1) / (16 * kMT);
@@ -788,7 +803,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   cudaGetDevice(&dev);
   cudaError_t err = cudaSuccess;
   std::call_once(once[dev & 63], [&] {
-    err = cudaFuncSetAttribute(attention_decode_kernel<Tok, D, kMT>,
+    err = cudaFuncSetAttribute(attention_decode_kernel<Tok, D, kMT, kH>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   });
   if (err != cudaSuccess) return err;
@@ -800,7 +815,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     d.num_seqs = std::min(kMaxSeqs, a.seqs.num_seqs - b);
     const int64_t most = ((int64_t)d.num_seqs * d.units_per_seq * room + kMinTiles - 1) / kMinTiles;
     const int grid = (int)std::min<int64_t>(std::min(attention_num_sms(), kMaxCtas), most);
-    err = launch_after_previous(attention_decode_kernel<Tok, D, kMT>, dim3((unsigned)grid),
+    err = launch_after_previous(attention_decode_kernel<Tok, D, kMT, kH>, dim3((unsigned)grid),
                                 dim3(32 * (1 + kGroups * kMT)), smem, stream, maps, d);
     if (err != cudaSuccess) return err;
   }
@@ -809,6 +824,14 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
 
 template <typename Tok, int D>
 cudaError_t launch_heads(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  // float32: the CUDA cores' work grows with the heads that a warp carries, so
+  // groups of up to 4 and 8 have kernels of their own (24 sequences of up to
+  // 3001 keys, 4 heads to a key head: 130 us with 16 carried, KKK with 4). The
+  // bf16 instruction takes 16 rows whatever the group.
+  if constexpr (sizeof(Tok) == 4) {
+    if (a.group <= 4) return launch<Tok, D, 1, 4>(a, workspace, stream);
+    if (a.group <= 8) return launch<Tok, D, 1, 8>(a, workspace, stream);
+  }
   if (a.group <= 16) return launch<Tok, D, 1>(a, workspace, stream);
   if (a.group <= 32) return launch<Tok, D, 2>(a, workspace, stream);
   return launch<Tok, D, 4>(a, workspace, stream);
