@@ -73,7 +73,7 @@ bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, int box_subs
                    CUtensorMap* map);
 int attention_num_sms();
 
-// Any dtype, any number of new tokens, on the CUDA cores (attn_simt.cu).
+// float32 prompts, on the CUDA cores (attn_simt.cu).
 cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace mxfp4el

@@ -1,8 +1,8 @@
-// attn_simt.cu -- attention over the paged cache on the CUDA cores: any
-// dtype, any number of new tokens, float32 arithmetic throughout.
+// attn_simt.cu -- float32 attention of prompts over the paged cache, on the
+// CUDA cores: the tensor cores have no operand type that keeps its 24 bits.
 //
-// One block takes a tile of up to 64 query rows of one key head: n tokens of
-// one sequence times the query heads that share the head (row i is token
+// One block takes a tile of 16 kR query rows of one key head: n tokens of one
+// sequence times the query heads that share the head (row i is token
 // i / heads, head i % heads), so every key and value row is read once for all
 // of them. The block walks the keys that any of its rows sees in tiles of 64,
 // with the running maximum and sum of each row:
@@ -12,50 +12,45 @@
 //
 // in powers of two (log2 e is folded into the scale).
 //
-// Bound: FMA issue (2 D multiply-adds per row and key). 256 threads hold a
-// 4 x 4 block of scores each and then 4 rows by D / 16 widths of the result:
-// 16 multiply-adds per two 16-byte shared-memory reads.
+// Bound: FMA issue (2 D multiply-adds per row and key) for long prompts, the
+// chain of one tile after another for short ones. 256 threads hold a kR x 4
+// block of scores each and then kR rows by D / 16 widths of the result; with
+// kR = 4 that is 64 multiply-adds per eight 16-byte shared-memory reads. The
+// next tile is copied while this one is computed.
+#include <algorithm>
+#include <mutex>
+
 #include "attn.cuh"
 
 namespace mxfp4el {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowsTile = 64;     // query rows per block
 constexpr int kKeysTile = 64;     // keys per step
 
-template <typename Tok>
-__device__ __forceinline__ float4 load4(const Tok* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                            *reinterpret_cast<const uint32_t*>(&b));
-}
-
-template <int D>
+template <int D, int kR>
 struct Smem {
-  float q[kRowsTile][D + 4];       // row strides of D + 4: 16-byte reads of 8 rows hit all banks
-  float k[kKeysTile][D + 4];
-  float v[kKeysTile][D];
-  float p[kRowsTile][kKeysTile + 4];
+  float q[16 * kR][D + 4];         // row strides of D + 4: 16-byte reads of 8 rows hit all banks
+  float k[2][kKeysTile][D + 4];
+  float v[2][kKeysTile][D];
+  float p[16 * kR][kKeysTile + 4];
 };
 
-template <typename Tok, int D>
+// 16 bytes global -> shared without a register; zeros where !valid.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+
+template <int D, int kR>
 __global__ void __launch_bounds__(kThreads)
 attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tokens_tile) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  Smem<D>& sh = *reinterpret_cast<Smem<D>*>(smem_raw);
+  Smem<D, kR>& sh = *reinterpret_cast<Smem<D, kR>*>(smem_raw);
+  constexpr int kRowsTile = 16 * kR;
+  pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int kvh = blockIdx.y / head_blocks;
   const int h0 = kvh * a.group + (blockIdx.y % head_blocks) * heads_tile;  // first query head
@@ -77,18 +72,19 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     const int row = i / (D / 4), c = i % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows)
-      x = load4(static_cast<const Tok*>(a.q) + (int64_t)(r.first + t0 + row / nh) * a.q_token +
-                (int64_t)(h0 + row % nh) * a.q_head + c);
+      x = __ldg(reinterpret_cast<const float4*>(
+          static_cast<const float*>(a.q) + (int64_t)(r.first + t0 + row / nh) * a.q_token +
+          (int64_t)(h0 + row % nh) * a.q_head + c));
     *reinterpret_cast<float4*>(&sh.q[row][c]) = x;
   }
 
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // 4 rows ty * 4.., keys tx + 16 j
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;  // rows ty * kR.., keys tx + 16 j
   const float scale = a.scale * kLog2e;
-  float m[4], l[4], o[4][D / 16];
-  int pos[4];
+  float m[kR], l[kR], o[kR][D / 16];
+  int pos[kR];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = ty * 4 + i;
+  for (int i = 0; i < kR; ++i) {
+    const int row = ty * kR + i;
     pos[i] = row < rows ? pos_lo + row / nh : -1;        // -1: sees nothing
     m[i] = -INFINITY;
     l[i] = 0.f;
@@ -99,46 +95,58 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
   // Keys any row of the tile sees: [0, sinks) and [first, last].
   const int last = min(pos_hi, r.len - 1);
   const int first = a.window ? max(0, pos_lo - a.window + 1) : 0;
-  for (int j0 = 0; j0 <= last; j0 += kKeysTile) {
-    if (j0 >= a.sinks && j0 + kKeysTile <= first) {       // between the sinks and the window
-      j0 = first / kKeysTile * kKeysTile - kKeysTile;
-      continue;
+  // The tiles that hold them, in order: the next one's first key.
+  auto next_tile = [&](int j0) {
+    j0 += kKeysTile;
+    return j0 >= a.sinks && j0 + kKeysTile <= first ? first / kKeysTile * kKeysTile : j0;
+  };
+  // Four threads copy a key's row and its value's; keys that no row sees and
+  // page ids out of range become zeros.
+  const int row = threadIdx.x >> 2;
+  auto copy_tile = [&](int j0, int buf) {
+    const int key = j0 + row;
+    const bool want = key <= last && (key >= first || key < a.sinks);
+    int64_t page = -1;
+    const int s = key & (a.cache.page_size - 1);
+    if (want) {
+      page = page_of(a.seqs, a.cache, b, key >> a.cache.page_shift);
+      if (page < 0 && (threadIdx.x & 3) == 0 && (s == 0 || row == 0))
+        atomicAdd(&a.status[kStatusBadPages], 1ull);
     }
-    __syncthreads();                                      // the last tile's readers are done
-    for (int i = threadIdx.x; i < kKeysTile * (D / 4); i += kThreads) {
-      const int j = i / (D / 4), c = i % (D / 4) * 4, key = j0 + j;
-      float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-      if (key <= last && (key >= first || key < a.sinks)) {
-        const int64_t page = page_of(a.seqs, a.cache, b, key >> a.cache.page_shift);
-        const int s = key & (a.cache.page_size - 1);
-        if (page >= 0) {
-          kx = load4(static_cast<const Tok*>(a.cache.k) + page * a.cache.k_page +
-                     kvh * a.cache.k_head + s * a.cache.k_slot + c);
-          vx = load4(static_cast<const Tok*>(a.cache.v) + page * a.cache.v_page +
-                     kvh * a.cache.v_head + s * a.cache.v_slot + c);
-        } else if (c == 0 && (s == 0 || j == 0) && a.status != nullptr) {
-          atomicAdd(&a.status[kStatusBadPages], 1ull);
-        }
-      }
-      *reinterpret_cast<float4*>(&sh.k[j][c]) = kx;
-      *reinterpret_cast<float4*>(&sh.v[j][c]) = vx;
+    const float* k = static_cast<const float*>(a.cache.k);
+    const float* v = static_cast<const float*>(a.cache.v);
+    if (page >= 0) {
+      k += page * a.cache.k_page + kvh * a.cache.k_head + s * a.cache.k_slot;
+      v += page * a.cache.v_page + kvh * a.cache.v_head + s * a.cache.v_slot;
     }
-    __syncthreads();
-
-    float s[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int c = (threadIdx.x & 3) * 4; c < D; c += 16) {
+      copy16(&sh.k[buf][row][c], k + (page >= 0 ? c : 0), page >= 0);
+      copy16(&sh.v[buf][row][c], v + (page >= 0 ? c : 0), page >= 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int j0 = next_tile(-kKeysTile), buf = 0;
+  if (j0 <= last) copy_tile(j0, 0);
+  for (; j0 <= last; j0 = next_tile(j0), buf ^= 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                   // this tile is there, the other buffer's readers are done
+    if (next_tile(j0) <= last) copy_tile(next_tile(j0), buf ^ 1);
+
+    float s[kR][4];
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      float4 qx[4], kx[4];
+      float4 qx[kR], kx[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) qx[i] = *reinterpret_cast<const float4*>(&sh.q[ty * 4 + i][c]);
+      for (int i = 0; i < kR; ++i) qx[i] = *reinterpret_cast<const float4*>(&sh.q[ty * kR + i][c]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4*>(&sh.k[tx + 16 * j][c]);
+      for (int j = 0; j < 4; ++j) kx[j] = *reinterpret_cast<const float4*>(&sh.k[buf][tx + 16 * j][c]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kR; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           s[i][j] = fmaf(qx[i].x, kx[j].x, s[i][j]);
@@ -154,7 +162,7 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     const bool whole = rows == kRowsTile && j0 + kKeysTile - 1 <= pos_lo &&
                        (a.window == 0 || pos_hi - j0 < a.window);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       float top = m[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -177,7 +185,7 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
         const bool hidden = !whole && !(key <= last && key_visible(key, pos[i], a.window, a.sinks));
         if (!hidden) sum += p;
         else p = -1.f;
-        sh.p[ty * 4 + i][tx + 16 * j] = p;
+        sh.p[ty * kR + i][tx + 16 * j] = p;
       }
 #pragma unroll
       for (int off = 8; off >= 1; off >>= 1) sum += __shfl_xor_sync(kFullMask, sum, off);
@@ -189,16 +197,16 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     __syncwarp();                                         // a row's p stays in its half warp
 #pragma unroll 2
     for (int j = 0; j < kKeysTile; j += 4) {
-      float4 px[4];
+      float4 px[kR];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) px[i] = *reinterpret_cast<const float4*>(&sh.p[ty * 4 + i][j]);
+      for (int i = 0; i < kR; ++i) px[i] = *reinterpret_cast<const float4*>(&sh.p[ty * kR + i][j]);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
 #pragma unroll
         for (int d = 0; d < D / 64; ++d) {
-          const float4 vx = *reinterpret_cast<const float4*>(&sh.v[j + jj][d * 64 + tx * 4]);
+          const float4 vx = *reinterpret_cast<const float4*>(&sh.v[buf][j + jj][d * 64 + tx * 4]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < kR; ++i) {
             const float p = jj == 0 ? px[i].x : jj == 1 ? px[i].y : jj == 2 ? px[i].z : px[i].w;
             if (whole || p >= 0.f || p != p) {
               o[i][4 * d + 0] = fmaf(p, vx.x, o[i][4 * d + 0]);
@@ -213,8 +221,8 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
   }
 
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = ty * 4 + i;
+  for (int i = 0; i < kR; ++i) {
+    const int row = ty * kR + i;
     if (row >= rows) continue;
     const int h = h0 + row % nh;
     float total = l[i], f = 1.f;
@@ -225,39 +233,49 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
       total = total * f + exp2_approx(z - base);
     }
     const float inv = total == 0.f ? 0.f : f / total;
-    Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(r.first + t0 + row / nh) * a.heads + h) * D;
+    float* out = static_cast<float*>(a.out) + ((int64_t)(r.first + t0 + row / nh) * a.heads + h) * D;
 #pragma unroll
     for (int d = 0; d < D / 64; ++d)
-      store4(out + d * 64 + tx * 4, make_float4(o[i][4 * d] * inv, o[i][4 * d + 1] * inv,
-                                                o[i][4 * d + 2] * inv, o[i][4 * d + 3] * inv));
+      *reinterpret_cast<float4*>(out + d * 64 + tx * 4) =
+          make_float4(o[i][4 * d] * inv, o[i][4 * d + 1] * inv, o[i][4 * d + 2] * inv,
+                      o[i][4 * d + 3] * inv);
   }
 }
 
-template <typename Tok, int D>
+template <int D, int kR>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  const int heads_tile = a.group < kRowsTile ? a.group : kRowsTile;
+  const int heads_tile = std::min(a.group, 16 * kR);
   const int head_blocks = (a.group + heads_tile - 1) / heads_tile;
-  const int tokens_tile = kRowsTile / heads_tile;
+  const int tokens_tile = 16 * kR / heads_tile;
   const dim3 grid((unsigned)query_tile_slots(a.seqs, a.T, tokens_tile),
                   (unsigned)(a.cache.kv_heads * head_blocks));
-  const int smem = (int)sizeof(Smem<D>);
-  cudaError_t err = cudaFuncSetAttribute(attention_simt_kernel<Tok, D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = (int)sizeof(Smem<D, kR>);
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t err = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    err = cudaFuncSetAttribute(attention_simt_kernel<D, kR>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
   if (err != cudaSuccess) return err;
-  attention_simt_kernel<Tok, D><<<grid, kThreads, smem, stream>>>(a, heads_tile, head_blocks,
-                                                                 tokens_tile);
-  err = cudaGetLastError();
-  if (err == cudaSuccess) note_launch();
-  return err;
+  return launch_after_previous(attention_simt_kernel<D, kR>, grid, dim3(kThreads), smem, stream, a,
+                               heads_tile, head_blocks, tokens_tile);
+}
+
+// Tiles of 64 rows, or of 32 where 64 would leave SMs without a second block
+// to hide the first one's waits behind.
+template <int D>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.T * a.heads;
+  return rows >= 2 * 64 * (int64_t)attention_num_sms() ? launch<D, 4>(a, stream)
+                                                       : launch<D, 2>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream) {
-  if (a.cache.token_dtype == kTokenBF16)
-    return a.cache.head_dim == 64 ? launch<__nv_bfloat16, 64>(a, stream)
-                                  : launch<__nv_bfloat16, 128>(a, stream);
-  return a.cache.head_dim == 64 ? launch<float, 64>(a, stream) : launch<float, 128>(a, stream);
+  return a.cache.head_dim == 64 ? launch_rows<64>(a, stream) : launch_rows<128>(a, stream);
 }
 
 }  // namespace mxfp4el
