@@ -102,6 +102,7 @@ class PagedSequences:
             raise ValueError("page_table, seq_lens and q_offsets do not match")
         self.page_table, self.seq_lens, self.q_offsets = page_table, seq_lens, q_offsets
         self.device, self.num_seqs = page_table.device, n
+        self._index = page_table.device.index
         self._c = _native.Sequences(
             page_table.data_ptr(), seq_lens.data_ptr(),
             q_offsets.data_ptr() if q_offsets is not None else None,
@@ -109,33 +110,27 @@ class PagedSequences:
         self._address = ctypes.addressof(self._c)
 
 
-def _check_rows(name: str, t: torch.Tensor, cache: PagedKVCache, heads: int | None = None):
-    """The shape and strides of a (tokens, heads, head_dim) tensor."""
-    shape, stride = t.shape, t.stride()
+# The calls below are short next to what Python spends on them, so their
+# checks are written out in one place each, and what they refuse is worked out
+# only then.
+def _refuse_rows(name: str, t: torch.Tensor, cache: PagedKVCache, heads: int | None = None):
     if t.dtype != cache.dtype:
         raise TypeError(f"{name} must have the cache's dtype {cache.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
-    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads):
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be (tokens, heads, {cache.head_dim})")
-    if stride[2] != 1:
-        raise ValueError(f"the rows of {name} must be contiguous")
-    return shape, stride
+    raise ValueError(f"the rows of {name} must be contiguous")
 
 
-def _check_out(name: str, out: torch.Tensor | None, q: torch.Tensor) -> torch.Tensor:
-    if out is None:
-        return torch.empty_like(q) if q.is_contiguous() else \
-            torch.empty(q.shape, dtype=q.dtype, device=q.device)
+def _check_out(name: str, out: torch.Tensor, q: torch.Tensor) -> None:
     if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device \
             or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of q's shape, dtype and device")
-    return out
 
 
-def _call(name: str, cache: PagedKVCache, args: tuple) -> None:
+def _call(f, name: str, cache: PagedKVCache, args: tuple) -> None:
     """One library call on the cache's device, the current stream last."""
-    f = getattr(_native.load(), name)
     index = cache._index
     if _current_device() == index:
         rc = f(*args, _raw_stream(index))
@@ -161,32 +156,43 @@ def append_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVC
     (head_dim) in the cache's dtype weigh an RMS norm of each head's row.
     See mxfp4el_append_kv in the C header.
     """
-    shape, qs = _check_rows("q", q, cache)
-    kshape, ks = _check_rows("k", k, cache, cache.num_kv_heads)
-    vshape, vs = _check_rows("v", v, cache, cache.num_kv_heads)
+    dtype, index, dim, kv_heads = cache.dtype, cache._index, cache.head_dim, cache.num_kv_heads
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    shape, kshape = q.shape, k.shape
+    if q.dtype is not dtype or q.get_device() != index or len(shape) != 3 or shape[2] != dim \
+            or qs[2] != 1:
+        _refuse_rows("q", q, cache)
+    if k.dtype is not dtype or k.get_device() != index or len(kshape) != 3 \
+            or kshape[1] != kv_heads or kshape[2] != dim or ks[2] != 1:
+        _refuse_rows("k", k, cache, kv_heads)
     T = shape[0]
-    if kshape[0] != T or vshape[0] != T:
+    if kshape[0] != T or v.shape[0] != T:
         raise ValueError("q, k and v must have the same number of tokens")
-    if seqs.device != cache.device:
+    if v.dtype is not dtype or v.get_device() != index or v.shape != kshape or vs[2] != 1:
+        _refuse_rows("v", v, cache, kv_heads)
+    if seqs._index != index:
         raise ValueError(f"the sequences are on {seqs.device}, the cache on {cache.device}")
     if seqs.q_offsets is None and seqs.num_seqs != T:
         raise ValueError("without q_offsets there is one token per sequence")
-    for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-        if w is not None and (w.dtype != cache.dtype or w.device != cache.device
-                              or w.shape != (cache.head_dim,) or not w.is_contiguous()):
-            raise ValueError(f"{name} must be ({cache.head_dim},) in the cache's dtype and device")
+    for w in (q_norm, k_norm):
+        if w is not None and (w.dtype is not dtype or w.get_device() != index
+                              or w.shape != (dim,) or not w.is_contiguous()):
+            raise ValueError(f"q_norm and k_norm must be ({dim},) in the cache's dtype, on its device")
     positions = rotary = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.device != cache.device \
+        if cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index \
                 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous (max_positions, rotary_dim) float32 "
                              "tensor on the cache's device")
         positions, rotary = cos_sin.shape
-        if rotary % 16 or not 0 < rotary <= cache.head_dim:
+        if rotary % 16 or not 0 < rotary <= dim:
             raise ValueError("rotary_dim must be a multiple of 16 up to head_dim")
-    q_out = _check_out("q_out", q_out, q)
+    if q_out is not None:
+        _check_out("q_out", q_out, q)
+    else:
+        q_out = torch.empty(shape, dtype=dtype, device=cache.device)
     if T:
-        _call("mxfp4el_append_kv", cache, (
+        _call(_native.load().mxfp4el_append_kv, "append_kv", cache, (
             q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
             None if q_norm is None else q_norm.data_ptr(),
             None if k_norm is None else k_norm.data_ptr(), eps,
@@ -209,24 +215,25 @@ def attention_workspace(device=None) -> torch.Tensor:
 _workspaces: dict[tuple[int, int], torch.Tensor] = {}
 
 
-def _workspace_of(cache: PagedKVCache) -> torch.Tensor:
-    key = (cache._index, _raw_stream(cache._index))
-    ws = _workspaces.get(key)
-    if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("pass a workspace (attention_workspace) while a graph is captured, "
-                               "or make a first call on this stream before the capture")
-        with torch.cuda.device(cache.device):
-            ws = _workspaces[key] = attention_workspace(cache.device)
+def _new_workspace(cache: PagedKVCache) -> torch.Tensor:
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError("pass a workspace (attention_workspace) while a graph is captured, "
+                           "or make a first call on this stream before the capture")
+    with torch.cuda.device(cache.device):
+        ws = attention_workspace(cache.device)
+    _workspaces[(cache._index, _raw_stream(cache._index))] = ws
     return ws
 
 
-def _attention(name, q, cache, seqs, scale, window, sinks, sink_logits, out, workspace):
-    shape, qs = _check_rows("q", q, cache)
+def _attention(decode, q, cache, seqs, scale, window, sinks, sink_logits, out, workspace):
+    shape, stride, index = q.shape, q.stride(), cache._index
+    if q.dtype is not cache.dtype or q.get_device() != index or len(shape) != 3 \
+            or shape[2] != cache.head_dim or stride[2] != 1:
+        _refuse_rows("q", q, cache)
     T, heads, dim = shape
     if heads == 0 or heads % cache.num_kv_heads:
         raise ValueError("the number of query heads must be a multiple of the cache's heads")
-    if seqs.device != cache.device:
+    if seqs._index != index:
         raise ValueError(f"the sequences are on {seqs.device}, the cache on {cache.device}")
     if seqs.q_offsets is None and seqs.num_seqs != T:
         raise ValueError("without q_offsets there is one token per sequence")
@@ -234,18 +241,30 @@ def _attention(name, q, cache, seqs, scale, window, sinks, sink_logits, out, wor
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
     if sink_logits is not None and (
-            sink_logits.dtype != torch.float32 or sink_logits.device != cache.device
+            sink_logits.dtype is not torch.float32 or sink_logits.get_device() != index
             or sink_logits.shape != (heads,) or not sink_logits.is_contiguous()):
         raise ValueError("sink_logits must be a (heads,) float32 tensor on the cache's device")
-    out = _check_out("out", out, q)
+    if out is not None:
+        _check_out("out", out, q)
+    elif stride[1] == dim and stride[0] == heads * dim:
+        out = torch.empty_like(q)
+    else:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if T:
-        ws = _workspace_of(cache) if workspace is None else workspace
-        rows = (heads,) if name == "mxfp4el_attention_decode" else (T, heads)
-        _call(name, cache, (
-            q.data_ptr(), qs[0], qs[1], cache._address, seqs._address,
-            dim ** -0.5 if scale is None else scale, window, sinks,
-            None if sink_logits is None else sink_logits.data_ptr(), out.data_ptr(), *rows,
-            ws.data_ptr(), ws.numel()))
+        if workspace is None:
+            workspace = _workspaces.get((index, _raw_stream(index)))
+            if workspace is None:
+                workspace = _new_workspace(cache)
+        args = (q.data_ptr(), stride[0], stride[1], cache._address, seqs._address,
+                dim ** -0.5 if scale is None else scale, window, sinks,
+                None if sink_logits is None else sink_logits.data_ptr(), out.data_ptr())
+        lib = _native.load()
+        if decode:
+            _call(lib.mxfp4el_attention_decode, "paged_attention_decode", cache,
+                  args + (heads, workspace.data_ptr(), workspace.numel()))
+        else:
+            _call(lib.mxfp4el_attention_prefill, "paged_attention_prefill", cache,
+                  args + (T, heads, workspace.data_ptr(), workspace.numel()))
     return out
 
 
@@ -268,7 +287,7 @@ def paged_attention_decode(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSequ
     if seqs.q_offsets is not None:
         raise ValueError("decode takes one token per sequence: leave q_offsets out, or use "
                          "paged_attention_prefill")
-    return _attention("mxfp4el_attention_decode", q, cache, seqs, scale, window, sinks, sink_logits,
+    return _attention(True, q, cache, seqs, scale, window, sinks, sink_logits,
                       out, workspace)
 
 
@@ -284,7 +303,7 @@ def paged_attention_prefill(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSeq
     the cache, behind any history. Arguments otherwise as
     :func:`paged_attention_decode`.
     """
-    return _attention("mxfp4el_attention_prefill", q, cache, seqs, scale, window, sinks,
+    return _attention(False, q, cache, seqs, scale, window, sinks,
                       sink_logits, out, workspace)
 
 
