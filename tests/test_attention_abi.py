@@ -106,3 +106,9 @@ def test_append_checks(lib):
 def test_page_errors_needs_somewhere_to_write(lib):
     from mxfp4_routed_expert_route_gb300 import _native as n
     assert lib.mxfp4el_page_errors(None, None) == n.ERR_INVALID_ARGUMENT
+
+
+def test_scale_is_positive(lib):
+    from mxfp4_routed_expert_route_gb300 import _native as n
+    for scale in (0.0, -0.125):
+        assert _prefill(lib, _cache(n), _seqs(n), scale=scale) == n.ERR_INVALID_ARGUMENT

@@ -513,3 +513,53 @@ def test_refusals():
         lib.PagedSequences(d["table"].long(), d["seq_lens"])
     with pytest.raises(ValueError):
         lib.PagedSequences(d["table"], d["seq_lens"][:1])
+
+
+# ------------------------------------------------------- many sequences ----
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("seqs", [30, 31, 100, 700])
+def test_prefill_many_sequences(dtype, seqs):
+    # Prompts and chunks of 0 to 40 new tokens behind histories of 0 to 60.
+    new = [(13 * i) % 41 for i in range(seqs)]
+    lens = [n + (29 * i) % 61 for i, n in enumerate(new)]
+    d = make(lens, new, heads=4, kv_heads=2, dtype=dtype, fill=math.nan)
+    check(d, False)
+    check(d, False, logits=True, window=20, sinks=3)
+
+
+def test_prefill_many_sequences_of_one_token():
+    lens = [1 + (37 * i) % 301 for i in range(90)]
+    d = make(lens, [1] * 90, heads=6, kv_heads=2, fill=math.nan)
+    want = check(d, False)
+    seqs = lib.PagedSequences(d["table"], d["seq_lens"])
+    assert torch.equal(lib.paged_attention_prefill(d["q"], d["cache"], seqs), want)
+
+
+def test_decode_more_sequences_than_a_launch_takes():
+    lens = [(41 * i) % 97 for i in range(2500)]
+    d = make(lens, [1] * 2500, heads=2, kv_heads=1, page=32, spare=1)
+    got = call(d, True)
+    for b0 in (0, 1000, 2400):      # the 64-bit form of a few stretches
+        part = dict(d, q=d["q"][b0:b0 + 100], table=d["table"][b0:b0 + 100],
+                    lens=lens[b0:b0 + 100], offsets=list(range(101)))
+        want, bound = ref.attention(part["q"], d["kp"], d["vp"], part["table"], part["lens"],
+                                    part["offsets"])
+        assert ((got[b0:b0 + 100].double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("decode", [True, False])
+def test_calls_in_a_row_do_not_disturb_each_other(dtype, decode):
+    # Different inputs through one workspace, nothing waited for between.
+    cases = [make([900 + 300 * i, 40, 2000 - 100 * i], [1] * 3 if decode else [30 + i, 40, 9],
+                  dim=64 if i % 2 else 128, dtype=dtype, seed=i, fill=math.nan) for i in range(4)]
+    kw = dict(window=150, sinks=5)
+    want = [(call(d, decode), call(d, decode, **kw)) for d in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(25):
+        got.append([(call(d, decode), call(d, decode, **kw)) for d in cases])
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert lib.wait_timeouts() == 0
