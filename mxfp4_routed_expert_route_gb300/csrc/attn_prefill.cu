@@ -208,6 +208,20 @@ __device__ __forceinline__ int page_id(const PrefillArgs& p, const Unit& u, int 
   return id;
 }
 
+// 32 bytes at p: at once where p allows it. A thread's rows lie apart, so each
+// store instruction touches 32 rows, and their number is what the epilogue
+// costs.
+__device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t* w) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *(reinterpret_cast<uint4*>(p) + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // Whether the row at position pos may see a key of [bad_lo, bad_hi].
 __device__ __forceinline__ bool may_see(const AttnArgs& a, int pos, int bad_lo, int bad_hi) {
   return bad_lo <= min(bad_hi, pos) &&
@@ -519,14 +533,12 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           tmem_ld32(o_addr + 32 * q, o);
           tmem_wait_ld();
           if (write && !again) {
+            uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = l == 0.f ? 0u : pack_bf16(o[8 * j + 2 * e] * inv, o[8 * j + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(out + 32 * q + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int j = 0; j < 16; ++j)
+              w[j] = l == 0.f ? 0u : pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
+            store32(out + 32 * q, w);
+            store32(out + 32 * q + 16, w + 8);
           }
         }
         tc_fence_before_sync();
