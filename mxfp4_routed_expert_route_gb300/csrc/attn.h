@@ -63,8 +63,15 @@ struct AttnArgs {
 // One new token of each sequence, split over the cache's length and joined
 // through the workspace (attn_decode.cu).
 cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream);
-size_t decode_workspace_bytes();
-size_t decode_counter_bytes();     // the prefill kernel's counters follow them
+
+// The workspace of an attention call: the decode kernel's counters, the
+// prefill kernels' (all zero between calls), and the pieces of split work.
+constexpr int kDecodeCounters = 256, kPrefillCounters = 768;
+constexpr size_t kPiecesBytes = (size_t)36 << 20;
+inline unsigned int* decode_counters(void* ws) { return static_cast<unsigned int*>(ws); }
+inline unsigned int* prefill_counters(void* ws) { return decode_counters(ws) + kDecodeCounters; }
+inline void* workspace_pieces(void* ws) { return prefill_counters(ws) + kPrefillCounters; }
+constexpr size_t kAttentionWorkspaceBytes = (kDecodeCounters + kPrefillCounters) * 4 + kPiecesBytes;
 
 // bf16 prompts on the tensor cores (attn_prefill.cu).
 cudaError_t launch_attention_prefill(const AttnArgs& a, void* workspace, cudaStream_t stream);
@@ -74,6 +81,6 @@ bool kv_tensor_map(const KvCacheView& c, bool values, int box_rows, int box_subs
 int attention_num_sms();
 
 // float32 prompts, on the CUDA cores (attn_simt.cu).
-cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attention_simt(const AttnArgs& a, void* workspace, cudaStream_t stream);
 
 }  // namespace mxfp4el

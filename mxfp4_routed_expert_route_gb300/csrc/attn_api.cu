@@ -114,6 +114,9 @@ int check_attention(const void* q, int64_t q_token, int64_t q_head, const mxfp4e
     return MXFP4EL_ERR_TOO_LARGE;
   rc = check_sequences(seqs, T, &a->seqs);
   if (rc != MXFP4EL_OK) return rc;
+  // The prefill kernels count (query tile, key head) units in 31 bits, with
+  // room for the grid past the last.
+  if ((T + seqs->num_seqs + 1) * a->cache.kv_heads > kMaxDim - (1 << 20)) return MXFP4EL_ERR_TOO_LARGE;
   if (T == 0) {
     *nothing = true;
     return MXFP4EL_OK;
@@ -215,7 +218,7 @@ extern "C" int mxfp4el_append_kv(const void* q, int64_t q_token_stride, int64_t 
              : MXFP4EL_ERR_CUDA;
 }
 
-extern "C" size_t mxfp4el_attention_workspace_size(void) { return decode_workspace_bytes(); }
+extern "C" size_t mxfp4el_attention_workspace_size(void) { return kAttentionWorkspaceBytes; }
 
 extern "C" int mxfp4el_attention_decode(const void* q, int64_t q_token_stride,
                                         int64_t q_head_stride, const mxfp4el_kv_cache* cache,
@@ -251,7 +254,7 @@ extern "C" int mxfp4el_attention_prefill(const void* q, int64_t q_token_stride,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t err = a.cache.token_dtype == kTokenBF16
                               ? launch_attention_prefill(a, workspace, s)
-                              : launch_attention_simt(a, s);
+                              : launch_attention_simt(a, workspace, s);
   return err == cudaSuccess ? MXFP4EL_OK : MXFP4EL_ERR_CUDA;
 }
 

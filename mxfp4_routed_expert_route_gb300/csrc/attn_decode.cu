@@ -52,8 +52,7 @@ constexpr int kQSlots = 2;
 
 // Bytes of a piece in the workspace: rows of o (128 floats), m and l.
 constexpr size_t kPieceBytes = (size_t)kRowsMax * 128 * 4 + 2 * kRowsMax * 4;
-// The workspace: this kernel's counters, the prefill kernel's, the pieces.
-constexpr size_t kCounterBytes = (size_t)kMaxCtas * 4, kPiecesAt = kCounterBytes + 256;
+static_assert(kMaxCtas <= kDecodeCounters && 2 * kMaxCtas * kPieceBytes <= kPiecesBytes, "workspace");
 
 template <typename Tok, int D, int kMT = 1, int kH = 16>
 struct Shape {
@@ -786,8 +785,8 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   d.units_per_seq = a.cache.kv_heads * d.head_blocks;
   d.box_rows = std::min(a.cache.page_size, S::kTile);
   while ((1 << d.box_shift) < d.box_rows) ++d.box_shift;
-  d.counters = static_cast<unsigned int*>(workspace);
-  d.pieces = static_cast<unsigned char*>(workspace) + kPiecesAt;
+  d.counters = decode_counters(workspace);
+  d.pieces = static_cast<unsigned char*>(workspace_pieces(workspace));
   DecodeMaps maps;
   if (!kv_tensor_map(a.cache, false, d.box_rows, S::kSubs, &maps.k) ||
       !kv_tensor_map(a.cache, true, d.box_rows, S::kSubs, &maps.v))
@@ -876,9 +875,6 @@ int attention_num_sms() {
   }
   return cached[dev];
 }
-
-size_t decode_counter_bytes() { return kCounterBytes; }
-size_t decode_workspace_bytes() { return kPiecesAt + 2 * (size_t)kMaxCtas * kPieceBytes; }
 
 cudaError_t launch_attention_decode(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   if (a.cache.token_dtype == kTokenBF16)

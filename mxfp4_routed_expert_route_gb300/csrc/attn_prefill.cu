@@ -19,24 +19,33 @@
 // other's softmax runs.
 //
 // Warps of a CTA (one CTA per SM, units from a counter, the longest first):
-//   0-3, 4-7  softmax and epilogue of tile 0 and of tile 1: one thread per
-//             row, so row maxima and sums need no exchange between threads.
-//             O is rescaled only when a row's maximum grew by more than 8
-//             (2^8 fits every format here); the stale maximum is as good a
+//   0-7, 8-15 softmax and epilogue of row tile 0 and of row tile 1: two
+//             threads per row, half of the keys each, which exchange maxima.
+//             (One thread per row, with nothing to exchange: the same for long
+//             prompts, 8192 tokens 733 against 720 us, and more than twice as
+//             long for a window of 128, whose chain of steps is what counts.)
+//             O is rescaled only when a row's maximum grew by more than 2^8,
+//             which fits every format here; the stale maximum is as good a
 //             base for the powers as the true one.
-//   8         takes units, copies queries, keys and values
-//   9         issues the matrix instructions
-//   10        values of key tiles that the mask cuts: rows that no query sees
+//   16        copies queries, keys and values
+//   17        issues the matrix instructions
+//   18        values of key tiles that the mask cuts: rows that no query sees
 //             are zeroed (a masked score gives P = 0, but 0 times what a stale
 //             page holds need not be 0), and so are infinities and NaN.
+//   19        takes units and looks up their rows and first pages
 // A value that is not finite must reach the rows that see it and no other,
 // which a matrix product cannot do in a tile that the mask cuts: there it
-// counts as zero, and warp 10 computes the rows that may see it by itself, on
+// counts as zero, and warp 18 computes the rows that may see it by itself, on
 // the CUDA cores; the epilogue leaves them out.
 //
 // P and the sum l: P is rounded to bf16 for the second product (a relative
 // error of 2^-8 at most, as the result's own rounding); l adds the float32
 // values.
+//
+// Few rows: where the units are at most half as many as the SMs (and the
+// sequences few), the keys of each are split over several CTAs. Each leaves
+// (m, l, O) of its rows in the workspace, and the last to arrive joins them in
+// their order along the keys.
 //
 // Every wait is bounded. A role whose wait gives up records it and goes on
 // without waiting, so that every role ends.
@@ -66,6 +75,9 @@ constexpr int kFewSeqs = 30;            // sequences that the unit warp keeps in
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
 constexpr float kRescale = 8.f;
+// A join reads every part's 128 rows of O, about what a key tile costs: with n
+// key tiles sqrt(n) parts leave sqrt(n) tiles and as many pieces to read.
+constexpr int kMaxParts = 32;           // one lane each
 
 template <int D>
 struct Shape {
@@ -85,9 +97,10 @@ struct PrefillArgs {
   AttnArgs a;
   int n;              // tokens per tile
   int box_rows, box_shift;
-  long long units;    // slots x key heads
+  int units;          // slots x key heads
   int slots;
-  unsigned int* counter;   // next unit; counter[1]: CTAs that are done
+  unsigned int* counter;   // next unit; [1]: CTAs that are done; then one per unit and row tile
+  float* pieces;           // per (unit part, row tile): 128 rows of O, then their m c and l
 };
 
 struct Unit {
@@ -98,7 +111,10 @@ struct Unit {
   int lo;             // first key of the first token's window
   int start;          // first key of the first window tile
   int sinks;          // keys below this are seen beside the window
-  int sink_tiles, tiles[2];     // key tiles for each row tile (tiles[1] >= tiles[0])
+  int sink_tiles;
+  int i0, tiles[2];   // key tiles [i0, tiles[t]) for row tile t (tiles[1] >= tiles[0])
+  int parts, piece;   // CTAs that share the unit; this one's piece
+  int first_piece, id;   // the first one's piece; the unit's number
 };
 
 template <int D>
@@ -109,6 +125,7 @@ struct __align__(16) PrefillShared {
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
   uint32_t tmem_base;
+  int joins[2];
   int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
   Unit unit[kUnitRing];
   int first_ids[kUnitRing][16];              // pages of the unit's first key tile
@@ -222,6 +239,20 @@ __device__ __forceinline__ void store32(__nv_bfloat16* p, const uint32_t* w) {
   }
 }
 
+// 1 / (l + e^(sink - m)) in the scale of m (a power of two's exponent), for a
+// row with running maximum m and sum l: out = o * that.
+__device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, float l) {
+  if (l == 0.f) return 0.f;
+  float f = 1.f;
+  if (a.sink_logits != nullptr) {
+    const float z = __ldg(a.sink_logits + head) * kLog2e;
+    const float top = fmaxf(m, z), base = top == -INFINITY ? 0.f : top;
+    f = exp2_approx(m - base);
+    l = l * f + exp2_approx(z - base);
+  }
+  return f / l;
+}
+
 // Whether the row at position pos may see a key of [bad_lo, bad_hi].
 __device__ __forceinline__ bool may_see(const AttnArgs& a, int pos, int bad_lo, int bad_hi) {
   return bad_lo <= min(bad_hi, pos) &&
@@ -302,10 +333,12 @@ __device__ __forceinline__ void slow_row(const AttnArgs& a, const Unit& u, int t
   for (int e = 0; e < kE; ++e) out[32 * e] = __float2bfloat16_rn(o[e] * inv);
 }
 
-template <int D>
+// kSplit: units may be shared by several CTAs.
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const PrefillArgs p) {
   using S = Shape<D>;
+  constexpr size_t kPieceFloats = (size_t)kRows * (D + 2);
   // Tiles start on 1024-byte boundaries (the swizzle's), and there is no room
   // to move up to one.
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -378,6 +411,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       const Unit u = sh.unit[slot];
       if (u.seq < 0) break;
       const int tiles = u.tiles[t];
+      const bool write = in_tile && tok < u.nt;
       const int pos = u.pos0 + min(tok, u.nt - 1);
       const int pos_first = u.pos0 + min(tok_first, u.nt - 1);
       const int pos_last = u.pos0 + min(tok_last, u.nt - 1);
@@ -388,7 +422,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       float m = -INFINITY, l = 0.f, mc = 0.f;     // mc: -m c, or 0 while m is -infinity
 
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i) {
+      for (int i = u.i0; i < tiles; ++i) {
         if (ok) ok = mbar_wait_warp(&sh.s_full[t], s_phase);
         s_phase ^= 1u;
         tc_fence_after_sync();
@@ -444,7 +478,8 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         bar_sync(1 + t, 256);
         tc_fence_after_sync();
         const float top = max3(m, mine, sh.row_max[t][half ^ 1][row]);
-        if (__any_sync(kFullMask, (top - m) * c > kRescale)) {
+        // (Rows that hold no token hold anything: they have no say.)
+        if (__any_sync(kFullMask, write && (top - m) * c > kRescale)) {
           // A maximum grew by more than kRescale (or was -infinity): O and l
           // move to the new base. O's last product is done: S was issued after
           // it.
@@ -453,7 +488,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           l *= keep;
           m = top;
           mc = m == -INFINITY ? 0.f : -m * c;
-          if (i > 0) {
+          if (i > u.i0) {
 #pragma unroll 1
             for (int q = 0; q < D / 2; q += 16) {
               uint32_t o[16];
@@ -498,11 +533,10 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         if (lane == 0) mbar_arrive(&sh.p_full[t]);
       }
 
-      const bool write = in_tile && tok < u.nt;
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                            ((int64_t)(u.row0 + tok) * a.heads + u.kvh * a.group + head) * D +
                            half * (D / 2);
-      if (tiles > 0) {
+      if (tiles > u.i0) {
         // The halves' sums, in an array of their own where there is room, else
         // after the last tile's maxima have been read and before the next
         // unit's are written.
@@ -513,40 +547,119 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         bar_sync(1 + t, 256);
         l += sums[half ^ 1][row];
         if (D != 64) bar_sync(1 + t, 256);
-        float total = l, f = 1.f;
-        if (a.sink_logits != nullptr) {
-          const float z = __ldg(a.sink_logits + u.kvh * a.group + head) * kLog2e;
-          const float ms = m * c, top = fmaxf(ms, z), base = top == -INFINITY ? 0.f : top;
-          f = exp2_approx(ms - base);
-          total = l * f + exp2_approx(z - base);
-        }
-        const float inv = l == 0.f ? 0.f : f / total;
+        const float inv = finish(a, u.kvh * a.group + head, m * c, l);
         ok = ok && mbar_wait_warp(&sh.o_full[t], o_phase);
         o_phase ^= 1u;
         tc_fence_after_sync();
         const int bad_lo = *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]);
         const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
         const bool again = may_see(a, pos, bad_lo, bad_hi);
+        if (!kSplit || u.parts == 1) {
 #pragma unroll
-        for (int q = 0; q < D / 64; ++q) {
-          float o[32];
-          tmem_ld32(o_addr + 32 * q, o);
-          tmem_wait_ld();
-          if (write && !again) {
-            uint32_t w[16];
+          for (int q = 0; q < D / 64; ++q) {
+            float o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_wait_ld();
+            if (write && !again) {
+              uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = l == 0.f ? 0u : pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
-            store32(out + 32 * q, w);
-            store32(out + 32 * q + 16, w + 8);
+              for (int j = 0; j < 16; ++j)
+                w[j] = l == 0.f ? 0u : pack_bf16(o[2 * j] * inv, o[2 * j + 1] * inv);
+              store32(out + 32 * q, w);
+              store32(out + 32 * q + 16, w + 8);
+            }
+          }
+        } else {
+          float* piece = p.pieces + (size_t)(u.piece * 2 + t) * kPieceFloats;
+#pragma unroll 1
+          for (int q = 0; q < D / 64; ++q) {
+            float o[32];
+            tmem_ld32(o_addr + 32 * q, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(piece + (size_t)row * D + half * (D / 2) + 32 * q + j) =
+                  make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+          if (half == 0) {
+            piece[kRows * D + row] = m * c;
+            piece[kRows * D + kRows + row] = again ? -1.f : l;     // -1: warp 18 computes the row
           }
         }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+      } else if (kSplit && u.parts > 1) {
+        if (half == 0) {
+          float* stats = p.pieces + (size_t)(u.piece * 2 + t) * kPieceFloats + kRows * D + row;
+          stats[0] = -INFINITY;
+          stats[kRows] = 0.f;
+        }
       } else if (write) {
         for (int j = 0; j < D / 16; ++j)
           *reinterpret_cast<uint4*>(out + 8 * j) = make_uint4(0, 0, 0, 0);
+      }
+      if (kSplit && u.parts > 1) {
+        __threadfence();
+        bar_sync(1 + t, 256);
+        if ((warp & 7) == 0 && lane == 0)
+          sh.joins[t] = atomicInc(p.counter + 2 + 2 * u.id + t, (unsigned)(u.parts - 1)) ==
+                        (unsigned)(u.parts - 1);
+        bar_sync(1 + t, 256);
+        if (sh.joins[t]) {
+          __threadfence();
+          // A warp per row, lane k with part k's m and l.
+          const float* first = p.pieces + (size_t)(u.first_piece * 2 + t) * kPieceFloats;
+          for (int r = warp & 7; r < p.n * a.group; r += 8) {
+            const int token = t * p.n + r / a.group, h = u.kvh * a.group + r % a.group;
+            if (token >= u.nt) break;
+            float mk = -INFINITY, lk = 0.f;
+            if (lane < u.parts) {
+              const float* stats = first + (size_t)lane * 2 * kPieceFloats + kRows * D + r;
+              mk = __ldcg(stats);
+              lk = __ldcg(stats + kRows);
+            }
+            float top = mk;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            const float f = exp2_approx(mk - (top == -INFINITY ? 0.f : top));
+            float total = lk * f;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
+            const bool skip = __any_sync(kFullMask, lk < 0.f);
+            const float inv = finish(a, h, top, total);
+            float o[D / 32] = {};
+#pragma unroll 4
+            for (int k = 0; k < u.parts; ++k) {
+              // A part that saw nothing has left no O.
+              const bool has = __shfl_sync(kFullMask, mk, k) != -INFINITY;
+              const float fk = __shfl_sync(kFullMask, f, k);
+              const float* x = first + (size_t)k * 2 * kPieceFloats + (size_t)r * D + lane * (D / 32);
+              if constexpr (D == 128) {
+                const float4 v = has ? __ldcg(reinterpret_cast<const float4*>(x))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                o[0] = fmaf(v.x, fk, o[0]);
+                o[1] = fmaf(v.y, fk, o[1]);
+                o[2] = fmaf(v.z, fk, o[2]);
+                o[3] = fmaf(v.w, fk, o[3]);
+              } else {
+                const float2 v = has ? __ldcg(reinterpret_cast<const float2*>(x))
+                                     : make_float2(0.f, 0.f);
+                o[0] = fmaf(v.x, fk, o[0]);
+                o[1] = fmaf(v.y, fk, o[1]);
+              }
+            }
+            if (!skip) {
+              uint32_t* to = reinterpret_cast<uint32_t*>(
+                  static_cast<__nv_bfloat16*>(a.out) +
+                  ((int64_t)(u.row0 + token) * a.heads + h) * D + lane * (D / 32));
+#pragma unroll
+              for (int e = 0; e < D / 64; ++e)
+                to[e] = total == 0.f ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
+            }
+          }
+        }
+        bar_sync(1 + t, 256);                          // joins has been read
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
@@ -568,7 +681,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
     const bool few = seqs <= kFewSeqs;
     SeqRows mine = {a.T, 0, 0, 0};                // lane r: the sequence of rank r
     int mine_seq = 0, before = 0, mine_tiles = 0; // query tiles of the sequences before it
-    long long units = p.units;
+    int units = p.units;
     if (few) {
       SeqRows r = mine;
       if (lane <= seqs)
@@ -591,18 +704,23 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         if (lane >= o) incl += up;
       }
       before = incl - mine_tiles;
-      units = (long long)__shfl_sync(kFullMask, incl, 31) * a.cache.kv_heads;
+      units = __shfl_sync(kFullMask, incl, 31) * a.cache.kv_heads;
     }
+    // Parts per unit, as far as the CTAs go round; index = unit * parts + part.
+    const int parts = kSplit && few && units > 0 && units <= (int)gridDim.x / 2 ? (int)gridDim.x / units : 1;
+    units *= parts;
     // Units published and not yet released, and their key tiles (lane s: ring
     // slot s's).
     int published = 0, released = 0, ahead = 0, slot_tiles = 0;
-    long long idx = blockIdx.x;
+    int idx = blockIdx.x;
     for (;;) {
       Unit u;
       u.seq = -1;
       if (idx < units) {
-        u.kvh = (int)(idx % a.cache.kv_heads);
-        const int s = (int)(idx / a.cache.kv_heads);
+        u.id = kSplit ? idx / parts : idx;
+        const int part = idx - u.id * parts;
+        const int s = u.id / a.cache.kv_heads;
+        u.kvh = u.id - s * a.cache.kv_heads;
         int tile;
         SeqRows r;
         if (few) {
@@ -634,14 +752,27 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         u.tiles[1] = u.hi > 0 ? u.sink_tiles + (u.hi - u.start + kKeys - 1) / kKeys : 0;
         u.tiles[0] = hi0 > 0 ? u.sink_tiles + (hi0 - u.start + kKeys - 1) / kKeys : 0;
         if (u.nt <= p.n) u.tiles[1] = 0;
+        u.parts = 1;
+        u.i0 = 0;
+        u.piece = idx;
+        u.first_piece = idx - part;
+        if (kSplit && parts > 1) {
+          const int all = max(u.tiles[0], u.tiles[1]);
+          u.parts = max(1, min(min(parts, kMaxParts), (int)sqrtf((float)all)));
+          u.i0 = (int)((long long)all * part / u.parts);
+          const int i1 = (int)((long long)all * (part + 1) / u.parts);
+          u.tiles[0] = min(u.tiles[0], i1);
+          u.tiles[1] = min(u.tiles[1], i1);
+          if (part >= u.parts) u.nt = 0;               // the unit has fewer
+        }
       }
       if (u.seq < 0 || u.nt > 0) {
-        const int tiles = u.seq < 0 ? 0 : max(u.tiles[0], u.tiles[1]);
+        const int tiles = u.seq < 0 ? 0 : max(0, max(u.tiles[0], u.tiles[1]) - u.i0);
         int id = 0;
         if (tiles > 0) {
-          const KeyTile kt = key_tile(u, 0, a.window);
+          const KeyTile kt = key_tile(u, u.i0, a.window);
           const int key = kt.j0 + lane * p.box_rows;
-          if (box_wanted(u, kt, 0, key, lane, p)) id = page_id(p, u, key);
+          if (box_wanted(u, kt, u.i0, key, lane, p)) id = page_id(p, u, key);
         }
         const int slot = published % kUnitRing;
         while (published - released >= kUnitRing) {
@@ -671,7 +802,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       }
       unsigned taken = 0;
       if (lane == 0) taken = atomicAdd(p.counter, 1u);
-      idx = (long long)gridDim.x + __shfl_sync(kFullMask, taken, 0);
+      idx = (int)(gridDim.x + __shfl_sync(kFullMask, taken, 0));
     }
     if (lane == 0) {
       // The last CTA to take its end leaves the counters at zero.
@@ -698,7 +829,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       }
       if (u.seq < 0) break;
       const int tiles = max(u.tiles[0], u.tiles[1]);
-      if (tiles == 0) continue;
+      if (tiles <= u.i0) continue;
 
       ok = ok && mbar_wait_warp(&sh.q_empty[q_slot], q_phase ^ 1u);
       const int row_tiles = u.nt > p.n ? 2 : 1;
@@ -715,7 +846,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         q_slot = 0;
         q_phase ^= 1u;
       }
-      for (int i = 0; i < tiles && ok; ++i) {
+      for (int i = u.i0; i < tiles && ok; ++i) {
         const KeyTile kt = key_tile(u, i, a.window);
         // Lane x copies box x, if a row sees a key of it; the next tile's
         // pages are looked up meanwhile.
@@ -794,6 +925,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       u.start = __shfl_sync(kFullMask, v.start, 0);
       u.sinks = __shfl_sync(kFullMask, v.sinks, 0);
       u.sink_tiles = __shfl_sync(kFullMask, v.sink_tiles, 0);
+      u.i0 = __shfl_sync(kFullMask, v.i0, 0);
       u.tiles[0] = __shfl_sync(kFullMask, v.tiles[0], 0);
       u.tiles[1] = __shfl_sync(kFullMask, v.tiles[1], 0);
       if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
@@ -803,22 +935,22 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       }
       if (u.seq < 0) break;
       const int tiles = max(u.tiles[0], u.tiles[1]);
-      if (tiles == 0) continue;
+      if (tiles <= u.i0) continue;
       const uint32_t q_addr = q_base + (uint32_t)q_slot * 2 * S::kTileBytes;
       if (ok) ok = mbar_wait_warp(&sh.q_full[q_slot], q_phase);
       if (ok) ok = mbar_wait_warp(&sh.full[stage], phase);
       tc_fence_after_sync();
-      int cols = key_tile(u, 0, a.window).cols;
+      int cols = key_tile(u, u.i0, a.window).cols;
       if (elect_one()) {
         const uint32_t idesc = mma_idesc((cols + 15) & ~15, false);
-        if (u.tiles[0] > 0) scores(0, q_addr, stage, idesc);
-        if (u.tiles[1] > 0) scores(1, q_addr, stage, idesc);
+        if (u.tiles[0] > u.i0) scores(0, q_addr, stage, idesc);
+        if (u.tiles[1] > u.i0) scores(1, q_addr, stage, idesc);
         tc_commit(&sh.empty[stage]);
-        if (tiles == 1) tc_commit(&sh.q_empty[q_slot]);
+        if (tiles == u.i0 + 1) tc_commit(&sh.q_empty[q_slot]);
       }
       __syncwarp();
       step();
-      for (int i = 0; i < tiles; ++i) {
+      for (int i = u.i0; i < tiles; ++i) {
         const int v_stage = stage;
         const uint32_t v_phase = phase;
         step();                                     // now at the next tile's keys
@@ -831,7 +963,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (i < u.tiles[t]) {
-            if (i == 0) {                           // the last unit's O has been read
+            if (i == u.i0) {                        // the last unit's O has been read
               if (ok) ok = mbar_wait_warp(&sh.o_empty[t], ((o_phase >> t) & 1u) ^ 1u);
               o_phase ^= 1u << t;
             }
@@ -845,7 +977,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
               for (int k = 0; k < kKeys / 16; ++k)
                 if (k < steps)
                   tc_mma_ts(o_tmem, p_tmem + k * 8, vd + (uint32_t)(k * 2048 >> 4), kIdescO,
-                            (i > 0 || k > 0) ? 1u : 0u);
+                            (i > u.i0 || k > 0) ? 1u : 0u);
               if (t == 1 || u.tiles[1] <= i) tc_commit(&sh.empty[v_stage]);
               if (i + 1 == u.tiles[t]) tc_commit(&sh.o_full[t]);
               else scores(t, q_addr, stage, idesc);
@@ -884,7 +1016,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       if (u.seq < 0) break;
       const int tiles = max(u.tiles[0], u.tiles[1]);
       int unit_lo = 0x7fffffff, unit_hi = -1;
-      for (int i = 0; i < tiles; ++i) {
+      for (int i = u.i0; i < tiles; ++i) {
         const KeyTile kt = key_tile(u, i, a.window);
         const int v_stage = stage + 1 < S::kStages ? stage + 1 : 0;
         if (kt.cut) {
@@ -957,8 +1089,28 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
+template <int D, bool kSplit>
+cudaError_t launch_kernel(const PrefillMaps& maps, const PrefillArgs& p, int grid,
+                          cudaStream_t stream) {
+  using S = Shape<D>;
+  constexpr size_t smem =
+      (size_t)(2 * S::kQSlots + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
+  static_assert(smem <= 227 * 1024, "shared memory");
+  static std::once_flag once[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t err = cudaSuccess;
+  std::call_once(once[dev & 63], [&] {
+    err = cudaFuncSetAttribute(attention_prefill_kernel<D, kSplit>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  });
+  if (err != cudaSuccess) return err;
+  return launch_after_previous(attention_prefill_kernel<D, kSplit>, dim3((unsigned)grid),
+                               dim3(kThreads), smem, stream, maps, p);
+}
+
 template <int D>
-cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
+cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   using S = Shape<D>;
   PrefillArgs p = {};
   p.a = a;
@@ -967,8 +1119,8 @@ cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
   while ((1 << p.box_shift) < p.box_rows) ++p.box_shift;
   const int64_t slots = query_tile_slots(a.seqs, a.T, 2 * p.n);
   p.slots = (int)slots;
-  p.units = slots * a.cache.kv_heads;
-  p.counter = static_cast<unsigned int*>(counters);
+  p.units = (int)(slots * a.cache.kv_heads);   // below 2^31, as the caller has checked
+  p.counter = prefill_counters(workspace);
   PrefillMaps maps;
   if (!kv_tensor_map(a.cache, false, p.box_rows, 1, &maps.k) ||
       !kv_tensor_map(a.cache, true, p.box_rows, 1, &maps.v))
@@ -986,28 +1138,21 @@ cudaError_t launch(const AttnArgs& a, void* counters, cudaStream_t stream) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
-  constexpr size_t smem =
-      (size_t)(2 * S::kQSlots + S::kStages) * S::kTileBytes + sizeof(PrefillShared<D>);
-  static_assert(smem <= 227 * 1024, "shared memory");
-  static std::once_flag once[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  cudaError_t err = cudaSuccess;
-  std::call_once(once[dev & 63], [&] {
-    err = cudaFuncSetAttribute(attention_prefill_kernel<D>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  });
-  if (err != cudaSuccess) return err;
-  const int grid = (int)std::min<int64_t>(attention_num_sms(), p.units);
-  return launch_after_previous(attention_prefill_kernel<D>, dim3((unsigned)grid), dim3(kThreads),
-                               smem, stream, maps, p);
+  p.pieces = static_cast<float*>(workspace_pieces(workspace));
+  static_assert(sizeof(float) * 2 * 256 * kRows * (D + 2) <= kPiecesBytes, "workspace");
+  // Where the units might be few enough to be split and long enough, a CTA per
+  // SM. (The form that cannot split is 5 % faster at short units.)
+  const int sms = std::min(attention_num_sms(), 256);
+  const int64_t room = (int64_t)a.seqs.max_pages << a.cache.page_shift;
+  if (a.seqs.num_seqs <= kFewSeqs && p.units <= sms && room >= 4 * kKeys)
+    return launch_kernel<D, true>(maps, p, sms, stream);
+  return launch_kernel<D, false>(maps, p, std::min(sms, p.units), stream);
 }
 
 }  // namespace
 
 cudaError_t launch_attention_prefill(const AttnArgs& a, void* workspace, cudaStream_t stream) {
-  void* counters = static_cast<unsigned char*>(workspace) + decode_counter_bytes();
-  return a.cache.head_dim == 64 ? launch<64>(a, counters, stream) : launch<128>(a, counters, stream);
+  return a.cache.head_dim == 64 ? launch<64>(a, workspace, stream) : launch<128>(a, workspace, stream);
 }
 
 }  // namespace mxfp4el

@@ -17,6 +17,10 @@
 // block of scores each and then kR rows by D / 16 widths of the result; with
 // kR = 4 that is 64 multiply-adds per eight 16-byte shared-memory reads. The
 // next tile is copied while this one is computed.
+//
+// Few rows: where the tiles are fewer than the SMs, the keys of each are split
+// over several blocks. Each leaves its (m, l, o) in the workspace, and the
+// last to arrive joins them in their order along the keys.
 #include <algorithm>
 #include <mutex>
 
@@ -43,9 +47,19 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool valid) {
                : "memory");
 }
 
-template <int D, int kR>
+// What the blocks of one tile share: `parts` of them, a counter per tile, and
+// per (tile, part) 16 kR rows of o and then their m and l.
+struct Split {
+  int parts;
+  unsigned int* counters;
+  float* pieces;
+};
+constexpr int kMinPartTiles = 4;  // key tiles to a part at least: less than that costs a join
+
+template <int D, int kR, bool kSplit>
 __global__ void __launch_bounds__(kThreads)
-attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tokens_tile) {
+attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tokens_tile,
+                      const Split split) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem<D, kR>& sh = *reinterpret_cast<Smem<D, kR>*>(smem_raw);
   constexpr int kRowsTile = 16 * kR;
@@ -59,13 +73,25 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
   const int slot = blockIdx.x;
   const int b = sequence_of_slot(a.seqs, slot, a.T, tokens_tile, lane);
   const SeqRows r = sequence_rows(a.seqs, b, a.T, a.cache.page_shift, a.status,
-                                  blockIdx.y == 0 && threadIdx.x == 0);
+                                  blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0);
   const int tile = a.seqs.q_offsets == nullptr ? 0 : slot - (r.first / tokens_tile + b);
   const int t0 = tile * tokens_tile;                     // first new token of the tile
   const int nt = min(tokens_tile, r.count - t0);
   if (nt <= 0) return;
   const int rows = nt * nh;
   const int pos_lo = r.pos0 + t0, pos_hi = pos_lo + nt - 1;
+
+  // Keys any row of the tile sees: [0, sinks) and [first, last], in tiles of
+  // kKeysTile; this block takes tiles [i0, i1) of them.
+  const int last = min(pos_hi, r.len - 1);
+  const int first = a.window ? max(0, pos_lo - a.window + 1) : 0;
+  const int first_tile = first / kKeysTile;
+  const int sink_tiles = min((a.sinks + kKeysTile - 1) / kKeysTile, first_tile);
+  const int tiles = last < 0 ? 0 : sink_tiles + last / kKeysTile - first_tile + 1;
+  const int parts = kSplit ? max(1, min(split.parts, tiles / kMinPartTiles)) : 1;
+  if ((int)blockIdx.z >= parts) return;
+  const int i0 = kSplit ? (int)((int64_t)tiles * blockIdx.z / parts) : 0;
+  const int i1 = kSplit ? (int)((int64_t)tiles * (blockIdx.z + 1) / parts) : tiles;
 
   // Query rows; rows past the tile are zeros.
   for (int i = threadIdx.x; i < kRowsTile * (D / 4); i += kThreads) {
@@ -92,13 +118,8 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     for (int d = 0; d < D / 16; ++d) o[i][d] = 0.f;
   }
 
-  // Keys any row of the tile sees: [0, sinks) and [first, last].
-  const int last = min(pos_hi, r.len - 1);
-  const int first = a.window ? max(0, pos_lo - a.window + 1) : 0;
-  // The tiles that hold them, in order: the next one's first key.
-  auto next_tile = [&](int j0) {
-    j0 += kKeysTile;
-    return j0 >= a.sinks && j0 + kKeysTile <= first ? first / kKeysTile * kKeysTile : j0;
+  auto tile_key = [&](int i) {
+    return (i < sink_tiles ? i : first_tile + i - sink_tiles) * kKeysTile;
   };
   // Four threads copy a key's row and its value's; keys that no row sees and
   // page ids out of range become zeros.
@@ -126,12 +147,12 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  int j0 = next_tile(-kKeysTile), buf = 0;
-  if (j0 <= last) copy_tile(j0, 0);
-  for (; j0 <= last; j0 = next_tile(j0), buf ^= 1) {
+  if (i0 < i1) copy_tile(tile_key(i0), 0);
+  for (int it = i0, buf = 0; it < i1; ++it, buf ^= 1) {
+    const int j0 = tile_key(it);
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();                   // this tile is there, the other buffer's readers are done
-    if (next_tile(j0) <= last) copy_tile(next_tile(j0), buf ^ 1);
+    if (it + 1 < i1) copy_tile(tile_key(it + 1), buf ^ 1);
 
     float s[kR][4];
 #pragma unroll
@@ -220,6 +241,60 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     }
   }
 
+  if (kSplit && parts > 1) {
+    constexpr size_t kPiece = (size_t)kRowsTile * (D + 2);
+    const size_t at = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+    float* base = split.pieces + at * split.parts * kPiece;
+    float* mine = base + blockIdx.z * kPiece;
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const int row = ty * kR + i;
+#pragma unroll
+      for (int d = 0; d < D / 64; ++d)
+        *reinterpret_cast<float4*>(mine + row * D + d * 64 + tx * 4) =
+            make_float4(o[i][4 * d], o[i][4 * d + 1], o[i][4 * d + 2], o[i][4 * d + 3]);
+      if (tx == 0) {
+        mine[kRowsTile * D + row] = m[i];
+        mine[kRowsTile * (D + 1) + row] = l[i];
+      }
+    }
+    __threadfence();
+    __shared__ int joins;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      joins = atomicInc(split.counters + at, (unsigned)(parts - 1)) == (unsigned)(parts - 1);
+    __syncthreads();
+    if (!joins) return;
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const float* stats = base + kRowsTile * D + ty * kR + i;
+      m[i] = -INFINITY;
+      for (int k = 0; k < parts; ++k) m[i] = fmaxf(m[i], __ldcg(stats + k * kPiece));
+      l[i] = 0.f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) o[i][d] = 0.f;
+    }
+    for (int k = 0; k < parts; ++k) {
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        const float* piece = base + k * kPiece;
+        const int row = ty * kR + i;
+        const float f = exp2_approx(__ldcg(piece + kRowsTile * D + row) -
+                                    (m[i] == -INFINITY ? 0.f : m[i]));
+        l[i] = fmaf(__ldcg(piece + kRowsTile * (D + 1) + row), f, l[i]);
+#pragma unroll
+        for (int d = 0; d < D / 64; ++d) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(piece + row * D + d * 64 + tx * 4));
+          o[i][4 * d] = fmaf(x.x, f, o[i][4 * d]);
+          o[i][4 * d + 1] = fmaf(x.y, f, o[i][4 * d + 1]);
+          o[i][4 * d + 2] = fmaf(x.z, f, o[i][4 * d + 2]);
+          o[i][4 * d + 3] = fmaf(x.w, f, o[i][4 * d + 3]);
+        }
+      }
+    }
+  }
+
 #pragma unroll
   for (int i = 0; i < kR; ++i) {
     const int row = ty * kR + i;
@@ -242,40 +317,64 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
   }
 }
 
-template <int D, int kR>
-cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  const int heads_tile = std::min(a.group, 16 * kR);
-  const int head_blocks = (a.group + heads_tile - 1) / heads_tile;
-  const int tokens_tile = 16 * kR / heads_tile;
-  const dim3 grid((unsigned)query_tile_slots(a.seqs, a.T, tokens_tile),
-                  (unsigned)(a.cache.kv_heads * head_blocks));
+template <int D, int kR, bool kSplit>
+cudaError_t launch_kernel(const AttnArgs& a, dim3 grid, int heads_tile, int head_blocks,
+                          int tokens_tile, const Split& split, cudaStream_t stream) {
   const int smem = (int)sizeof(Smem<D, kR>);
   static std::once_flag once[64];
   int dev = 0;
   cudaGetDevice(&dev);
   cudaError_t err = cudaSuccess;
   std::call_once(once[dev & 63], [&] {
-    err = cudaFuncSetAttribute(attention_simt_kernel<D, kR>,
+    err = cudaFuncSetAttribute(attention_simt_kernel<D, kR, kSplit>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (err != cudaSuccess) return err;
-  return launch_after_previous(attention_simt_kernel<D, kR>, grid, dim3(kThreads), smem, stream, a,
-                               heads_tile, head_blocks, tokens_tile);
+  return launch_after_previous(attention_simt_kernel<D, kR, kSplit>, grid, dim3(kThreads), smem,
+                               stream, a, heads_tile, head_blocks, tokens_tile, split);
+}
+
+template <int D, int kR>
+cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  const int heads_tile = std::min(a.group, 16 * kR);
+  const int head_blocks = (a.group + heads_tile - 1) / heads_tile;
+  const int tokens_tile = 16 * kR / heads_tile;
+  dim3 grid((unsigned)query_tile_slots(a.seqs, a.T, tokens_tile),
+            (unsigned)(a.cache.kv_heads * head_blocks));
+  // Parts: up to two blocks per SM in all, and no more than the longest keys
+  // that a row could see allow.
+  const int64_t tiles = (int64_t)grid.x * grid.y, sms = attention_num_sms();
+  Split split = {};
+  split.parts = 1;
+  split.counters = prefill_counters(workspace);
+  split.pieces = static_cast<float*>(workspace_pieces(workspace));
+  if (tiles < sms && tiles <= kPrefillCounters) {
+    int64_t keys = (int64_t)a.seqs.max_pages << a.cache.page_shift;
+    if (a.window > 0) keys = std::min<int64_t>(keys, (int64_t)a.window + a.sinks + tokens_tile + 128);
+    split.parts = (int)std::max<int64_t>(
+        1, std::min<int64_t>(2 * sms / tiles, keys / (kMinPartTiles * kKeysTile)));
+  }
+  grid.z = (unsigned)split.parts;
+  return split.parts > 1 ? launch_kernel<D, kR, true>(a, grid, heads_tile, head_blocks, tokens_tile,
+                                                      split, stream)
+                         : launch_kernel<D, kR, false>(a, grid, heads_tile, head_blocks,
+                                                       tokens_tile, split, stream);
 }
 
 // Tiles of 64 rows, or of 32 where 64 would leave SMs without a second block
 // to hide the first one's waits behind.
 template <int D>
-cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_rows(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.T * a.heads;
-  return rows >= 2 * 64 * (int64_t)attention_num_sms() ? launch<D, 4>(a, stream)
-                                                       : launch<D, 2>(a, stream);
+  return rows >= 2 * 64 * (int64_t)attention_num_sms() ? launch<D, 4>(a, workspace, stream)
+                                                       : launch<D, 2>(a, workspace, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_simt(const AttnArgs& a, cudaStream_t stream) {
-  return a.cache.head_dim == 64 ? launch_rows<64>(a, stream) : launch_rows<128>(a, stream);
+cudaError_t launch_attention_simt(const AttnArgs& a, void* workspace, cudaStream_t stream) {
+  return a.cache.head_dim == 64 ? launch_rows<64>(a, workspace, stream)
+                                : launch_rows<128>(a, workspace, stream);
 }
 
 }  // namespace mxfp4el

@@ -563,3 +563,42 @@ def test_calls_in_a_row_do_not_disturb_each_other(dtype, decode):
         for a, b in zip(g, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert lib.wait_timeouts() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (6, 2), (100, 1)])
+def test_prefill_split_over_the_keys(dtype, dim, heads, kv_heads):
+    # Few rows behind histories long and short: units in many parts, in few
+    # and whole, rows that see nothing, a part that only the later row tile
+    # reaches.
+    lens, new = [6000, 1025, 130, 3, 0, 2048], [70, 3, 130, 5, 0, 300]
+    d = make(lens, new, heads=heads, kv_heads=kv_heads, dim=dim, dtype=dtype, page=32,
+             fill=math.nan)
+    first = check(d, False, logits=True)
+    for _ in range(3):
+        assert torch.equal(call(d, False, True), first)
+    check(d, False, window=1500, sinks=200)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_values_not_finite_in_a_split_unit(dtype):
+    lens, new = [5000], [40]
+    d = make(lens, new, heads=4, kv_heads=1, dtype=dtype)
+    clean = call(d, False, window=4000, sinks=50)
+    for j in (4975, 970, 20):        # seen by the last rows, by the first, by all
+        page, slot = int(d["table"][0, j // 16]), j % 16
+        d["vp"][page, :, slot, 9] = math.inf
+        got = check(d, False, window=4000, sinks=50)
+        if j == 4975:
+            assert torch.equal(got[:15, :, :9], clean[:15, :, :9])
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("heads,kv_heads", [(100, 1), (128, 1), (66, 2)])
+def test_many_heads_to_a_key_head(decode, dtype, heads, kv_heads):
+    lens = [70, 1, 333, 0]
+    new = [1] * 4 if decode else [70, 1, 5, 0]
+    check(make(lens, new, heads=heads, kv_heads=kv_heads, dtype=dtype, fill=math.nan), decode,
+          logits=True)
