@@ -12,7 +12,10 @@
 // Bound: bytes. A unit reads 2 len D elements of cache and does 2 len D
 // multiply-adds a row, a few operations per byte, so the design is about
 // keeping HBM busy: one warp issues tensor copies of whole pages into a ring
-// of stages and never computes; four warps per 16 heads consume.
+// of stages and never computes; four warps per 16 heads consume. 128 sequences
+// of up to 16384 keys, 8 key heads of 128: 647 us, 6.7 TB/s, as fast as a plain
+// copy; two of up to 131072: 162 us, 6.5 TB/s, of which the launch and the join
+// take about 5; DRAM reads 1.00 times the keys and values.
 //
 // Split. Lengths live on the device, so the host launches a fixed grid and
 // every CTA derives the same split: the tiles of all units, in unit order,
@@ -20,8 +23,11 @@
 // finished there. Otherwise each of its CTAs writes an unnormalised piece
 // (m, l, o) to the workspace, and the CTA that arrives last joins the pieces
 // in their order along the keys, so the result does not depend on who is
-// last. Every run holds at least kMinTiles tiles: a piece costs a round trip
-// through L2, about what three tiles cost.
+// last. A join costs a round trip through L2, about what three tiles cost, so
+// runs hold at least kMinTiles tiles, and where no unit has more than
+// kWholeTiles the units are dealt out whole instead (one sequence of 333 keys,
+// 8 key heads: 12.0 us with joins, 11.4 without; 16 sequences of up to 132
+// visible keys: 11.9 and 8.3).
 //
 // Matrix products. bf16: mma.sync m16n8k16 with the 16 heads as rows. The
 // legacy tensor path is enough here (two instructions per key and 16 heads
@@ -45,6 +51,7 @@ namespace {
 
 constexpr int kGroups = 4;              // key groups of a tile: one consumer warp each per 16 heads
 constexpr int kMinTiles = 4;            // tiles per run at least (see above)
+constexpr int kWholeTiles = 8;
 constexpr int kMaxCtas = 256;
 constexpr int kMaxSeqs = 1024;          // sequences per launch (the prefix sums' shared memory)
 constexpr int kRowsMax = 64;            // query heads per unit: 16 kMT, kMT <= 4
@@ -97,6 +104,7 @@ struct __align__(16) DecodeShared {
   float merge_m[kMT][2][16], merge_l[kMT][2][16];
   int last;
   long long scan[8 + 4 * kMT];
+  int longest[8 + 4 * kMT];
   long long prefix[kMaxSeqs + 1];     // tiles of all units before sequence b
 };
 
@@ -505,6 +513,8 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
+    prefetch_tensor_map(&maps.k);
+    prefetch_tensor_map(&maps.v);
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], kGroups * kMT);
@@ -523,6 +533,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     const int per = (d.num_seqs + kThreads - 1) / kThreads;
     const int b0 = min((int)threadIdx.x * per, d.num_seqs), b1 = min(b0 + per, d.num_seqs);
     long long mine = 0;
+    int most = 0;
     for (int b = b0; b < b1; ++b) {
       const int n = sequence_len(d, b);
       int lo, st, ft, tiles;
@@ -530,7 +541,10 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       if (blockIdx.x == 0 && __ldg(a.seqs.seq_lens + d.seq0 + b) > n)
         atomicAdd(&a.status[kStatusBadPages], 1ull);
       mine += (long long)tiles * d.units_per_seq;
+      most = max(most, tiles);
     }
+    most = __reduce_max_sync(kFullMask, most);
+    if (lane == 0) sh.longest[warp] = most;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -552,7 +566,22 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   }
   const long long total = sh.prefix[d.num_seqs];
   const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);
-  const long long t0 = per * blockIdx.x, t1 = min(t0 + per, total);
+  long long t0 = per * blockIdx.x, t1 = min(t0 + per, total);
+  int longest = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, sh.longest[w]);
+  if (longest <= kWholeTiles) {
+    // Whole units: from unit units b / grid to the next CTA's first.
+    const long long units = (long long)d.num_seqs * d.units_per_seq;
+    auto first_tile = [&](long long unit) {
+      const int b = (int)(unit / d.units_per_seq);
+      if (b >= d.num_seqs) return total;
+      return sh.prefix[b] + (unit - (long long)b * d.units_per_seq) *
+                                ((sh.prefix[b + 1] - sh.prefix[b]) / d.units_per_seq);
+    };
+    t0 = first_tile(units * blockIdx.x / gridDim.x);
+    t1 = first_tile(units * (blockIdx.x + 1) / gridDim.x);
+  }
   if (t0 >= t1) return;
 
   if (warp == 0) {
@@ -812,7 +841,8 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   for (int b = 0; b < a.seqs.num_seqs; b += kMaxSeqs) {
     d.seq0 = b;
     d.num_seqs = std::min(kMaxSeqs, a.seqs.num_seqs - b);
-    const int64_t most = ((int64_t)d.num_seqs * d.units_per_seq * room + kMinTiles - 1) / kMinTiles;
+    const int64_t units = (int64_t)d.num_seqs * d.units_per_seq;
+    const int64_t most = std::max(units, (units * room + kMinTiles - 1) / kMinTiles);
     const int grid = (int)std::min<int64_t>(std::min(attention_num_sms(), kMaxCtas), most);
     err = launch_after_previous(attention_decode_kernel<Tok, D, kMT, kH>, dim3((unsigned)grid),
                                 dim3(32 * (1 + kGroups * kMT)), smem, stream, maps, d);
@@ -825,7 +855,7 @@ template <typename Tok, int D>
 cudaError_t launch_heads(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   // float32: the CUDA cores' work grows with the heads that a warp carries, so
   // groups of up to 4 and 8 have kernels of their own (24 sequences of up to
-  // 3001 keys, 4 heads to a key head: 130 us with 16 carried, KKK with 4). The
+  // 3001 keys, 4 heads to a key head: 130 us with 16 carried, 40 with 4). The
   // bf16 instruction takes 16 rows whatever the group.
   if constexpr (sizeof(Tok) == 4) {
     if (a.group <= 4) return launch<Tok, D, 1, 4>(a, workspace, stream);

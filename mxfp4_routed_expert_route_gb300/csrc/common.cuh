@@ -432,6 +432,11 @@ __device__ __forceinline__ void tmem_wait_ld() {
 }
 
 // --------------------------------------------------------- TMA tensor loads --
+// Brings a tensor map of the kernel's parameters to where the copies read it.
+__device__ __forceinline__ void prefetch_tensor_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
+}
+
 // 2D tiled load of a box at element coordinates (x innermost, y); x times
 // the element size must be a multiple of 16 bytes.
 __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y,

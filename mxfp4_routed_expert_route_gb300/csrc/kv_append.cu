@@ -8,7 +8,9 @@
 // values to the token's slot of the cache.
 //
 // Bound: bytes. (heads + 2 kv_heads) head_dim elements are read and as many
-// written; the rotation table adds rotary_dim floats per token.
+// written; the rotation table adds rotary_dim floats per token. 8192 tokens, 64
+// query and 8 key heads of 128, normed and turned: 58.5 us, 5.8 TB/s. A handful
+// of tokens: 2.3 us, a launch.
 //
 // Layout: a row's lanes hold two chunks of 8 elements each (chunk j of the
 // first half of the turned elements and its partner in the second half, so
@@ -16,6 +18,10 @@
 // rotary_dim pair up among themselves). head_dim / 16 lanes make a row, so a
 // warp takes 32 / (head_dim / 16) rows at a time, of one token: the cosines
 // and sines of the token stay in the lanes' registers for all of its rows.
+// Queries, keys and values are separate runs of steps, so that each step's
+// addresses are sums and its arithmetic (two float32 at a time) has no cases:
+// 41,900 instructions per scheduler and 58.5 us; with the cases inside one loop
+// 63,800 and 65; one step per warp, each looking its token up anew, 92 us.
 #include <algorithm>
 
 #include "attn.cuh"
