@@ -146,7 +146,8 @@ int mxfp4el_attention_decode(const void* q, int64_t q_token_stride, int64_t q_he
  * mxfp4el_attention_prefill -- T new tokens of seqs->num_seqs sequences,
  * rows as seqs->q_offsets says (NULL: one token per sequence, T ==
  * num_seqs). Rows past q_offsets[num_seqs] give zeros. Everything else as
- * mxfp4el_attention_decode.
+ * mxfp4el_attention_decode. (T + num_seqs + 1) * num_kv_heads beyond about
+ * 2^31 is MXFP4EL_ERR_TOO_LARGE.
  */
 int mxfp4el_attention_prefill(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                               const mxfp4el_kv_cache* cache, const mxfp4el_sequences* seqs,
