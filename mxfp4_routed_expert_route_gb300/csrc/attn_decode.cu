@@ -74,6 +74,10 @@ struct Shape {
       (kMT == 1 ? 5 : kMT == 2 ? 4 : sizeof(Tok) == 2 ? 3 : 2) * 32768 / (2 * (int)kHalf);
   static constexpr int kQRow = D * (int)sizeof(Tok) + 16;           // padded row in shared memory
   static constexpr int kAcc = kH * D / 32;                          // result elements per lane
+  // The join of a unit's four warps goes through shared memory in kPasses
+  // parts of kPass elements, of which each warp finishes kShare.
+  static constexpr int kPasses = kMT == 4 || (kMT == 2 && sizeof(Tok) == 4) ? 2 : 1;
+  static constexpr int kPass = kAcc / kPasses, kShare = kPass / kGroups;
 };
 
 struct Unit {
@@ -101,7 +105,7 @@ template <int kMT>
 struct __align__(16) DecodeShared {
   uint64_t full[16], empty[16];
   uint64_t q_full[kQSlots], q_empty[kQSlots];
-  float merge_m[kMT][2][16], merge_l[kMT][2][16];
+  float merge_m[kMT][kGroups][16], merge_l[kMT][kGroups][16];
   int last;
   long long scan[8 + 4 * kMT];
   int longest[8 + 4 * kMT];
@@ -124,27 +128,46 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, int n, int* lo, int*
   *tiles = max(1, *sink_tiles + (n + kTile - 1) / kTile - *first_tile);
 }
 
-template <typename Tok, int D, int kMT>
-__device__ __forceinline__ Unit locate(const DecodeArgs& d, const DecodeShared<kMT>& sh,
-                                       long long tile, long long* unit_first) {
-  int lo = 0, hi = d.num_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sh.prefix[mid] <= tile) lo = mid;
-    else hi = mid;
-  }
+// The units of a run, one after another.
+template <int kTile, int kMT>
+struct Walk {
+  int i;               // unit of the sequence
+  long long first;     // its first tile
   Unit u;
-  u.b = lo;
-  u.len = sequence_len(d, lo);
-  tiles_of<Shape<Tok, D>::kTile>(d.a, u.len, &u.lo, &u.sink_tiles, &u.first_tile, &u.tiles);
-  const int i = (int)((tile - sh.prefix[lo]) / u.tiles);
-  *unit_first = sh.prefix[lo] + (long long)i * u.tiles;
-  u.kvh = i / d.head_blocks;
-  const int blk = i - u.kvh * d.head_blocks;
-  u.head0 = u.kvh * d.a.group + blk * 16 * kMT;
-  u.rows = min(16 * kMT, d.a.group - blk * 16 * kMT);
-  return u;
-}
+  __device__ __forceinline__ void sequence(const DecodeArgs& d, int b) {
+    u.b = b;
+    u.len = sequence_len(d, b);
+    tiles_of<kTile>(d.a, u.len, &u.lo, &u.sink_tiles, &u.first_tile, &u.tiles);
+  }
+  __device__ __forceinline__ void unit(const DecodeArgs& d) {
+    const int blk = d.head_blocks == 1 ? 0 : i % d.head_blocks;
+    u.kvh = d.head_blocks == 1 ? i : i / d.head_blocks;
+    u.head0 = u.kvh * d.a.group + blk * 16 * kMT;
+    u.rows = min(16 * kMT, d.a.group - blk * 16 * kMT);
+  }
+  // The unit that holds `tile`.
+  __device__ __forceinline__ void start(const DecodeArgs& d, const DecodeShared<kMT>& sh,
+                                        long long tile) {
+    int lo = 0, hi = d.num_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sh.prefix[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    sequence(d, lo);
+    i = (int)((tile - sh.prefix[lo]) / u.tiles);
+    first = sh.prefix[lo] + (long long)i * u.tiles;
+    unit(d);
+  }
+  __device__ __forceinline__ void next(const DecodeArgs& d) {
+    first += u.tiles;
+    if (++i == d.units_per_seq) {
+      i = 0;
+      if (u.b + 1 < d.num_seqs) sequence(d, u.b + 1);
+    }
+    unit(d);
+  }
+};
 
 // ---------------------------------------------------------------- consumers --
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -183,12 +206,12 @@ __device__ __forceinline__ uint32_t box_row(int j, int box_rows, int box_shift, 
 
 // One warp: 16 query heads x the warp's share of each tile's keys.
 // Result element i of a lane: row row(i), column col(i).
-template <typename Tok, int D, int kH>
+template <typename Tok, int D, int kH, int kMT>
 struct Consumer;
 
-template <int D>
-struct Consumer<__nv_bfloat16, D, 16> {
-  using S = Shape<__nv_bfloat16, D>;
+template <int D, int kMT>
+struct Consumer<__nv_bfloat16, D, 16, kMT> {
+  using S = Shape<__nv_bfloat16, D, kMT>;
   uint32_t q[D / 16][4];
   float m[2], l[2];          // rows lane / 4 and lane / 4 + 8; l: this lane's keys only
   float acc[S::kAcc];
@@ -283,21 +306,11 @@ struct Consumer<__nv_bfloat16, D, 16> {
       mma_bf16(acc + 8 * n + 4, p, b[2], b[3]);
     }
   }
-  // Joins the piece (ms, ls, o) of other keys, o laid out as acc.
-  __device__ __forceinline__ void merge(const float* ms, const float* ls, const float* o, int lane,
-                                        float*) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float mo = ms[lane / 4 + 8 * r], top = fmaxf(m[r], mo);
-      const float base = top == -INFINITY ? 0.f : top;
-      const float f = exp2_approx(m[r] - base), g = exp2_approx(mo - base);
-      l[r] = l[r] * f + ((lane & 3) == 0 ? ls[lane / 4 + 8 * r] * g : 0.f);
-      m[r] = top;
-#pragma unroll
-      for (int i = 0; i < S::kAcc; ++i)
-        if (((i >> 1) & 1) == r) acc[i] = acc[i] * f + o[i * 32 + lane] * g;
-    }
-  }
+  // The rows that a share of the result holds: element e of the share that
+  // starts at element `first` is in row share_row(first, share_of(e), lane).
+  static constexpr int kShareRows = 2;
+  static constexpr __device__ __forceinline__ int share_of(int e) { return (e >> 1) & 1; }
+  static __device__ __forceinline__ int share_row(int, int q, int lane) { return lane / 4 + 8 * q; }
   // Row statistics to shared memory (16 each).
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
 #pragma unroll
@@ -314,9 +327,9 @@ struct Consumer<__nv_bfloat16, D, 16> {
 };
 
 // kH of the 16 heads that the warp's buffers have room for.
-template <int D, int kH>
-struct Consumer<float, D, kH> {
-  using S = Shape<float, D, 1, kH>;
+template <int D, int kH, int kMT>
+struct Consumer<float, D, kH, kMT> {
+  using S = Shape<float, D, kMT, kH>;
   static constexpr int kL = kH / 4;    // heads per lane in the scores
   static constexpr int kW = D / 32;    // result columns per lane
   uint32_t q_addr;
@@ -436,27 +449,9 @@ struct Consumer<float, D, kH> {
       }
     }
   }
-  __device__ __forceinline__ void merge(const float* ms, const float* ls, const float* o, int lane,
-                                        float* p) {
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kL; ++i) {
-      const int h = (lane >> 3) * kL + i;
-      const float mo = ms[h], top = fmaxf(m[i], mo);
-      const float base = top == -INFINITY ? 0.f : top;
-      const float f = exp2_approx(m[i] - base), g = exp2_approx(mo - base);
-      l[i] = l[i] * f + ((lane & 7) == 0 ? ls[h] * g : 0.f);
-      m[i] = top;
-      if ((lane & 7) == 0) {
-        p[h] = f;
-        p[16 + h] = g;
-      }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < S::kAcc; ++i)
-      acc[i] = acc[i] * p[i / kW] + o[i * 32 + lane] * p[16 + i / kW];
-  }
+  static constexpr int kShareRows = S::kShare / kW;
+  static constexpr __device__ __forceinline__ int share_of(int e) { return e / kW; }
+  static __device__ __forceinline__ int share_row(int first, int q, int) { return first / kW + q; }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
@@ -496,7 +491,7 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, fl
 }
 
 template <typename Tok, int D, int kMT, int kH>
-__global__ void __launch_bounds__(32 * (1 + kGroups * kMT))
+__global__ void __launch_bounds__(32 * (1 + kGroups * kMT), 1)
 attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs d) {
   using S = Shape<Tok, D, kMT, kH>;
   constexpr int kThreads = 32 * (1 + kGroups * kMT), kConsumers = kThreads - 32;
@@ -504,7 +499,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* q_smem = ring + (size_t)S::kStages * 2 * S::kHalf;
   float* merge = reinterpret_cast<float*>(q_smem + kQSlots * 16 * kMT * S::kQRow);
-  float* p_smem = merge + (size_t)kMT * 2 * S::kAcc * 32;            // float32: p per warp
+  float* p_smem = merge + (size_t)kMT * kGroups * S::kPass * 32;     // float32: p per warp
   constexpr int kPFloats = sizeof(Tok) == 4 ? 144 : 0;
   DecodeShared<kMT>& sh =
       *reinterpret_cast<DecodeShared<kMT>*>(p_smem + kGroups * kMT * kPFloats);
@@ -586,63 +581,79 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      bool ok = true;
-      int stage = 0, slot = 0;
-      uint32_t phase = 0, q_phase = 0;
-      const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
-      for (long long t = t0; t < t1 && ok;) {
-        long long first;
-        const Unit u = locate<Tok, D, kMT>(d, sh, t, &first);
-        const int i0 = (int)(t - first), i1 = (int)min((long long)u.tiles, t1 - first);
-        t = first + i1;
-        if (!mbar_wait(&sh.q_empty[slot], q_phase ^ 1u)) { ok = false; break; }
+    // Lanes 0 to 15 each copy one box of a tile: lane & 7 says which, lane >> 3
+    // keys or values. The ids of the next tile's pages are on their way while
+    // this one waits for room.
+    static_assert(S::kTile / 8 <= 8, "boxes of a tile (pages have 8 slots at least)");
+    bool ok = true;
+    int stage = 0, slot = 0;
+    uint32_t phase = 0, q_phase = 0;
+    const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
+    const int x = (lane & 7) << d.box_shift, half = lane >> 3;
+    const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
+    const CUtensorMap* map = half == 0 ? &maps.k : &maps.v;
+    Walk<S::kTile, kMT> w;
+    w.start(d, sh, t0);
+    for (long long t = t0; t < t1 && ok; w.next(d)) {
+      const Unit u = w.u;
+      const int i0 = (int)(t - w.first), i1 = (int)min((long long)u.tiles, t1 - w.first);
+      t = w.first + i1;
+      const int* table = a.seqs.page_table + (int64_t)(d.seq0 + u.b) * a.seqs.table_stride;
+      // The lane's box of tile i has a key that is seen; *id is its page.
+      auto box = [&](int i, int* id, int* s0) {
+        const int j0 = (i < u.sink_tiles ? i : u.first_tile + i - u.sink_tiles) * S::kTile;
+        const int k0 = j0 + x, k1 = min(k0 + d.box_rows, u.len);
+        const bool seen =
+            half < 2 && x < S::kTile && k0 < k1 && (k1 > u.lo || k0 < a.sinks);
+        if (seen) *id = __ldg(table + (k0 >> a.cache.page_shift));
+        *s0 = k0 & (a.cache.page_size - 1);
+        return seen;
+      };
+      int id = 0, s0;
+      bool seen = box(i0, &id, &s0);
+      ok = mbar_wait_warp(&sh.q_empty[slot], q_phase ^ 1u);
+      if (!ok) break;
+      if (lane == 0)
         mbar_arrive_expect_tx(&sh.q_full[slot], (uint32_t)(u.rows * D * sizeof(Tok)));
-        const Tok* q = static_cast<const Tok*>(a.q) + (int64_t)(d.seq0 + u.b) * a.q_token +
-                       (int64_t)u.head0 * a.q_head;
-        for (int r = 0; r < u.rows; ++r)
-          bulk_copy_g2s(q_smem + (size_t)(slot * 16 * kMT + r) * S::kQRow, q + r * a.q_head,
-                        D * sizeof(Tok), &sh.q_full[slot], keep);
-        if (++slot == kQSlots) {
-          slot = 0;
-          q_phase ^= 1u;
+      __syncwarp();
+      const Tok* q = static_cast<const Tok*>(a.q) + (int64_t)(d.seq0 + u.b) * a.q_token +
+                     (int64_t)u.head0 * a.q_head;
+      for (int r = lane; r < u.rows; r += 32)
+        bulk_copy_g2s(q_smem + (size_t)(slot * 16 * kMT + r) * S::kQRow, q + r * a.q_head,
+                      D * sizeof(Tok), &sh.q_full[slot], keep);
+      if (++slot == kQSlots) {
+        slot = 0;
+        q_phase ^= 1u;
+      }
+      for (int i = i0; i < i1; ++i) {
+        int next_id = 0, next_s0 = 0;
+        const bool next_seen = i + 1 < i1 && box(i + 1, &next_id, &next_s0);
+        ok = mbar_wait_warp(&sh.empty[stage], phase ^ 1u);
+        if (!ok) break;
+        const uint32_t boxes = __ballot_sync(0xffffffffu, seen);
+        if (lane == 0) {
+          if (boxes == 0) mbar_arrive(&sh.full[stage]);
+          else mbar_arrive_expect_tx(&sh.full[stage], __popc(boxes) * box_bytes);
         }
-        const int* table = a.seqs.page_table + (int64_t)(d.seq0 + u.b) * a.seqs.table_stride;
-        for (int i = i0; i < i1; ++i) {
-          const int j0 = (i < u.sink_tiles ? i : u.first_tile + i - u.sink_tiles) * S::kTile;
-          if (!mbar_wait(&sh.empty[stage], phase ^ 1u)) { ok = false; break; }
-          unsigned char* dst = ring + (size_t)stage * 2 * S::kHalf;
-          // Boxes with a key that is seen.
-          uint32_t boxes = 0;
-          for (int x = 0; x < S::kTile; x += d.box_rows) {
-            const int k0 = j0 + x, k1 = min(k0 + d.box_rows, u.len);
-            if (k0 < k1 && (k1 > u.lo || k0 < a.sinks)) boxes |= 1u << (x >> d.box_shift);
-          }
-          const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
-          if (boxes == 0) {
-            mbar_arrive(&sh.full[stage]);
-          } else {
-            mbar_arrive_expect_tx(&sh.full[stage], 2u * __popc(boxes) * box_bytes);
-            for (uint32_t left = boxes; left; left &= left - 1) {
-              const int x = (__ffs(left) - 1) << d.box_shift, key = j0 + x;
-              // An id out of range reads as zeros (the copy's fill).
-              const int id = __ldg(table + (key >> a.cache.page_shift));
-              if ((unsigned)id >= (uint64_t)a.cache.num_pages)
-                atomicAdd(&a.status[kStatusBadPages], 1ull);
-              const int s0 = key & (a.cache.page_size - 1);
-              unsigned char* at = dst + (size_t)x * D * sizeof(Tok);
-              tma_load_5d(at, &maps.k, 0, s0, 0, u.kvh, id, &sh.full[stage], once);
-              tma_load_5d(at + S::kHalf, &maps.v, 0, s0, 0, u.kvh, id, &sh.full[stage], once);
-            }
-          }
-          if (++stage == S::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        __syncwarp();
+        if (seen) {
+          // An id out of range reads as zeros (the copy's fill).
+          if (half == 0 && (unsigned)id >= (uint64_t)a.cache.num_pages)
+            atomicAdd(&a.status[kStatusBadPages], 1ull);
+          tma_load_5d(ring + (size_t)stage * 2 * S::kHalf + (size_t)half * S::kHalf +
+                          (size_t)x * D * sizeof(Tok),
+                      map, 0, s0, 0, u.kvh, id, &sh.full[stage], once);
+        }
+        seen = next_seen;
+        id = next_id;
+        s0 = next_s0;
+        if (++stage == S::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
     }
+    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
     return;
   }
 
@@ -652,16 +663,19 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   // counters end as they should.
   const int cw = warp - 1, group = cw % kGroups, mt = cw / kGroups;
   const int bar = 1 + mt;                                   // the four warps of 16 heads
-  float* buf = merge + (size_t)mt * 2 * S::kAcc * 32;
+  float* buf = merge + (size_t)mt * kGroups * S::kPass * 32;
   float* p_warp = p_smem + cw * kPFloats;
   const float scale = a.scale * kLog2e;
-  Consumer<Tok, D, kH> c;
+  using C = Consumer<Tok, D, kH, kMT>;
+  C c;
   bool ok = true;
   int stage = 0, slot = 0;
   uint32_t phase = 0, q_phase = 0;
-  for (long long t = t0; t < t1;) {
-    long long first;
-    const Unit u = locate<Tok, D, kMT>(d, sh, t, &first);
+  Walk<S::kTile, kMT> walk;
+  walk.start(d, sh, t0);
+  for (long long t = t0; t < t1; walk.next(d)) {
+    const Unit u = walk.u;
+    const long long first = walk.first;
     const int i0 = (int)(t - first), i1 = (int)min((long long)u.tiles, t1 - first);
     t = first + i1;
     ok = ok && mbar_wait_warp(&sh.q_full[slot], q_phase);
@@ -700,56 +714,74 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       q_phase ^= 1u;
     }
 
-    // The four groups' (m, l, o), joined in two rounds: 2 into 0 and 3 into
-    // 1, then 1 into 0.
-#pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
-      float* mine = buf + (size_t)(group & (half - 1)) * S::kAcc * 32;
-      float* ms = sh.merge_m[mt][group & (half - 1)];
-      float* ls = sh.merge_l[mt][group & (half - 1)];
-      if (group >= half && group < 2 * half) {
-        c.stats(ms, ls, lane);
-#pragma unroll
-        for (int i = 0; i < S::kAcc; ++i) mine[i * 32 + lane] = c.acc[i];
-      }
-      bar_sync(bar, 32 * kGroups);
-      if (group < half) c.merge(ms, ls, mine, lane, p_warp);
-      bar_sync(bar, 32 * kGroups);
-    }
+    // The four warps' (m, l, o) meet in shared memory, and each warp joins and
+    // writes a quarter of the result.
     const bool whole = i0 == 0 && i1 == u.tiles;
-    if (group == 0) {
-      float* ms = sh.merge_m[mt][0];
-      float* ls = sh.merge_l[mt][0];
-      c.stats(ms, ls, lane);
-      __syncwarp();
-      if (whole) {
-        Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
+    bar_sync(bar, 32 * kGroups);                 // the last unit's have been read
+    c.stats(sh.merge_m[mt][group], sh.merge_l[mt][group], lane);
+    // Row r: the warps' factors, the common maximum and the sum.
+    auto join_row = [&](int r, float (&f)[kGroups], float* m) {
+      *m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < S::kAcc; i += 2) {
-          const int r = Consumer<Tok, D, kH>::row(i, lane), rr = mt * 16 + r;
-          if (rr < u.rows) {
-            const float inv = finish(a, u.head0 + rr, ms[r], ls[r]);
-            store_pair(out + (int64_t)rr * D + Consumer<Tok, D, kH>::col(i, lane), c.acc[i] * inv,
-                       c.acc[i + 1] * inv);
-          }
-        }
-      } else {
-        unsigned char* piece = d.pieces + (size_t)(2 * blockIdx.x + (i0 == 0 ? 1 : 0)) * kPieceBytes;
-        float* o = reinterpret_cast<float*>(piece);
-        float* st = o + kRowsMax * 128;
+      for (int k = 0; k < kGroups; ++k) *m = fmaxf(*m, sh.merge_m[mt][k][r]);
+      const float base = *m == -INFINITY ? 0.f : *m;
+      float l = 0.f;
 #pragma unroll
-        for (int i = 0; i < S::kAcc; i += 2) {
-          const int rr = mt * 16 + Consumer<Tok, D, kH>::row(i, lane);
-          if (rr < u.rows)
-            *reinterpret_cast<float2*>(o + rr * D + Consumer<Tok, D, kH>::col(i, lane)) =
-                make_float2(c.acc[i], c.acc[i + 1]);
-        }
-        if (lane < 16 && mt * 16 + lane < u.rows) {
-          st[mt * 16 + lane] = ms[lane];
-          st[kRowsMax + mt * 16 + lane] = ls[lane];
-        }
-        __threadfence();
+      for (int k = 0; k < kGroups; ++k) {
+        f[k] = exp2_approx(sh.merge_m[mt][k][r] - base);
+        l = fmaf(sh.merge_l[mt][k][r], f[k], l);
       }
+      return l;
+    };
+    float* piece = reinterpret_cast<float*>(
+        d.pieces + (size_t)(2 * blockIdx.x + (i0 == 0 ? 1 : 0)) * kPieceBytes);
+    Tok* unit_out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
+#pragma unroll
+    for (int pass = 0; pass < S::kPasses; ++pass) {
+      if (pass > 0) bar_sync(bar, 32 * kGroups);
+#pragma unroll
+      for (int i = 0; i < S::kPass; ++i)
+        buf[(group * S::kPass + i) * 32 + lane] = c.acc[pass * S::kPass + i];
+      bar_sync(bar, 32 * kGroups);
+      const int mine = group * S::kShare, first_i = pass * S::kPass + mine;
+      float f[C::kShareRows][kGroups];
+      int rr[C::kShareRows];
+#pragma unroll
+      for (int q = 0; q < C::kShareRows; ++q) {
+        const int r = C::share_row(first_i, q, lane);
+        rr[q] = mt * 16 + r;
+        float m;
+        const float l = join_row(r, f[q], &m);
+        if (whole) {
+          const float inv = rr[q] < u.rows ? finish(a, u.head0 + rr[q], m, l) : 0.f;
+#pragma unroll
+          for (int k = 0; k < kGroups; ++k) f[q][k] *= inv;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < S::kShare; e += 2) {
+        const int q = C::share_of(e);
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          x = fmaf(buf[(k * S::kPass + mine + e) * 32 + lane], f[q][k], x);
+          y = fmaf(buf[(k * S::kPass + mine + e + 1) * 32 + lane], f[q][k], y);
+        }
+        const int col = C::col(first_i + e, lane);
+        if (rr[q] < u.rows) {
+          if (whole) store_pair(unit_out + (int64_t)rr[q] * D + col, x, y);
+          else *reinterpret_cast<float2*>(piece + rr[q] * D + col) = make_float2(x, y);
+        }
+      }
+    }
+    if (!whole) {
+      if (group == 0 && lane < 16 && mt * 16 + lane < u.rows) {
+        float f[kGroups], m;
+        const float l = join_row(lane, f, &m);
+        piece[kRowsMax * 128 + mt * 16 + lane] = m;
+        piece[kRowsMax * 128 + kRowsMax + mt * 16 + lane] = l;
+      }
+      __threadfence();
     }
     if (!whole) {
       // The unit's CTAs are those that own its tiles' runs; the first owns
@@ -763,7 +795,6 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       if (sh.last) {
         __threadfence();
         const int n = c_last - c_first + 1;
-        Tok* out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
         for (int r = cw; r < u.rows; r += kGroups * kMT) {
           auto piece = [&](int k) {
             return reinterpret_cast<const float*>(
@@ -795,12 +826,10 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
           const float inv = finish(a, u.head0 + r, m, l);
 #pragma unroll
           for (int w = 0; w < D / 32; w += 2)
-            store_pair(out + (int64_t)r * D + lane * (D / 32) + w, o[w] * inv, o[w + 1] * inv);
+            store_pair(unit_out + (int64_t)r * D + lane * (D / 32) + w, o[w] * inv, o[w + 1] * inv);
         }
       }
     }
-    // ms and ls of group 0 are read before the next unit's rounds write them.
-    bar_sync(bar, 32 * kGroups);
   }
   if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
 }
@@ -822,7 +851,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   constexpr size_t smem = 1024 + (size_t)S::kStages * 2 * S::kHalf +
                           (size_t)kQSlots * 16 * kMT * S::kQRow +
-                          (size_t)kMT * 2 * S::kAcc * 32 * 4 +
+                          (size_t)kMT * kGroups * S::kPass * 32 * 4 +
                           (sizeof(Tok) == 4 ? (size_t)kGroups * kMT * 144 * 4 : 0) +
                           sizeof(DecodeShared<kMT>);
   static_assert(smem <= 227 * 1024, "shared memory");
