@@ -63,7 +63,7 @@ static_assert(kMaxCtas <= kDecodeCounters && 2 * kMaxCtas * kPieceBytes <= kPiec
 
 template <typename Tok, int D, int kMT = 1, int kH = 16>
 struct Shape {
-  static constexpr int kTile = sizeof(Tok) == 2 ? 64 : 32;          // keys per tile
+  static constexpr int kTile = sizeof(Tok) == 2 ? 8192 / D : 32;    // keys per tile
   static constexpr int kPer = kTile / kGroups;                      // keys per consumer warp
   static constexpr int kSub = 128 / sizeof(Tok);                    // elements in 128 bytes
   static constexpr int kSubs = D / kSub;                            // 128-byte columns of a row
@@ -212,6 +212,7 @@ struct Consumer;
 template <int D, int kMT>
 struct Consumer<__nv_bfloat16, D, 16, kMT> {
   using S = Shape<__nv_bfloat16, D, kMT>;
+  static constexpr int kB = S::kPer / 16;      // blocks of 16 keys
   uint32_t q[D / 16][4];
   float m[2], l[2];          // rows lane / 4 and lane / 4 + 8; l: this lane's keys only
   float acc[S::kAcc];
@@ -229,32 +230,36 @@ struct Consumer<__nv_bfloat16, D, 16, kMT> {
 #pragma unroll
     for (int i = 0; i < S::kAcc; ++i) acc[i] = 0.f;
   }
-  // vis: bit j set: key j of this warp's 16 is seen (all ones: no mask).
+  // vis: bit j set: key j of this warp's share is seen (all ones: no mask).
   __device__ __forceinline__ void tile(uint32_t k_addr, uint32_t v_addr, int group, int lane,
                                        float scale, uint32_t vis, const DecodeArgs& d, float*) {
     const int x = lane & 7;
     const uint32_t box = (uint32_t)d.box_rows * 128u;
-    const uint32_t krow = k_addr + box_row(group * 16 + (lane >> 4) * 8 + x, d.box_rows,
-                                           d.box_shift, S::kSubs);
-    float s[2][4] = {};
+    float s[2 * kB][4] = {};
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      uint32_t b[4];
-      const int c = (k & 3) * 2 + ((lane >> 3) & 1);
-      ldmatrix_x4(krow + (uint32_t)(k / 4) * box + (uint32_t)((c ^ x) << 4), b);
-      mma_bf16(s[0], q[k], b[0], b[1]);
-      mma_bf16(s[1], q[k], b[2], b[3]);
+    for (int y = 0; y < kB; ++y) {
+      const uint32_t krow = k_addr + box_row(group * S::kPer + y * 16 + (lane >> 4) * 8 + x,
+                                             d.box_rows, d.box_shift, S::kSubs);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        uint32_t b[4];
+        const int c = (k & 3) * 2 + ((lane >> 3) & 1);
+        ldmatrix_x4(krow + (uint32_t)(k / 4) * box + (uint32_t)((c ^ x) << 4), b);
+        mma_bf16(s[2 * y], q[k], b[0], b[1]);
+        mma_bf16(s[2 * y + 1], q[k], b[2], b[3]);
+      }
     }
-    const int j0 = (lane & 3) * 2;       // this lane's keys: j0, j0 + 1, j0 + 8, j0 + 9
+    const int j0 = (lane & 3) * 2;       // this lane's keys: j0, j0 + 1 of each eight
+    float top[2] = {-INFINITY, -INFINITY}, base[2];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int n = 0; n < 2 * kB; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e) {
         s[n][e] = (vis >> (n * 8 + j0 + (e & 1))) & 1u ? s[n][e] * scale : -INFINITY;
-    float top[2], base[2];
+        top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+      }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
       top[r] = fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 1));
       top[r] = fmaxf(m[r], fmaxf(top[r], __shfl_xor_sync(kFullMask, top[r], 2)));
     }
@@ -270,40 +275,45 @@ struct Consumer<__nv_bfloat16, D, 16, kMT> {
         m[r] = top[r];
       }
     }
-    uint32_t p[4];
+    uint32_t p[kB][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       base[r] = top[r] == -INFINITY ? 0.f : top[r];
 #pragma unroll
-      for (int n = 0; n < 2; ++n) {
+      for (int n = 0; n < 2 * kB; ++n) {
         const uint32_t w = pack_bf16(exp2_approx(s[n][2 * r] - base[r]),
                                      exp2_approx(s[n][2 * r + 1] - base[r]));
         l[r] += bf16_lo(w) + bf16_hi(w);
-        p[2 * n + r] = w;
+        p[n / 2][2 * (n & 1) + r] = w;
       }
     }
     // Values of keys that are not seen may be anything: they count as zeros.
-    uint32_t keep[2];
+    constexpr uint32_t kAll = kB == 2 ? 0xffffffffu : 0xffffu;
+    const bool whole = (vis & kAll) == kAll;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
-      keep[n] = ((vis >> (n * 8 + j0)) & 1u ? 0x0000ffffu : 0u) |
-                ((vis >> (n * 8 + j0 + 1)) & 1u ? 0xffff0000u : 0u);
-    const bool whole = (vis & 0xffffu) == 0xffffu;
-    const uint32_t vrow = v_addr + box_row(group * 16 + ((lane >> 3) & 1) * 8 + x, d.box_rows,
-                                           d.box_shift, S::kSubs);
+    for (int y = 0; y < kB; ++y) {
+      uint32_t keep[2];
 #pragma unroll
-    for (int n = 0; n < D / 16; ++n) {
-      uint32_t b[4];
-      const int c = (n & 3) * 2 + (lane >> 4);
-      ldmatrix_x4_trans(vrow + (uint32_t)(n / 4) * box + (uint32_t)((c ^ x) << 4), b);
-      if (!whole) {
-        b[0] &= keep[0];
-        b[1] &= keep[1];
-        b[2] &= keep[0];
-        b[3] &= keep[1];
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t pair = vis >> (y * 16 + n * 8 + j0);
+        keep[n] = (pair & 1u ? 0x0000ffffu : 0u) | (pair & 2u ? 0xffff0000u : 0u);
       }
-      mma_bf16(acc + 8 * n, p, b[0], b[1]);
-      mma_bf16(acc + 8 * n + 4, p, b[2], b[3]);
+      const uint32_t vrow = v_addr + box_row(group * S::kPer + y * 16 + ((lane >> 3) & 1) * 8 + x,
+                                             d.box_rows, d.box_shift, S::kSubs);
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        const int c = (n & 3) * 2 + (lane >> 4);
+        ldmatrix_x4_trans(vrow + (uint32_t)(n / 4) * box + (uint32_t)((c ^ x) << 4), b);
+        if (!whole) {
+          b[0] &= keep[0];
+          b[1] &= keep[1];
+          b[2] &= keep[0];
+          b[3] &= keep[1];
+        }
+        mma_bf16(acc + 8 * n, p[y], b[0], b[1]);
+        mma_bf16(acc + 8 * n + 4, p[y], b[2], b[3]);
+      }
     }
   }
   // The rows that a share of the result holds: element e of the share that
@@ -581,15 +591,15 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
 
   if (warp == 0) {
     // ------------------------------------------------------------- producer
-    // Lanes 0 to 15 each copy one box of a tile: lane & 7 says which, lane >> 3
+    // Each lane copies one box of a tile at most: lane & 15 says which, lane >> 4
     // keys or values. The ids of the next tile's pages are on their way while
     // this one waits for room.
-    static_assert(S::kTile / 8 <= 8, "boxes of a tile (pages have 8 slots at least)");
+    static_assert(S::kTile / 8 <= 16, "boxes of a tile (pages have 8 slots at least)");
     bool ok = true;
     int stage = 0, slot = 0;
     uint32_t phase = 0, q_phase = 0;
     const uint64_t once = l2_evict_first_policy(), keep = l2_evict_normal_policy();
-    const int x = (lane & 7) << d.box_shift, half = lane >> 3;
+    const int x = (lane & 15) << d.box_shift, half = lane >> 4;
     const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
     const CUtensorMap* map = half == 0 ? &maps.k : &maps.v;
     Walk<S::kTile, kMT> w;
@@ -604,7 +614,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         const int j0 = (i < u.sink_tiles ? i : u.first_tile + i - u.sink_tiles) * S::kTile;
         const int k0 = j0 + x, k1 = min(k0 + d.box_rows, u.len);
         const bool seen =
-            half < 2 && x < S::kTile && k0 < k1 && (k1 > u.lo || k0 < a.sinks);
+            x < S::kTile && k0 < k1 && (k1 > u.lo || k0 < a.sinks);
         if (seen) *id = __ldg(table + (k0 >> a.cache.page_shift));
         *s0 = k0 & (a.cache.page_size - 1);
         return seen;
