@@ -49,7 +49,6 @@
 namespace mxfp4el {
 namespace {
 
-constexpr int kGroups = 4;              // key groups of a tile: one consumer warp each per 16 heads
 constexpr int kMinTiles = 4;            // tiles per run at least (see above)
 constexpr int kWholeTiles = 8;
 constexpr int kMaxCtas = 256;
@@ -63,7 +62,14 @@ static_assert(kMaxCtas <= kDecodeCounters && 2 * kMaxCtas * kPieceBytes <= kPiec
 
 template <typename Tok, int D, int kMT = 1, int kH = 16>
 struct Shape {
-  static constexpr int kTile = sizeof(Tok) == 2 ? 8192 / D : 32;    // keys per tile
+  // Key groups of a tile: one consumer warp each per 16 heads. float32 works
+  // on the CUDA cores and needs more of them: 26 sequences of up to 57434 keys,
+  // heads of 64: 147 us with four groups, 111 with eight. bf16 does not (139
+  // sequences of up to 1384 keys, heads of 64: 48.2 us with four, 52.0 with
+  // eight, whose join is longer).
+  static constexpr int kGroups = sizeof(Tok) == 4 && kMT == 1 ? 8 : 4;
+  // 32 KB of keys and values in a tile, or eight float32 keys a group.
+  static constexpr int kTile = sizeof(Tok) == 2 ? 8192 / D : kGroups * 8;   // keys per tile
   static constexpr int kPer = kTile / kGroups;                      // keys per consumer warp
   static constexpr int kSub = 128 / sizeof(Tok);                    // elements in 128 bytes
   static constexpr int kSubs = D / kSub;                            // 128-byte columns of a row
@@ -74,10 +80,11 @@ struct Shape {
       (kMT == 1 ? 5 : kMT == 2 ? 4 : sizeof(Tok) == 2 ? 3 : 2) * 32768 / (2 * (int)kHalf);
   static constexpr int kQRow = D * (int)sizeof(Tok) + 16;           // padded row in shared memory
   static constexpr int kAcc = kH * D / 32;                          // result elements per lane
-  // The join of a unit's four warps goes through shared memory in kPasses
+  // The join of a unit's warps goes through shared memory in kPasses
   // parts of kPass elements, of which each warp finishes kShare.
-  static constexpr int kPasses = kMT == 4 || (kMT == 2 && sizeof(Tok) == 4) ? 2 : 1;
-  static constexpr int kPass = kAcc / kPasses, kShare = kPass / kGroups;
+  static constexpr int kPasses = kAcc == 64 || kMT == 4 || (kMT == 2 && sizeof(Tok) == 4) ? 2 : 1;
+  static constexpr int kPass = kAcc / kPasses;
+  static constexpr int kShare = kPass / kGroups >= 2 ? kPass / kGroups : 2;
 };
 
 struct Unit {
@@ -101,14 +108,14 @@ struct DecodeMaps {
   CUtensorMap k, v;       // (128 bytes, slot, 128-byte column, head, page), 128-byte swizzle
 };
 
-template <int kMT>
+template <int kMT, int kGroups>
 struct __align__(16) DecodeShared {
   uint64_t full[16], empty[16];
   uint64_t q_full[kQSlots], q_empty[kQSlots];
   float merge_m[kMT][kGroups][16], merge_l[kMT][kGroups][16];
   int last;
-  long long scan[8 + 4 * kMT];
-  int longest[8 + 4 * kMT];
+  long long scan[1 + kGroups * kMT];  // per warp
+  int longest[1 + kGroups * kMT];
   long long prefix[kMaxSeqs + 1];     // tiles of all units before sequence b
 };
 
@@ -146,17 +153,17 @@ struct Walk {
     u.rows = min(16 * kMT, d.a.group - blk * 16 * kMT);
   }
   // The unit that holds `tile`.
-  __device__ __forceinline__ void start(const DecodeArgs& d, const DecodeShared<kMT>& sh,
+  __device__ __forceinline__ void start(const DecodeArgs& d, const long long* prefix,
                                         long long tile) {
     int lo = 0, hi = d.num_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (sh.prefix[mid] <= tile) lo = mid;
+      if (prefix[mid] <= tile) lo = mid;
       else hi = mid;
     }
     sequence(d, lo);
-    i = (int)((tile - sh.prefix[lo]) / u.tiles);
-    first = sh.prefix[lo] + (long long)i * u.tiles;
+    i = (int)((tile - prefix[lo]) / u.tiles);
+    first = prefix[lo] + (long long)i * u.tiles;
     unit(d);
   }
   __device__ __forceinline__ void next(const DecodeArgs& d) {
@@ -459,7 +466,7 @@ struct Consumer<float, D, kH, kMT> {
       }
     }
   }
-  static constexpr int kShareRows = S::kShare / kW;
+  static constexpr int kShareRows = S::kShare < kW ? 1 : S::kShare / kW;
   static constexpr __device__ __forceinline__ int share_of(int e) { return e / kW; }
   static __device__ __forceinline__ int share_row(int first, int q, int) { return first / kW + q; }
   __device__ __forceinline__ void stats(float* ms, float* ls, int lane) {
@@ -501,18 +508,18 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, fl
 }
 
 template <typename Tok, int D, int kMT, int kH>
-__global__ void __launch_bounds__(32 * (1 + kGroups * kMT), 1)
+__global__ void __launch_bounds__(32 * (1 + Shape<Tok, D, kMT, kH>::kGroups * kMT), 1)
 attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArgs d) {
   using S = Shape<Tok, D, kMT, kH>;
-  constexpr int kThreads = 32 * (1 + kGroups * kMT), kConsumers = kThreads - 32;
+  constexpr int kThreads = 32 * (1 + S::kGroups * kMT), kConsumers = kThreads - 32;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* q_smem = ring + (size_t)S::kStages * 2 * S::kHalf;
   float* merge = reinterpret_cast<float*>(q_smem + kQSlots * 16 * kMT * S::kQRow);
-  float* p_smem = merge + (size_t)kMT * kGroups * S::kPass * 32;     // float32: p per warp
+  float* p_smem = merge + (size_t)kMT * S::kGroups * S::kPass * 32;     // float32: p per warp
   constexpr int kPFloats = sizeof(Tok) == 4 ? 144 : 0;
-  DecodeShared<kMT>& sh =
-      *reinterpret_cast<DecodeShared<kMT>*>(p_smem + kGroups * kMT * kPFloats);
+  DecodeShared<kMT, S::kGroups>& sh =
+      *reinterpret_cast<DecodeShared<kMT, S::kGroups>*>(p_smem + S::kGroups * kMT * kPFloats);
   const AttnArgs& a = d.a;
   const int warp = __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -522,11 +529,11 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     prefetch_tensor_map(&maps.v);
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], kGroups * kMT);
+      mbar_init(&sh.empty[s], S::kGroups * kMT);
     }
     for (int s = 0; s < kQSlots; ++s) {
       mbar_init(&sh.q_full[s], 1);
-      mbar_init(&sh.q_empty[s], kGroups * kMT);
+      mbar_init(&sh.q_empty[s], S::kGroups * kMT);
     }
     fence_mbar_init();
   }
@@ -603,7 +610,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
     const CUtensorMap* map = half == 0 ? &maps.k : &maps.v;
     Walk<S::kTile, kMT> w;
-    w.start(d, sh, t0);
+    w.start(d, sh.prefix, t0);
     for (long long t = t0; t < t1 && ok; w.next(d)) {
       const Unit u = w.u;
       const int i0 = (int)(t - w.first), i1 = (int)min((long long)u.tiles, t1 - w.first);
@@ -671,9 +678,9 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   // A wait that gives up is recorded; the warp then goes on without waiting,
   // so that every warp still reaches every barrier and the workspace's
   // counters end as they should.
-  const int cw = warp - 1, group = cw % kGroups, mt = cw / kGroups;
-  const int bar = 1 + mt;                                   // the four warps of 16 heads
-  float* buf = merge + (size_t)mt * kGroups * S::kPass * 32;
+  const int cw = warp - 1, group = cw % S::kGroups, mt = cw / S::kGroups;
+  const int bar = 1 + mt;                                   // the warps of 16 heads
+  float* buf = merge + (size_t)mt * S::kGroups * S::kPass * 32;
   float* p_warp = p_smem + cw * kPFloats;
   const float scale = a.scale * kLog2e;
   using C = Consumer<Tok, D, kH, kMT>;
@@ -682,7 +689,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   int stage = 0, slot = 0;
   uint32_t phase = 0, q_phase = 0;
   Walk<S::kTile, kMT> walk;
-  walk.start(d, sh, t0);
+  walk.start(d, sh.prefix, t0);
   for (long long t = t0; t < t1; walk.next(d)) {
     const Unit u = walk.u;
     const long long first = walk.first;
@@ -724,20 +731,20 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       q_phase ^= 1u;
     }
 
-    // The four warps' (m, l, o) meet in shared memory, and each warp joins and
-    // writes a quarter of the result.
+    // The warps' (m, l, o) meet in shared memory, and each warp joins and
+    // writes a share of the result.
     const bool whole = i0 == 0 && i1 == u.tiles;
-    bar_sync(bar, 32 * kGroups);                 // the last unit's have been read
+    bar_sync(bar, 32 * S::kGroups);                 // the last unit's have been read
     c.stats(sh.merge_m[mt][group], sh.merge_l[mt][group], lane);
     // Row r: the warps' factors, the common maximum and the sum.
-    auto join_row = [&](int r, float (&f)[kGroups], float* m) {
+    auto join_row = [&](int r, float (&f)[S::kGroups], float* m) {
       *m = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k) *m = fmaxf(*m, sh.merge_m[mt][k][r]);
+      for (int k = 0; k < S::kGroups; ++k) *m = fmaxf(*m, sh.merge_m[mt][k][r]);
       const float base = *m == -INFINITY ? 0.f : *m;
       float l = 0.f;
 #pragma unroll
-      for (int k = 0; k < kGroups; ++k) {
+      for (int k = 0; k < S::kGroups; ++k) {
         f[k] = exp2_approx(sh.merge_m[mt][k][r] - base);
         l = fmaf(sh.merge_l[mt][k][r], f[k], l);
       }
@@ -748,13 +755,15 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     Tok* unit_out = static_cast<Tok*>(a.out) + ((int64_t)(d.seq0 + u.b) * a.heads + u.head0) * D;
 #pragma unroll
     for (int pass = 0; pass < S::kPasses; ++pass) {
-      if (pass > 0) bar_sync(bar, 32 * kGroups);
+      if (pass > 0) bar_sync(bar, 32 * S::kGroups);
 #pragma unroll
       for (int i = 0; i < S::kPass; ++i)
         buf[(group * S::kPass + i) * 32 + lane] = c.acc[pass * S::kPass + i];
-      bar_sync(bar, 32 * kGroups);
-      const int mine = group * S::kShare, first_i = pass * S::kPass + mine;
-      float f[C::kShareRows][kGroups];
+      bar_sync(bar, 32 * S::kGroups);
+      const int mine = group * S::kShare;
+      if (mine >= S::kPass) continue;
+      const int first_i = pass * S::kPass + mine;
+      float f[C::kShareRows][S::kGroups];
       int rr[C::kShareRows];
 #pragma unroll
       for (int q = 0; q < C::kShareRows; ++q) {
@@ -765,7 +774,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         if (whole) {
           const float inv = rr[q] < u.rows ? finish(a, u.head0 + rr[q], m, l) : 0.f;
 #pragma unroll
-          for (int k = 0; k < kGroups; ++k) f[q][k] *= inv;
+          for (int k = 0; k < S::kGroups; ++k) f[q][k] *= inv;
         }
       }
 #pragma unroll
@@ -773,7 +782,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         const int q = C::share_of(e);
         float x = 0.f, y = 0.f;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
+        for (int k = 0; k < S::kGroups; ++k) {
           x = fmaf(buf[(k * S::kPass + mine + e) * 32 + lane], f[q][k], x);
           y = fmaf(buf[(k * S::kPass + mine + e + 1) * 32 + lane], f[q][k], y);
         }
@@ -786,7 +795,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     }
     if (!whole) {
       if (group == 0 && lane < 16 && mt * 16 + lane < u.rows) {
-        float f[kGroups], m;
+        float f[S::kGroups], m;
         const float l = join_row(lane, f, &m);
         piece[kRowsMax * 128 + mt * 16 + lane] = m;
         piece[kRowsMax * 128 + kRowsMax + mt * 16 + lane] = l;
@@ -805,7 +814,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       if (sh.last) {
         __threadfence();
         const int n = c_last - c_first + 1;
-        for (int r = cw; r < u.rows; r += kGroups * kMT) {
+        for (int r = cw; r < u.rows; r += S::kGroups * kMT) {
           auto piece = [&](int k) {
             return reinterpret_cast<const float*>(
                 d.pieces + (size_t)(2 * (c_first + k) + (k == 0 ? 1 : 0)) * kPieceBytes);
@@ -861,9 +870,9 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   constexpr size_t smem = 1024 + (size_t)S::kStages * 2 * S::kHalf +
                           (size_t)kQSlots * 16 * kMT * S::kQRow +
-                          (size_t)kMT * kGroups * S::kPass * 32 * 4 +
-                          (sizeof(Tok) == 4 ? (size_t)kGroups * kMT * 144 * 4 : 0) +
-                          sizeof(DecodeShared<kMT>);
+                          (size_t)kMT * S::kGroups * S::kPass * 32 * 4 +
+                          (sizeof(Tok) == 4 ? (size_t)S::kGroups * kMT * 144 * 4 : 0) +
+                          sizeof(DecodeShared<kMT, S::kGroups>);
   static_assert(smem <= 227 * 1024, "shared memory");
   static std::once_flag once[64];
   int dev = 0;
@@ -884,7 +893,7 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     const int64_t most = std::max(units, (units * room + kMinTiles - 1) / kMinTiles);
     const int grid = (int)std::min<int64_t>(std::min(attention_num_sms(), kMaxCtas), most);
     err = launch_after_previous(attention_decode_kernel<Tok, D, kMT, kH>, dim3((unsigned)grid),
-                                dim3(32 * (1 + kGroups * kMT)), smem, stream, maps, d);
+                                dim3(32 * (1 + S::kGroups * kMT)), smem, stream, maps, d);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
