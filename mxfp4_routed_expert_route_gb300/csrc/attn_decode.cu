@@ -43,6 +43,7 @@
 #include <algorithm>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "attn.cuh"
 
@@ -82,7 +83,8 @@ struct Shape {
   static constexpr int kAcc = kH * D / 32;                          // result elements per lane
   // The join of a unit's warps goes through shared memory in kPasses
   // parts of kPass elements, of which each warp finishes kShare.
-  static constexpr int kPasses = kAcc == 64 || kMT == 4 || (kMT == 2 && sizeof(Tok) == 4) ? 2 : 1;
+  static constexpr int kPasses =
+      kMT == 4 || (sizeof(Tok) == 4 && (kMT == 2 || kAcc == 64)) ? 2 : 1;
   static constexpr int kPass = kAcc / kPasses;
   static constexpr int kShare = kPass / kGroups >= 2 ? kPass / kGroups : 2;
 };
@@ -135,6 +137,12 @@ __device__ __forceinline__ void tiles_of(const AttnArgs& a, int n, int* lo, int*
   *tiles = max(1, *sink_tiles + (n + kTile - 1) / kTile - *first_tile);
 }
 
+// a / b of counts of tiles, which nearly always fit 32 bits: the 64-bit
+// division costs some 300 cycles, and the first copy waits for several.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The units of a run, one after another.
 template <int kTile, int kMT>
 struct Walk {
@@ -162,15 +170,16 @@ struct Walk {
       else hi = mid;
     }
     sequence(d, lo);
-    i = (int)((tile - prefix[lo]) / u.tiles);
+    i = (int)divide(tile - prefix[lo], u.tiles);
     first = prefix[lo] + (long long)i * u.tiles;
     unit(d);
   }
-  __device__ __forceinline__ void next(const DecodeArgs& d) {
+  __device__ __forceinline__ void next(const DecodeArgs& d, long long end) {
     first += u.tiles;
+    if (first >= end) return;
     if (++i == d.units_per_seq) {
       i = 0;
-      if (u.b + 1 < d.num_seqs) sequence(d, u.b + 1);
+      sequence(d, u.b + 1);
     }
     unit(d);
   }
@@ -577,7 +586,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     __syncthreads();
   }
   const long long total = sh.prefix[d.num_seqs];
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)kMinTiles);
+  const long long per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
   long long t0 = per * blockIdx.x, t1 = min(t0 + per, total);
   int longest = 0;
 #pragma unroll
@@ -586,13 +595,13 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     // Whole units: from unit units b / grid to the next CTA's first.
     const long long units = (long long)d.num_seqs * d.units_per_seq;
     auto first_tile = [&](long long unit) {
-      const int b = (int)(unit / d.units_per_seq);
+      const int b = (int)divide(unit, d.units_per_seq);
       if (b >= d.num_seqs) return total;
       return sh.prefix[b] + (unit - (long long)b * d.units_per_seq) *
-                                ((sh.prefix[b + 1] - sh.prefix[b]) / d.units_per_seq);
+                                divide(sh.prefix[b + 1] - sh.prefix[b], d.units_per_seq);
     };
-    t0 = first_tile(units * blockIdx.x / gridDim.x);
-    t1 = first_tile(units * (blockIdx.x + 1) / gridDim.x);
+    t0 = first_tile(divide(units * blockIdx.x, gridDim.x));
+    t1 = first_tile(divide(units * (blockIdx.x + 1), gridDim.x));
   }
   if (t0 >= t1) return;
 
@@ -611,7 +620,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     const CUtensorMap* map = half == 0 ? &maps.k : &maps.v;
     Walk<S::kTile, kMT> w;
     w.start(d, sh.prefix, t0);
-    for (long long t = t0; t < t1 && ok; w.next(d)) {
+    for (long long t = t0; t < t1 && ok; w.next(d, t1)) {
       const Unit u = w.u;
       const int i0 = (int)(t - w.first), i1 = (int)min((long long)u.tiles, t1 - w.first);
       t = w.first + i1;
@@ -690,7 +699,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   uint32_t phase = 0, q_phase = 0;
   Walk<S::kTile, kMT> walk;
   walk.start(d, sh.prefix, t0);
-  for (long long t = t0; t < t1; walk.next(d)) {
+  for (long long t = t0; t < t1; walk.next(d, t1)) {
     const Unit u = walk.u;
     const long long first = walk.first;
     const int i0 = (int)(t - first), i1 = (int)min((long long)u.tiles, t1 - first);
@@ -805,7 +814,8 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     if (!whole) {
       // The unit's CTAs are those that own its tiles' runs; the first owns
       // the counter. The last to arrive joins.
-      const int c_first = (int)(first / per), c_last = (int)((first + u.tiles - 1) / per);
+      const int c_first = (int)divide(first, per),
+                c_last = (int)divide(first + u.tiles - 1, per);
       bar_sync(1 + kMT, kConsumers);
       if (cw == 0 && lane == 0)
         sh.last = atomicInc(d.counters + c_first, (unsigned)(c_last - c_first)) ==
@@ -814,39 +824,66 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       if (sh.last) {
         __threadfence();
         const int n = c_last - c_first + 1;
-        for (int r = cw; r < u.rows; r += S::kGroups * kMT) {
-          auto piece = [&](int k) {
-            return reinterpret_cast<const float*>(
-                d.pieces + (size_t)(2 * (c_first + k) + (k == 0 ? 1 : 0)) * kPieceBytes);
-          };
-          float m = -INFINITY;
-          for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(piece(k) + kRowsMax * 128 + r));
+        auto piece = [&](int k) {
+          return reinterpret_cast<const float*>(
+              d.pieces + (size_t)(2 * (c_first + k) + (k == 0 ? 1 : 0)) * kPieceBytes);
+        };
+        // kR rows of the result a warp at a time, their reads in flight
+        // together.
+        constexpr int kStep = S::kGroups * kMT;
+        auto join = [&](auto rows_at_once) {
+          constexpr int kR = decltype(rows_at_once)::value;
+          for (int r0 = cw; r0 < u.rows; r0 += kStep * kR) {
+            int rr[kR];
+            float m[kR], l[kR] = {}, o[kR][D / 32] = {};
 #pragma unroll
-          for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-          const float base = m == -INFINITY ? 0.f : m;
-          float l = 0.f, o[D / 32] = {};
-#pragma unroll 4
-          for (int k = 0; k < n; ++k) {
-            const float* pk = piece(k);
-            const float f = exp2_approx(__ldcg(pk + kRowsMax * 128 + r) - base);
-            l = fmaf(__ldcg(pk + kRowsMax * 128 + kRowsMax + r), f, l);
-            if constexpr (D == 128) {
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(pk + r * D) + lane);
-              o[0] = fmaf(x.x, f, o[0]);
-              o[1] = fmaf(x.y, f, o[1]);
-              o[2] = fmaf(x.z, f, o[2]);
-              o[3] = fmaf(x.w, f, o[3]);
-            } else {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(pk + r * D) + lane);
-              o[0] = fmaf(x.x, f, o[0]);
-              o[1] = fmaf(x.y, f, o[1]);
+            for (int q = 0; q < kR; ++q) {
+              rr[q] = min(r0 + q * kStep, u.rows - 1);
+              m[q] = -INFINITY;
+            }
+            for (int k = lane; k < n; k += 32)
+#pragma unroll
+              for (int q = 0; q < kR; ++q)
+                m[q] = fmaxf(m[q], __ldcg(piece(k) + kRowsMax * 128 + rr[q]));
+#pragma unroll
+            for (int s = 16; s >= 1; s >>= 1)
+#pragma unroll
+              for (int q = 0; q < kR; ++q)
+                m[q] = fmaxf(m[q], __shfl_xor_sync(kFullMask, m[q], s));
+#pragma unroll(kR == 1 ? 4 : 2)
+            for (int k = 0; k < n; ++k) {
+              const float* pk = piece(k);
+#pragma unroll
+              for (int q = 0; q < kR; ++q) {
+                const float base = m[q] == -INFINITY ? 0.f : m[q];
+                const float f = exp2_approx(__ldcg(pk + kRowsMax * 128 + rr[q]) - base);
+                l[q] = fmaf(__ldcg(pk + kRowsMax * 128 + kRowsMax + rr[q]), f, l[q]);
+                if constexpr (D == 128) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(pk + rr[q] * D) + lane);
+                  o[q][0] = fmaf(x.x, f, o[q][0]);
+                  o[q][1] = fmaf(x.y, f, o[q][1]);
+                  o[q][2] = fmaf(x.z, f, o[q][2]);
+                  o[q][3] = fmaf(x.w, f, o[q][3]);
+                } else {
+                  const float2 x = __ldcg(reinterpret_cast<const float2*>(pk + rr[q] * D) + lane);
+                  o[q][0] = fmaf(x.x, f, o[q][0]);
+                  o[q][1] = fmaf(x.y, f, o[q][1]);
+                }
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < kR; ++q) {
+              if (r0 + q * kStep >= u.rows) break;
+              const float inv = finish(a, u.head0 + rr[q], m[q], l[q]);
+#pragma unroll
+              for (int w = 0; w < D / 32; w += 2)
+                store_pair(unit_out + (int64_t)rr[q] * D + lane * (D / 32) + w, o[q][w] * inv,
+                           o[q][w + 1] * inv);
             }
           }
-          const float inv = finish(a, u.head0 + r, m, l);
-#pragma unroll
-          for (int w = 0; w < D / 32; w += 2)
-            store_pair(unit_out + (int64_t)r * D + lane * (D / 32) + w, o[w] * inv, o[w + 1] * inv);
-        }
+        };
+        if (kMT > 1 || u.rows <= kStep) join(std::integral_constant<int, 1>());
+        else join(std::integral_constant<int, 2>());
       }
     }
   }
