@@ -101,6 +101,8 @@ struct DecodeArgs {
   int seq0, num_seqs;     // sequences of this launch
   int units_per_seq;      // key heads x head blocks
   int head_blocks;
+  long long units_per_cta;     // all units / CTAs, and the remainder
+  int units_over;
   int box_rows, box_shift;     // slots per tensor copy: min(page_size, kTile)
   unsigned int* counters;
   unsigned char* pieces;
@@ -118,7 +120,7 @@ struct __align__(16) DecodeShared {
   int last;
   long long scan[1 + kGroups * kMT];  // per warp
   int longest[1 + kGroups * kMT];
-  long long prefix[kMaxSeqs + 1];     // tiles of all units before sequence b
+  long long prefix[kMaxSeqs + 1];     // tiles of one unit of each sequence before b
 };
 
 __device__ __forceinline__ int sequence_len(const DecodeArgs& d, int b) {
@@ -160,18 +162,21 @@ struct Walk {
     u.head0 = u.kvh * d.a.group + blk * 16 * kMT;
     u.rows = min(16 * kMT, d.a.group - blk * 16 * kMT);
   }
-  // The unit that holds `tile`.
+  // The unit that holds `tile`; called by a whole warp.
   __device__ __forceinline__ void start(const DecodeArgs& d, const long long* prefix,
-                                        long long tile) {
-    int lo = 0, hi = d.num_seqs;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= tile) lo = mid;
-      else hi = mid;
-    }
-    sequence(d, lo);
-    i = (int)divide(tile - prefix[lo], u.tiles);
-    first = prefix[lo] + (long long)i * u.tiles;
+                                        long long tile, int lane) {
+    const int step = (d.num_seqs + 31) / 32;
+    auto before = [&](int b, bool in) {          // the entries at or before `tile`, less one
+      return __popc(__ballot_sync(kFullMask, in && b < d.num_seqs &&
+                                                 prefix[b] * d.units_per_seq <= tile)) - 1;
+    };
+    static_assert(kMaxSeqs <= 32 * 32, "two steps");
+    int b = step * before(lane * step, true);
+    b += before(b + lane, lane < step);
+    sequence(d, b);
+    first = prefix[b] * d.units_per_seq;
+    i = (int)divide(tile - first, u.tiles);
+    first += (long long)i * u.tiles;
     unit(d);
   }
   __device__ __forceinline__ void next(const DecodeArgs& d, long long end) {
@@ -561,7 +566,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       tiles_of<S::kTile>(a, n, &lo, &st, &ft, &tiles);
       if (blockIdx.x == 0 && __ldg(a.seqs.seq_lens + d.seq0 + b) > n)
         atomicAdd(&a.status[kStatusBadPages], 1ull);
-      mine += (long long)tiles * d.units_per_seq;
+      mine += tiles;
       most = max(most, tiles);
     }
     most = __reduce_max_sync(kFullMask, most);
@@ -580,28 +585,29 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
       int lo, st, ft, tiles;
       tiles_of<S::kTile>(a, sequence_len(d, b), &lo, &st, &ft, &tiles);
       sh.prefix[b] = run;
-      run += (long long)tiles * d.units_per_seq;
+      run += tiles;
     }
     if (b1 == d.num_seqs && b0 < b1) sh.prefix[d.num_seqs] = run;
     __syncthreads();
   }
-  const long long total = sh.prefix[d.num_seqs];
+  const long long total = sh.prefix[d.num_seqs] * d.units_per_seq;
   const long long per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
   long long t0 = per * blockIdx.x, t1 = min(t0 + per, total);
   int longest = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, sh.longest[w]);
   if (longest <= kWholeTiles) {
-    // Whole units: from unit units b / grid to the next CTA's first.
-    const long long units = (long long)d.num_seqs * d.units_per_seq;
+    // Whole units: units_per_cta each, and one more for the first CTAs.
+    const long long mine = d.units_per_cta * blockIdx.x +
+                           min((int)blockIdx.x, d.units_over);
     auto first_tile = [&](long long unit) {
       const int b = (int)divide(unit, d.units_per_seq);
       if (b >= d.num_seqs) return total;
-      return sh.prefix[b] + (unit - (long long)b * d.units_per_seq) *
-                                divide(sh.prefix[b + 1] - sh.prefix[b], d.units_per_seq);
+      return sh.prefix[b] * d.units_per_seq + (unit - (long long)b * d.units_per_seq) *
+                                                  (sh.prefix[b + 1] - sh.prefix[b]);
     };
-    t0 = first_tile(divide(units * blockIdx.x, gridDim.x));
-    t1 = first_tile(divide(units * (blockIdx.x + 1), gridDim.x));
+    t0 = first_tile(mine);
+    t1 = first_tile(mine + d.units_per_cta + ((int)blockIdx.x < d.units_over ? 1 : 0));
   }
   if (t0 >= t1) return;
 
@@ -619,7 +625,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
     const uint32_t box_bytes = (uint32_t)d.box_rows * D * sizeof(Tok);
     const CUtensorMap* map = half == 0 ? &maps.k : &maps.v;
     Walk<S::kTile, kMT> w;
-    w.start(d, sh.prefix, t0);
+    w.start(d, sh.prefix, t0, lane);
     for (long long t = t0; t < t1 && ok; w.next(d, t1)) {
       const Unit u = w.u;
       const int i0 = (int)(t - w.first), i1 = (int)min((long long)u.tiles, t1 - w.first);
@@ -698,7 +704,7 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
   int stage = 0, slot = 0;
   uint32_t phase = 0, q_phase = 0;
   Walk<S::kTile, kMT> walk;
-  walk.start(d, sh.prefix, t0);
+  walk.start(d, sh.prefix, t0, lane);
   for (long long t = t0; t < t1; walk.next(d, t1)) {
     const Unit u = walk.u;
     const long long first = walk.first;
@@ -929,6 +935,8 @@ cudaError_t launch(const AttnArgs& a, void* workspace, cudaStream_t stream) {
     const int64_t units = (int64_t)d.num_seqs * d.units_per_seq;
     const int64_t most = std::max(units, (units * room + kMinTiles - 1) / kMinTiles);
     const int grid = (int)std::min<int64_t>(std::min(attention_num_sms(), kMaxCtas), most);
+    d.units_per_cta = units / grid;
+    d.units_over = (int)(units % grid);
     err = launch_after_previous(attention_decode_kernel<Tok, D, kMT, kH>, dim3((unsigned)grid),
                                 dim3(32 * (1 + S::kGroups * kMT)), smem, stream, maps, d);
     if (err != cudaSuccess) return err;
