@@ -12,9 +12,9 @@
 // Bound: bytes. A unit reads 2 len D elements of cache and does 2 len D
 // multiply-adds a row, a few operations per byte, so the design is about
 // keeping HBM busy: one warp issues tensor copies of whole pages into a ring
-// of stages and never computes; four warps per 16 heads consume. 128 sequences
-// of up to 16384 keys, 8 key heads of 128: 647 us, 6.7 TB/s, as fast as a plain
-// copy; two of up to 131072: 162 us, 6.5 TB/s, of which the launch and the join
+// of stages and never computes; four or eight warps per 16 heads consume. 128
+// sequences of up to 16384 keys, 8 key heads of 128: 621 us, 7.0 TB/s, a little
+// above a plain copy; two of up to 131072: 160 us, 6.6 TB/s, of which the launch and the join
 // take about 5; DRAM reads 1.00 times the keys and values.
 //
 // Split. Lengths live on the device, so the host launches a fixed grid and
@@ -23,11 +23,11 @@
 // finished there. Otherwise each of its CTAs writes an unnormalised piece
 // (m, l, o) to the workspace, and the CTA that arrives last joins the pieces
 // in their order along the keys, so the result does not depend on who is
-// last. A join costs a round trip through L2, about what three tiles cost, so
-// runs hold at least kMinTiles tiles, and where no unit has more than
-// kWholeTiles the units are dealt out whole instead (one sequence of 333 keys,
-// 8 key heads: 12.0 us with joins, 11.4 without; 16 sequences of up to 132
-// visible keys: 11.9 and 8.3).
+// last. A join costs round trips through L2, so runs hold at least kMinTiles tiles
+// (one sequence of 1000 keys: 8.5 us with two, 9.2 with four, 12.6 with six), and
+// where no unit has more than kWholeTiles the units are dealt out whole instead
+// (one sequence of 333 keys, 8 key heads: 11.1 us with joins, 8.0 without; 16
+// sequences of up to 132 visible keys: 11.7 and 6.9).
 //
 // Matrix products. bf16: mma.sync m16n8k16 with the 16 heads as rows. The
 // legacy tensor path is enough here (two instructions per key and 16 heads
@@ -50,7 +50,7 @@
 namespace mxfp4el {
 namespace {
 
-constexpr int kMinTiles = 4;            // tiles per run at least (see above)
+constexpr int kMinTiles = 2;            // tiles per run at least (see above)
 constexpr int kWholeTiles = 8;
 constexpr int kMaxCtas = 256;
 constexpr int kMaxSeqs = 1024;          // sequences per launch (the prefix sums' shared memory)
