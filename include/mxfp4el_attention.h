@@ -70,7 +70,7 @@ typedef struct mxfp4el_kv_cache {
  *
  * A page id outside [0, num_pages) is not followed: attention takes its keys
  * and values as zeros, the append drops the token's key and value. A length
- * beyond max_pages * page_size is cut to it. Each is counted for
+ * beyond max_pages * page_size, or beyond 2^30, is cut to it. Each is counted for
  * mxfp4el_page_errors() where it is met.
  */
 typedef struct mxfp4el_sequences {

@@ -37,6 +37,11 @@ __device__ __forceinline__ int first_row(const SequencesView& s, int b, int T) {
   return s.q_offsets == nullptr ? min(b, T) : min(max(__ldg(s.q_offsets + b), 0), T);
 }
 
+// Keys that a row of the page table has room for, up to kMaxKeys.
+__device__ __forceinline__ int table_room(const SequencesView& s, int page_shift) {
+  return (int)min((int64_t)s.max_pages << page_shift, (int64_t)kMaxKeys);
+}
+
 // Sequence b of the call; b == num_seqs stands for the rows past the last
 // sequence, which have no keys. Offsets are cut to [0, T].
 __device__ __forceinline__ SeqRows sequence_rows(const SequencesView& s, int b, int T,
@@ -47,9 +52,9 @@ __device__ __forceinline__ SeqRows sequence_rows(const SequencesView& s, int b, 
   r.first = first_row(s, b, T);
   r.count = max((past ? T : first_row(s, b + 1, T)) - r.first, 0);
   r.len = past ? 0 : max(__ldg(s.seq_lens + b), 0);
-  const int64_t room = (int64_t)s.max_pages << page_shift;
+  const int room = table_room(s, page_shift);
   if (r.len > room) {
-    r.len = (int)room;
+    r.len = room;
     if (count_errors) atomicAdd(&status[kStatusBadPages], 1ull);
   }
   r.pos0 = r.len - r.count;

@@ -8,6 +8,11 @@
 
 namespace mxfp4el {
 
+// Lengths, windows and first tokens are cut to this many keys (no cache holds
+// as many), and a call has no more tokens than that, so that positions (-2^30
+// at least), their differences and sums with tile sizes stay in 32 bits.
+constexpr int kMaxKeys = 1 << 30;
+
 // Keys and values of one sequence are found through its page table; strides
 // are in elements.
 struct KvCacheView {

@@ -11,7 +11,7 @@ namespace mxfp4el {
 namespace {
 
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxTokens = (int64_t)1 << 30;
+constexpr int64_t kMaxTokens = kMaxKeys;
 constexpr int64_t kMaxStride = (int64_t)1 << 39;     // elements; a byte stride fits a tensor map
 constexpr int64_t kMaxHeads = 1 << 15;
 constexpr int64_t kMaxGroup = 128;                   // query heads to a key head
@@ -144,9 +144,10 @@ int check_attention(const void* q, int64_t q_token, int64_t q_head, const mxfp4e
   a->T = (int)T;
   a->heads = (int)heads;
   a->group = (int)(heads / a->cache.kv_heads);
-  // A window that no length reaches is no window.
-  a->window = window > kMaxDim ? 0 : (int)window;
-  a->sinks = a->window == 0 ? 0 : (int)(sinks > kMaxDim ? kMaxDim : sinks);
+  // A window that no length reaches is no window; first tokens past every
+  // length show no more.
+  a->window = window >= kMaxKeys ? 0 : (int)window;
+  a->sinks = a->window == 0 ? 0 : (int)(sinks > kMaxKeys ? kMaxKeys : sinks);
   a->status = device_status_words();
   return a->status == nullptr ? MXFP4EL_ERR_CUDA : MXFP4EL_OK;
 }

@@ -124,8 +124,8 @@ struct __align__(16) DecodeShared {
 };
 
 __device__ __forceinline__ int sequence_len(const DecodeArgs& d, int b) {
-  const int64_t room = (int64_t)d.a.seqs.max_pages << d.a.cache.page_shift;
-  return (int)min((int64_t)max(__ldg(d.a.seqs.seq_lens + d.seq0 + b), 0), room);
+  return min(max(__ldg(d.a.seqs.seq_lens + d.seq0 + b), 0),
+             table_room(d.a.seqs, d.a.cache.page_shift));
 }
 
 // Tiles with a key that the token of a sequence of n keys sees; one (empty)
