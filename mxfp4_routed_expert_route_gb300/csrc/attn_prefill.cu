@@ -17,11 +17,11 @@
 // Bound: tensor throughput, 4 D operations per row and key, as long as the
 // powers keep up: the two tiles take turns, one in the tensor pipe while the
 // other's softmax runs. A prompt of 8192 tokens, 64 query and 8 key heads of
-// 128: 715 to 755 us by the board, 1.46 to 1.54 PFLOP/s of unmasked work, the
+// 128, in calls one after another: 743 us, 1.48 PFLOP/s of unmasked work, the
 // tensor pipe busy 66 % of the cycles at 1.95 GHz and 1.37 kW; the same with
 // softmax warps that only pass the tiles on: 641 us. Short units (a window of
-// 128) are bound by the chain of their steps: 46 us for 4096 tokens, heads of
-// 64, issue slots used 29 %.
+// 128) are bound by the chain of their steps: 40 us for 4096 tokens, heads of
+// 64.
 //
 // Warps of a CTA (one CTA per SM, units from a counter, the longest first):
 //   0-7, 8-15 softmax and epilogue of row tile 0 and of row tile 1: two
@@ -37,12 +37,16 @@
 //   17        issues the matrix instructions
 //   18        values of key tiles that the mask cuts: rows that no query sees
 //             are zeroed (a masked score gives P = 0, but 0 times what a stale
-//             page holds need not be 0), and so are infinities and NaN.
+//             page holds need not be 0), and so are infinities and NaN in rows
+//             that some queries see and some do not.
 //   19        takes units and looks up their rows and first pages
 // A value that is not finite must reach the rows that see it and no other,
-// which a matrix product cannot do in a tile that the mask cuts: there it
-// counts as zero, and warp 18 computes the rows that may see it by itself, on
-// the CUDA cores; the epilogue leaves them out.
+// which a matrix product cannot do where the mask cuts. There it counts as
+// zero, and since a positive weight times an infinity or NaN is that infinity
+// or NaN whatever the weight, the epilogue adds it to the rows that see its
+// key: the keys at the two edges of the mask, fewer than a unit's tokens at
+// each. (8192 tokens with nothing but NaN for values: 1.16 ms, 0.69 without; 32
+// heads with a key head each, whose units are 256 tokens: 2.6 ms, 0.40.)
 //
 // P and the sum l: P is rounded to bf16 for the second product (a relative
 // error of 2^-8 at most, as the result's own rounding); l adds the float32
@@ -132,7 +136,7 @@ struct __align__(16) PrefillShared {
   uint64_t drain;
   uint32_t tmem_base;
   int joins[2];
-  int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys with values that are not finite
+  int bad_lo[kUnitRing], bad_hi[kUnitRing];   // keys whose values that are not finite were zeroed
   Unit unit[kUnitRing];
   int first_ids[kUnitRing][16];              // pages of the unit's first key tile
   float row_max[2][2][kRows];                // [tile][half of the keys]
@@ -259,84 +263,69 @@ __device__ __forceinline__ float finish(const AttnArgs& a, int head, float m, fl
   return f / l;
 }
 
-// Whether the row at position pos may see a key of [bad_lo, bad_hi].
-__device__ __forceinline__ bool may_see(const AttnArgs& a, int pos, int bad_lo, int bad_hi) {
-  return bad_lo <= min(bad_hi, pos) &&
-         (a.window == 0 || bad_hi > pos - a.window || bad_lo < a.sinks);
+// Whether every token of the unit sees key j, which one of them sees.
+__device__ __forceinline__ bool all_see(const Unit& u, int j, int window) {
+  return j <= u.pos0 &&
+         (window == 0 || j > u.pos0 + u.nt - 1 - window || j < u.sinks);
 }
 
-// One row on the CUDA cores (see the top) by one warp: lane i holds elements
-// i, i + 32, ... of the row; four keys at a time.
+// O of a warp's rows (columns col0 .. col0 + D / 2 - 1 of the head, at o_addr)
+// plus the values that are not finite of the keys in [bad_lo, bad_hi] that some
+// of the unit's tokens see and some do not: those before the window of the
+// last token, and those behind the first token. `pos` is the lane's position,
+// pos_last the warp's last.
 template <int D>
-__device__ __forceinline__ void slow_row(const AttnArgs& a, const Unit& u, int token, int head,
-                                         int lane) {
-  constexpr int kE = D / 32;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                           (int64_t)(u.row0 + token) * a.q_token + head * a.q_head + lane;
-  const int pos = u.pos0 + token;
-  float x[kE], o[kE] = {};
-#pragma unroll
-  for (int e = 0; e < kE; ++e) x[e] = __bfloat162float(q[32 * e]) * (a.scale * kLog2e);
-  float m = -INFINITY, l = 0.f;
+__device__ __forceinline__ void add_not_finite(const AttnArgs& a, const Unit& u, int bad_lo,
+                                               int bad_hi, int pos, int pos_last, bool row,
+                                               uint32_t o_addr, int col0, int lane) {
+  const __nv_bfloat16* values = static_cast<const __nv_bfloat16*>(a.cache.v) +
+                                (int64_t)u.kvh * a.cache.v_head + col0;
 #pragma unroll 1
-  for (int j0 = 0; j0 <= pos; j0 += 4) {
-    if (a.window != 0 && j0 >= a.sinks && j0 + 3 <= pos - a.window) {
-      j0 = ((pos - a.window + 1) & ~3) - 4;        // on to the window's first keys
-      continue;
-    }
-    float s[4];
-    int64_t at[4];
+  for (int edge = 0; edge < 2; ++edge) {
+    const int from = max(bad_lo, edge == 0 ? max(u.lo, u.sinks) : u.pos0 + 1);
+    const int to = min(bad_hi, edge == 1 ? pos_last
+                               : a.window == 0 ? -1
+                                               : min(u.pos0, u.pos0 + u.nt - 1 - a.window));
+#pragma unroll 1
+    for (int j0 = from; j0 <= to; j0 += 32) {
+      // Lane i looks up key j0 + i; a page id out of range has zeros.
+      int64_t at = -1;
+      if (j0 + lane <= to) {
+        const int64_t page = page_of(a.seqs, a.cache, u.seq, (j0 + lane) >> a.cache.page_shift);
+        if (page >= 0)
+          at = page * a.cache.v_page + ((j0 + lane) & (a.cache.page_size - 1)) * a.cache.v_slot;
+      }
+      const uint32_t keys = __ballot_sync(kFullMask, at >= 0);
+#pragma unroll 1
+      for (int q = 0; q < D / 2; q += 16) {
+        uint32_t o[16];
+        __syncwarp();
+        tmem_ld16(o_addr + q, o);
+        tmem_wait_ld();
+        for (uint32_t left = keys; left != 0; left &= left - 1) {
+          const int i = __ffs(left) - 1;
+          const uint4* v = reinterpret_cast<const uint4*>(values + __shfl_sync(kFullMask, at, i) + q);
+          if (!row || !key_visible(j0 + i, pos, a.window, a.sinks)) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = j0 + i;
-      at[i] = -1;
-      s[i] = -INFINITY;
-      if (j <= pos && key_visible(j, pos, a.window, a.sinks)) {
-        const int64_t page = page_of(a.seqs, a.cache, u.seq, j >> a.cache.page_shift);
-        const int slot = j & (a.cache.page_size - 1);
-        s[i] = 0.f;
-        if (page >= 0) {
-          const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(a.cache.k) +
-                                   page * a.cache.k_page + u.kvh * a.cache.k_head +
-                                   slot * a.cache.k_slot + lane;
-          at[i] = page * a.cache.v_page + u.kvh * a.cache.v_head + slot * a.cache.v_slot + lane;
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = __ldg(v + h);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int e = 0; e < kE; ++e) s[i] = fmaf(x[e], __bfloat162float(k[32 * e]), s[i]);
+            for (int e = 0; e < 4; ++e) {
+              float lo = __uint_as_float(o[8 * h + 2 * e]), hi = __uint_as_float(o[8 * h + 2 * e + 1]);
+              if ((w[e] & 0x7f80u) == 0x7f80u) lo += __uint_as_float(w[e] << 16);
+              if ((w[e] & 0x7f800000u) == 0x7f800000u) hi += __uint_as_float(w[e] & 0xffff0000u);
+              o[8 * h + 2 * e] = __float_as_uint(lo);
+              o[8 * h + 2 * e + 1] = __float_as_uint(hi);
+            }
+          }
         }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) s[i] += __shfl_xor_sync(kFullMask, s[i], off);
-      }
-    }
-    const float top = fmaxf(m, fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])));
-    const float base = top == -INFINITY ? 0.f : top, keep = exp2_approx(m - base);
-    m = top;
-    l *= keep;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] *= keep;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = exp2_approx(s[i] - base);
-      if (j0 + i <= pos && key_visible(j0 + i, pos, a.window, a.sinks)) l += p;
-      if (at[i] >= 0) {
-#pragma unroll
-        for (int e = 0; e < kE; ++e)
-          o[e] = fmaf(p, __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.v)[at[i] + 32 * e]),
-                      o[e]);
+        __syncwarp();
+        tmem_st16(o_addr + q, o);
+        tmem_wait_st();
       }
     }
   }
-  float f = 1.f;
-  if (a.sink_logits != nullptr) {
-    const float z = __ldg(a.sink_logits + head) * kLog2e;
-    const float top = fmaxf(m, z), base = top == -INFINITY ? 0.f : top;
-    f = exp2_approx(m - base);
-    l = l * f + exp2_approx(z - base);
-  }
-  const float inv = l == 0.f ? 0.f : f / l;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
-                       ((int64_t)(u.row0 + token) * a.heads + head) * D + lane;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) out[32 * e] = __float2bfloat16_rn(o[e] * inv);
 }
 
 // kSplit: units may be shared by several CTAs.
@@ -560,16 +549,20 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         ok = ok && mbar_wait_warp(&sh.o_full[t], o_phase);
         o_phase ^= 1u;
         tc_fence_after_sync();
-        const int bad_lo = *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]);
-        const int bad_hi = *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]);
-        const bool again = may_see(a, pos, bad_lo, bad_hi);
+        // Warp 18 may still be at key tiles that only the other row tile sees;
+        // all that these rows see is in the range by now, and what is not
+        // theirs changes nothing.
+        const int bad_lo = __shfl_sync(kFullMask, *reinterpret_cast<volatile int*>(&sh.bad_lo[slot]), 0);
+        const int bad_hi = __shfl_sync(kFullMask, *reinterpret_cast<volatile int*>(&sh.bad_hi[slot]), 0);
+        if (bad_lo <= bad_hi)
+          add_not_finite<D>(a, u, bad_lo, bad_hi, pos, pos_last, write, o_addr, half * (D / 2), lane);
         if (!kSplit || u.parts == 1) {
 #pragma unroll
           for (int q = 0; q < D / 64; ++q) {
             float o[32];
             tmem_ld32(o_addr + 32 * q, o);
             tmem_wait_ld();
-            if (write && !again) {
+            if (write) {
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j)
@@ -592,7 +585,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           }
           if (half == 0) {
             piece[kRows * D + row] = m * c;
-            piece[kRows * D + kRows + row] = again ? -1.f : l;     // -1: warp 18 computes the row
+            piece[kRows * D + kRows + row] = l;
           }
         }
         tc_fence_before_sync();
@@ -635,7 +628,6 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
             float total = lk * f;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
-            const bool skip = __any_sync(kFullMask, lk < 0.f);
             const float inv = finish(a, h, top, total);
             float o[D / 32] = {};
 #pragma unroll 4
@@ -658,14 +650,12 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
                 o[1] = fmaf(v.y, fk, o[1]);
               }
             }
-            if (!skip) {
-              uint32_t* to = reinterpret_cast<uint32_t*>(
-                  static_cast<__nv_bfloat16*>(a.out) +
-                  ((int64_t)(u.row0 + token) * a.heads + h) * D + lane * (D / 32));
+            uint32_t* to = reinterpret_cast<uint32_t*>(
+                static_cast<__nv_bfloat16*>(a.out) +
+                ((int64_t)(u.row0 + token) * a.heads + h) * D + lane * (D / 32));
 #pragma unroll
-              for (int e = 0; e < D / 64; ++e)
-                to[e] = total == 0.f ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-            }
+            for (int e = 0; e < D / 64; ++e)
+              to[e] = total == 0.f ? 0u : pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
           }
         }
         bar_sync(1 + t, 256);                          // joins has been read
@@ -1036,6 +1026,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           for (int r = lane; r < ((kt.cols + 15) & ~15); r += 32) {
             const int key = kt.j0 + r;
             const bool seen = key < kt.end && (i < u.sink_tiles || key >= u.lo || key < u.sinks);
+            if (seen && all_see(u, key, a.window)) continue;
 #pragma unroll
             for (int c = 0; c < 8 * S::kSubs; ++c) {
               // Lanes start at different pieces of their rows: no bank conflicts.
@@ -1075,12 +1066,6 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
           if (lane == 0) mbar_arrive(&sh.full[v_stage]);
         }
         stage = stage + 2 < S::kStages ? stage + 2 : stage + 2 - S::kStages;
-      }
-      if (unit_hi >= 0) {
-#pragma unroll 1
-        for (int r = 0; r < u.nt * a.group; ++r)
-          if (may_see(a, u.pos0 + r / a.group, unit_lo, unit_hi))
-            slow_row<D>(a, u, r / a.group, u.kvh * a.group + r % a.group, lane);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.u_empty[slot]);
