@@ -28,6 +28,7 @@ _DTYPES = {torch.float32: _native.DTYPE_F32, torch.bfloat16: _native.DTYPE_BF16}
 # torch.cuda.current_stream(device).cuda_stream, which costs 2 us a call.
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 class PagedKVCache:
@@ -215,13 +216,19 @@ def attention_workspace(device=None) -> torch.Tensor:
 _workspaces: dict[tuple[int, int], torch.Tensor] = {}
 
 
-def _new_workspace(cache: PagedKVCache) -> torch.Tensor:
-    if torch.cuda.is_current_stream_capturing():
-        raise RuntimeError("pass a workspace (attention_workspace) while a graph is captured, "
-                           "or make a first call on this stream before the capture")
-    with torch.cuda.device(cache.device):
-        ws = attention_workspace(cache.device)
-    _workspaces[(cache._index, _raw_stream(cache._index))] = ws
+def _kept_workspace(cache: PagedKVCache) -> torch.Tensor:
+    index = cache._index
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return _kept_workspace(cache)
+    # A graph may run on any stream, beside the calls of this one.
+    if _capturing():
+        raise RuntimeError("pass a workspace of its own (attention_workspace) to a call that "
+                           "is captured in a graph")
+    key = (index, _raw_stream(index))
+    ws = _workspaces.get(key)
+    if ws is None:
+        ws = _workspaces[key] = attention_workspace(cache.device)
     return ws
 
 
@@ -252,9 +259,7 @@ def _attention(decode, q, cache, seqs, scale, window, sinks, sink_logits, out, w
         out = torch.empty(shape, dtype=q.dtype, device=q.device)
     if T:
         if workspace is None:
-            workspace = _workspaces.get((index, _raw_stream(index)))
-            if workspace is None:
-                workspace = _new_workspace(cache)
+            workspace = _kept_workspace(cache)
         args = (q.data_ptr(), stride[0], stride[1], cache._address, seqs._address,
                 dim ** -0.5 if scale is None else scale, window, sinks,
                 None if sink_logits is None else sink_logits.data_ptr(), out.data_ptr())
@@ -281,8 +286,9 @@ def paged_attention_decode(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSequ
     own among them) and the first ``sinks``. ``sink_logits`` (num_heads)
     float32 adds exp(logit) to each head's softmax sum. A sequence without
     keys gives zeros. ``workspace`` is an :func:`attention_workspace`; by
-    default one per stream is kept. See mxfp4el_attention_decode in the C
-    header.
+    default one per stream is kept. A call that is captured in a graph has to
+    bring one, since the graph may run beside the stream's other calls. See
+    mxfp4el_attention_decode in the C header.
     """
     if seqs.q_offsets is not None:
         raise ValueError("decode takes one token per sequence: leave q_offsets out, or use "

@@ -145,3 +145,37 @@ def test_nothing_but_nan_values():
     assert torch.isnan(call(d, False)).all()
     assert torch.isnan(call(d, False, window=200, sinks=4)).all()
     assert lib.wait_timeouts() == 0
+
+
+# ----------------------------------------------------------- workspaces ----
+@pytest.mark.parametrize("decode", [True, False])
+def test_a_captured_call_brings_its_workspace(decode):
+    # The stream's kept one would be shared by the graph, wherever it runs, and
+    # the stream's later calls.
+    d = make([400, 3000], [1, 1] if decode else [100, 9], dim=128)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want = call(d, decode)
+    out = torch.empty_like(d["q"])
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="workspace"):
+        with torch.cuda.graph(g, stream=s):
+            out.zero_()
+            call(d, decode, out=out)
+    # Two graphs of one stream, replayed side by side on others.
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(2):
+        ws = lib.attention_workspace()
+        outs.append(torch.empty_like(d["q"]))
+        graphs.append((torch.cuda.CUDAGraph(), ws))
+        with torch.cuda.graph(graphs[-1][0], stream=s):
+            for _ in range(20):
+                call(d, decode, out=outs[-1], workspace=ws)
+    torch.cuda.synchronize()
+    for (g, _), t in zip(graphs, streams):
+        with torch.cuda.stream(t):
+            g.replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
