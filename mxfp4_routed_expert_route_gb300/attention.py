@@ -260,16 +260,18 @@ def _attention(decode, q, cache, seqs, scale, window, sinks, sink_logits, out, w
     if T:
         if workspace is None:
             workspace = _kept_workspace(cache)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
         args = (q.data_ptr(), stride[0], stride[1], cache._address, seqs._address,
                 dim ** -0.5 if scale is None else scale, window, sinks,
                 None if sink_logits is None else sink_logits.data_ptr(), out.data_ptr())
         lib = _native.load()
         if decode:
             _call(lib.mxfp4el_attention_decode, "paged_attention_decode", cache,
-                  args + (heads, workspace.data_ptr(), workspace.numel()))
+                  args + (heads, workspace.data_ptr(), workspace.nbytes))
         else:
             _call(lib.mxfp4el_attention_prefill, "paged_attention_prefill", cache,
-                  args + (T, heads, workspace.data_ptr(), workspace.numel()))
+                  args + (T, heads, workspace.data_ptr(), workspace.nbytes))
     return out
 
 

@@ -179,3 +179,21 @@ def test_a_captured_call_brings_its_workspace(decode):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_the_workspace_is_looked_at(decode):
+    d = make([40, 20], [1, 1] if decode else [30, 20])
+    want = call(d, decode)
+    ws = lib.attention_workspace()
+    with pytest.raises(ValueError, match="workspace"):
+        call(d, decode, workspace=ws.cpu())
+    with pytest.raises(ValueError, match="workspace"):
+        call(d, decode, workspace=torch.zeros(2, ws.numel(), dtype=torch.uint8, device="cuda").t())
+    with pytest.raises(lib.MXFP4Error):
+        call(d, decode, workspace=ws[256:])                  # too short
+    with pytest.raises(lib.MXFP4Error):
+        call(d, decode, workspace=torch.zeros(ws.numel() + 16, dtype=torch.uint8,
+                                              device="cuda")[16:])          # not aligned
+    # What counts is its bytes.
+    assert torch.equal(call(d, decode, workspace=ws.view(torch.float32)), want)
