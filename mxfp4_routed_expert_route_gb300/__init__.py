@@ -18,7 +18,7 @@ import ctypes
 
 import torch
 
-from . import _native
+from . import _native, attention
 from .attention import (PagedKVCache, PagedSequences, append_kv, attention_workspace, page_errors,
                         paged_attention_decode, paged_attention_prefill)
 
@@ -383,7 +383,8 @@ def device_errors(device=None) -> int:
 def wait_timeouts(device=None) -> int:
     """Kernel waits that gave up after their time limit since the last query
     (syncs). Always 0 on a healthy device; a nonzero count means the outputs
-    of the calls since the last query are not valid."""
+    of the calls since the last query are not valid. The attention workspaces
+    that the package keeps are then given up; a program zeroes its own."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     n = ctypes.c_int64(0)
     with torch.cuda.device(dev):
@@ -391,4 +392,6 @@ def wait_timeouts(device=None) -> int:
         _native.check(_native.load().mxfp4el_wait_timeouts(ctypes.c_void_p(stream),
                                                            ctypes.byref(n)),
                       "mxfp4el_wait_timeouts")
+        if n.value:
+            attention._drop_workspaces(torch.cuda.current_device())
     return int(n.value)

@@ -205,7 +205,8 @@ def append_kv(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: PagedKVC
 def attention_workspace(device=None) -> torch.Tensor:
     """A zeroed workspace for the attention calls, to be kept and passed as
     ``workspace``. Calls that may run at the same time (on different streams,
-    or in different graphs) need one each."""
+    or in different graphs) need one each. After :func:`wait_timeouts` has
+    reported a wait that gave up, it has to be zeroed."""
     dev = torch.device("cuda" if device is None else device)
     return torch.zeros(_native.load().mxfp4el_attention_workspace_size(), dtype=torch.uint8,
                        device=dev)
@@ -214,6 +215,13 @@ def attention_workspace(device=None) -> torch.Tensor:
 # The workspace of calls that bring none: one per device and stream, so that
 # calls on different streams do not share one.
 _workspaces: dict[tuple[int, int], torch.Tensor] = {}
+
+
+def _drop_workspaces(index: int) -> None:
+    """A call that gave up may leave a workspace's counters as they should not
+    be: the next calls on the device get new ones."""
+    for key in [k for k in _workspaces if k[0] == index]:
+        del _workspaces[key]
 
 
 def _kept_workspace(cache: PagedKVCache) -> torch.Tensor:

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mxfp4_routed_expert_route_gb300 as lib
+from mxfp4_routed_expert_route_gb300 import attention
 from test_attention_gpu import BF16, F32, call, check, make
 
 pytestmark = pytest.mark.gpu
@@ -197,3 +198,31 @@ def test_the_workspace_is_looked_at(decode):
                                               device="cuda")[16:])          # not aligned
     # What counts is its bytes.
     assert torch.equal(call(d, decode, workspace=ws.view(torch.float32)), want)
+
+
+def test_kept_workspaces_are_given_up_after_a_wait_that_gave_up(monkeypatch):
+    # The count comes from a stand-in for the library's call.
+    d = make([3000, 9000], [1, 1], dim=128)
+    want = call(d, True)
+    kept = attention._workspaces
+    assert any(k[0] == 0 for k in kept)
+    native = lib._native.load()
+    old = next(t for k, t in kept.items() if k[0] == 0)
+
+    class Library:
+        count = 3
+
+        def mxfp4el_wait_timeouts(self, stream, n):
+            n._obj.value = self.count
+            return 0
+
+        def __getattr__(self, name):
+            return getattr(native, name)
+
+    monkeypatch.setattr(lib._native, "load", Library)
+    assert lib.wait_timeouts() == 3 and not any(k[0] == 0 for k in kept)
+    old[:4096].fill_(1)               # what a call that gave up might leave
+    assert torch.equal(call(d, True), want)
+    Library.count = 0
+    assert lib.wait_timeouts() == 0 and any(k[0] == 0 for k in kept)
+    assert torch.equal(call(d, True), want)
