@@ -133,7 +133,8 @@ attention_simt_kernel(const AttnArgs a, int heads_tile, int head_blocks, int tok
     const int s = key & (a.cache.page_size - 1);
     if (want) {
       page = page_of(a.seqs, a.cache, b, key >> a.cache.page_shift);
-      if (page < 0 && (threadIdx.x & 3) == 0 && (s == 0 || row == 0))
+      // Counted at the page's first key that this tile wants.
+      if (page < 0 && (threadIdx.x & 3) == 0 && (s == 0 || row == 0 || key == first))
         atomicAdd(&a.status[kStatusBadPages], 1ull);
     }
     const float* k = static_cast<const float*>(a.cache.k);

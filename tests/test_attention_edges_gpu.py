@@ -226,3 +226,19 @@ def test_kept_workspaces_are_given_up_after_a_wait_that_gave_up(monkeypatch):
     Library.count = 0
     assert lib.wait_timeouts() == 0 and any(k[0] == 0 for k in kept)
     assert torch.equal(call(d, True), want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("window,sinks,bad", [(50, 0, 1), (37, 0, 1), (37, 2, 0), (1, 0, 3), (0, 0, 0)])
+def test_every_page_id_out_of_range_is_counted(dtype, decode, window, sinks, bad):
+    # 100 keys in pages of 32: windows that begin inside a page, first tokens.
+    d = make([100], [1], dtype=dtype, page=32)
+    d["table"][0, bad] = -7
+    lib.page_errors()
+    call(d, decode, window=window, sinks=sinks)
+    assert lib.page_errors() > 0
+    if window == 37 and sinks == 0:      # a page that nothing sees is not looked up
+        d["table"][0, 0], d["table"][0, 1] = -7, 0
+        call(d, decode, window=window)
+        assert lib.page_errors() == 0
