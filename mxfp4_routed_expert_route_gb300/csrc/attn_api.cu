@@ -12,7 +12,8 @@ namespace {
 
 constexpr int64_t kMaxDim = ((int64_t)1 << 31) - 1;
 constexpr int64_t kMaxTokens = kMaxKeys;
-constexpr int64_t kMaxStride = (int64_t)1 << 39;     // elements; a byte stride fits a tensor map
+constexpr int64_t kMaxStrideBytes = ((int64_t)1 << 40) - 1;   // as a tensor map has it
+constexpr int64_t kMaxSpanBytes = (int64_t)1 << 56;
 constexpr int64_t kMaxHeads = 1 << 15;
 constexpr int64_t kMaxGroup = 128;                   // query heads to a key head
 
@@ -32,10 +33,12 @@ Span span_of(const void* p, int64_t bytes) {
 int check_rows(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width,
                int64_t esize, Span* span) {
   if (p == nullptr || !aligned16(p)) return MXFP4EL_ERR_INVALID_ARGUMENT;
-  if (s0 < 0 || s1 < 0 || s0 * esize % 16 != 0 || s1 * esize % 16 != 0)
+  if (s0 < 0 || s1 < 0 || s0 % (16 / esize) != 0 || s1 % (16 / esize) != 0)
     return MXFP4EL_ERR_INVALID_ARGUMENT;
-  if (s0 > kMaxStride || s1 > kMaxStride) return MXFP4EL_ERR_TOO_LARGE;
-  *span = span_of(p, ((n0 - 1) * s0 + (n1 - 1) * s1 + width) * esize);
+  if (s0 > kMaxStrideBytes / esize || s1 > kMaxStrideBytes / esize) return MXFP4EL_ERR_TOO_LARGE;
+  const __int128 bytes = ((__int128)(n0 - 1) * s0 + (__int128)(n1 - 1) * s1 + width) * esize;
+  if (bytes > kMaxSpanBytes) return MXFP4EL_ERR_TOO_LARGE;
+  *span = span_of(p, (int64_t)bytes);
   return MXFP4EL_OK;
 }
 
@@ -55,8 +58,8 @@ int check_cache(const mxfp4el_kv_cache* c, KvCacheView* v, Span* k_span, Span* v
   for (int i = 0; i < 2; ++i) {
     // Slots of a page must not fall together: the append writes them.
     if (st[i][2] < c->head_dim) return MXFP4EL_ERR_INVALID_ARGUMENT;
-    if (st[i][2] * es % 16 != 0) return MXFP4EL_ERR_INVALID_ARGUMENT;
-    if (st[i][2] > kMaxStride / 1024) return MXFP4EL_ERR_TOO_LARGE;
+    if (st[i][2] % (16 / es) != 0) return MXFP4EL_ERR_INVALID_ARGUMENT;
+    if (st[i][2] > kMaxStrideBytes / es) return MXFP4EL_ERR_TOO_LARGE;
     Span* s = i == 0 ? k_span : v_span;
     const int rc = check_rows(base[i], c->num_pages, st[i][0], c->num_kv_heads, st[i][1],
                               (c->page_size - 1) * st[i][2] + c->head_dim, es, s);
