@@ -66,7 +66,8 @@ typedef struct mxfp4el_kv_cache {
  * a sequence's length are not read. seq_lens is (num_seqs) int32. q_offsets
  * is (num_seqs + 1) int32, starting at 0 and never falling: sequence b's new
  * tokens are rows q_offsets[b] .. q_offsets[b + 1] - 1 of the call's token
- * arrays. NULL: one new token per sequence, row b.
+ * arrays. NULL: one new token per sequence, row b. All lie on 4-byte
+ * boundaries, as sink_logits does.
  *
  * A page id outside [0, num_pages) is not followed: attention takes its keys
  * and values as zeros, the append drops the token's key and value. A length

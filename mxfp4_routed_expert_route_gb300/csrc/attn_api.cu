@@ -18,6 +18,7 @@ constexpr int64_t kMaxHeads = 1 << 15;
 constexpr int64_t kMaxGroup = 128;                   // query heads to a key head
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 struct Span {
   uintptr_t lo, hi;   // bytes [lo, hi); empty when equal
@@ -90,6 +91,8 @@ int check_sequences(const mxfp4el_sequences* s, int64_t T, SequencesView* v) {
                           (s->max_pages > 0 && (s->page_table == nullptr ||
                                                 (s->num_seqs > 1 && s->table_stride < 0)))))
     return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (!aligned4(s->page_table) || !aligned4(s->seq_lens) || !aligned4(s->q_offsets))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
   if (s->q_offsets == nullptr && s->num_seqs != T) return MXFP4EL_ERR_INVALID_ARGUMENT;
   v->page_table = s->page_table;
   v->seq_lens = s->seq_lens;
@@ -127,7 +130,8 @@ int check_attention(const void* q, int64_t q_token, int64_t q_head, const mxfp4e
   const int64_t es = a->cache.token_dtype == kTokenBF16 ? 2 : 4, D = a->cache.head_dim;
   rc = check_rows(q, T, q_token, heads, q_head, D, es, &qs);
   if (rc != MXFP4EL_OK) return rc;
-  if (out == nullptr || !aligned16(out)) return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (out == nullptr || !aligned16(out) || !aligned4(sink_logits))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
   const Span os = span_of(out, T * heads * D * es);
   const Span others[] = {qs, ks, vs, span_of(sink_logits, heads * 4),
                          span_of(workspace, (int64_t)workspace_bytes),

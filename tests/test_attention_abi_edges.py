@@ -1,7 +1,5 @@
 """Sizes and addresses at the edge of what the attention operators' C entry
 points accept: everything here returns before any GPU work."""
-import pytest
-
 from test_attention_abi import _append, _cache, _prefill, _seqs, lib  # noqa: F401
 
 
@@ -21,3 +19,13 @@ def test_strides_past_the_address_space(lib):  # noqa: F811
     # A tensor map takes byte strides below 2^40, whatever the type.
     f32 = dict(dtype=n.DTYPE_F32, k_page_stride=1 << 38)
     assert _prefill(lib, _cache(n, **f32), s) == big
+
+
+def test_addresses_between_elements(lib):  # noqa: F811
+    from mxfp4_routed_expert_route_gb300 import _native as n
+    bad, c = n.ERR_INVALID_ARGUMENT, _cache(n)
+    for kw in (dict(page_table=(1 << 24) + 2), dict(seq_lens=(1 << 25) + 1),
+               dict(q_offsets=(1 << 26) + 3)):
+        assert _prefill(lib, c, _seqs(n, **kw)) == bad, kw
+        assert _append(lib, c, _seqs(n, **kw)) == bad, kw
+    assert _prefill(lib, c, _seqs(n), logits=(1 << 39) + 2) == bad
