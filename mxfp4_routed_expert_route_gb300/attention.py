@@ -96,7 +96,7 @@ class PagedSequences:
                 raise ValueError(f"{name} is on {t.device}, page_table on {page_table.device}")
             if t.dtype != torch.int32:
                 raise TypeError(f"{name} must be int32")
-            if t.dim() != dim or (t.numel() > 1 and t.stride(-1) != 1):
+            if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1):
                 raise ValueError(f"{name} must have {dim} dimension(s) and contiguous rows")
         n = page_table.shape[0]
         if seq_lens.shape[0] != n or (q_offsets is not None and q_offsets.shape[0] != n + 1):

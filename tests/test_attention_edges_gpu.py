@@ -242,3 +242,15 @@ def test_every_page_id_out_of_range_is_counted(dtype, decode, window, sinks, bad
         d["table"][0, 0], d["table"][0, 1] = -7, 0
         call(d, decode, window=window)
         assert lib.page_errors() == 0
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_a_table_of_one_page_each_in_any_layout(decode):
+    # A column of page ids: its inner stride counts for nothing.
+    d = make([9, 16, 3], [1, 1, 1] if decode else [5, 16, 1])
+    want = call(d, decode)
+    ids = d["table"][:, 0].clone()
+    for table in (ids[None].t(), ids.view(3, 1), torch.stack([ids, ids], 1)[:, 1:]):
+        assert torch.equal(call(dict(d, table=table), decode), want)
+    with pytest.raises(ValueError):
+        lib.PagedSequences(d["table"].t().contiguous().t(), d["seq_lens"])
