@@ -685,6 +685,13 @@ attention_decode_kernel(const __grid_constant__ DecodeMaps maps, const DecodeArg
         }
       }
     }
+    // No copy may outlive the block, also where a consumer's wait gave up: the
+    // last one into every stage and query slot (before a first one, the wait
+    // ends at once).
+    for (int s = 0; s < S::kStages; ++s)
+      ok &= mbar_wait_warp(&sh.full[s], s < stage ? phase : phase ^ 1u);
+    for (int s = 0; s < kQSlots; ++s)
+      ok &= mbar_wait_warp(&sh.q_full[s], s < slot ? q_phase : q_phase ^ 1u);
     if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
     return;
   }

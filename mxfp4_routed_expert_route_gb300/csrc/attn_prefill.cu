@@ -58,7 +58,8 @@
 // their order along the keys.
 //
 // Every wait is bounded. A role whose wait gives up records it and goes on
-// without waiting, so that every role ends.
+// without waiting (the copies stop), so that every role ends; copies that are
+// on their way are waited for, with the same bound.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -385,6 +386,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem_base, 0);
   pdl_wait();
   bool ok = true;
+  struct { int stage, q_slot; uint32_t phase, q_phase, raw_parity; } last = {};   // the copies' state
 
   // The softmax threads hold 64 scores each: they take registers that the
   // other warps give up (512 x 104 + 128 x 64 = 640 x 96).
@@ -815,6 +817,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
     const uint64_t keep = l2_evict_normal_policy();
     int slot = 0, stage = 0, q_slot = 0;
     uint32_t u_phase = 0, phase = 0, q_phase = 0;
+    uint32_t raw_parity = 0;                      // bit s: raw[s]'s next phase
     for (;;) {
       ok = ok && mbar_wait_warp(&sh.u_full[slot], u_phase);
       if (!ok) break;
@@ -831,6 +834,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
       if (tiles <= u.i0) continue;
 
       ok = ok && mbar_wait_warp(&sh.q_empty[q_slot], q_phase ^ 1u);
+      if (!ok) break;
       const int row_tiles = u.nt > p.n ? 2 : 1;
       if (elect_one()) {
         mbar_arrive_expect_tx(&sh.q_full[q_slot],
@@ -861,7 +865,10 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
                                (uint32_t)p.box_rows * 128u * S::kSubs;
         for (int v = 0; v < 2; ++v) {
           ok = ok && mbar_wait_warp(&sh.empty[stage], phase ^ 1u);
-          uint64_t* bar = v && kt.cut ? &sh.raw[stage] : &sh.full[stage];
+          if (!ok) break;
+          const bool raw = v && kt.cut;
+          uint64_t* bar = raw ? &sh.raw[stage] : &sh.full[stage];
+          raw_parity ^= raw ? 1u << stage : 0u;
           if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
           __syncwarp();
           if (want) {
@@ -879,6 +886,7 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
         id = next_id;
       }
     }
+    last = {stage, q_slot, phase, q_phase, raw_parity};
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------ matrix instructions
     // The whole warp runs the loop, on values the compiler can tell are the
@@ -1078,9 +1086,18 @@ attention_prefill_kernel(const __grid_constant__ PrefillMaps maps, const Prefill
   }
   if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   tc_fence_before_sync();
-  __syncthreads();
+  const bool gave_up = __syncthreads_or(!ok);
   tc_fence_after_sync();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  // No copy may outlive the block: where no wait gave up, all have been used.
+  if (gave_up && warp == kLoadWarp) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_wait_warp(&sh.raw[s], ((last.raw_parity >> s) & 1u) ^ 1u);
+      mbar_wait_warp(&sh.full[s], s < last.stage ? last.phase : last.phase ^ 1u);
+    }
+    for (int s = 0; s < S::kQSlots; ++s)
+      mbar_wait_warp(&sh.q_full[s], s < last.q_slot ? last.q_phase : last.q_phase ^ 1u);
+  }
 }
 
 template <int D, bool kSplit>
