@@ -54,7 +54,7 @@ constexpr int kMinTiles = 2;            // tiles per run at least (see above)
 constexpr int kWholeTiles = 8;
 constexpr int kMaxCtas = 256;
 constexpr int kMaxSeqs = 1024;          // sequences per launch (the prefix sums' shared memory)
-constexpr int kRowsMax = 64;            // query heads per unit: 16 kMT, kMT <= 4
+constexpr int kRowsMax = 32;            // query heads per unit: 16 kMT, kMT <= 2
 constexpr int kQSlots = 2;
 
 // Bytes of a piece in the workspace: rows of o (128 floats), m and l.
@@ -68,7 +68,7 @@ struct Shape {
   // heads of 64: 147 us with four groups, 111 with eight. bf16 does not (139
   // sequences of up to 1384 keys, heads of 64: 48.2 us with four, 52.0 with
   // eight, whose join is longer).
-  static constexpr int kGroups = sizeof(Tok) == 4 && kMT == 1 ? 8 : 4;
+  static constexpr int kGroups = sizeof(Tok) == 4 ? 8 : 4;
   // 32 KB of keys and values in a tile, or eight float32 keys a group.
   static constexpr int kTile = sizeof(Tok) == 2 ? 8192 / D : kGroups * 8;   // keys per tile
   static constexpr int kPer = kTile / kGroups;                      // keys per consumer warp
@@ -76,15 +76,13 @@ struct Shape {
   static constexpr int kSubs = D / kSub;                            // 128-byte columns of a row
   static constexpr uint32_t kHalf = (uint32_t)kTile * D * sizeof(Tok);   // keys (or values) of a tile
   // 160 KB of keys and values in flight per SM, less beside the buffers of 32
-  // and 64 heads; HBM's latency times an SM's share of its bandwidth is 45 KB.
-  static constexpr int kStages =
-      (kMT == 1 ? 5 : kMT == 2 ? 4 : sizeof(Tok) == 2 ? 3 : 2) * 32768 / (2 * (int)kHalf);
+  // heads; HBM's latency times an SM's share of its bandwidth is 45 KB.
+  static constexpr int kStages = (kMT == 1 ? 5 : 4) * 32768 / (2 * (int)kHalf);
   static constexpr int kQRow = D * (int)sizeof(Tok) + 16;           // padded row in shared memory
   static constexpr int kAcc = kH * D / 32;                          // result elements per lane
   // The join of a unit's warps goes through shared memory in kPasses
   // parts of kPass elements, of which each warp finishes kShare.
-  static constexpr int kPasses =
-      kMT == 4 || (sizeof(Tok) == 4 && (kMT == 2 || kAcc == 64)) ? 2 : 1;
+  static constexpr int kPasses = sizeof(Tok) == 4 && kAcc == 64 ? 2 : 1;
   static constexpr int kPass = kAcc / kPasses;
   static constexpr int kShare = kPass / kGroups >= 2 ? kPass / kGroups : 2;
 };
@@ -955,15 +953,22 @@ template <typename Tok, int D>
 cudaError_t launch_heads(const AttnArgs& a, void* workspace, cudaStream_t stream) {
   // float32: the CUDA cores' work grows with the heads that a warp carries, so
   // groups of up to 4 and 8 have kernels of their own (24 sequences of up to
-  // 3001 keys, 4 heads to a key head, four warps: 130 us with 16 carried, 40 with 4). The
-  // bf16 instruction takes 16 rows whatever the group.
+  // 3001 keys, 4 heads to a key head, four warps: 130 us with 16 carried, 40
+  // with 4; 8 heads to a key head, heads of 128, eight warps: 60 us with 16
+  // carried, 41 with 8). Wider groups are blocks of 16 heads.
   if constexpr (sizeof(Tok) == 4) {
     if (a.group <= 4) return launch<Tok, D, 1, 4>(a, workspace, stream);
     if (a.group <= 8) return launch<Tok, D, 1, 8>(a, workspace, stream);
+    return launch<Tok, D, 1>(a, workspace, stream);
+  } else {
+    // bf16: the instruction takes 16 rows whatever the group. Units of 32 heads
+    // read a tile once for two blocks of 16: 32 sequences of up to 4096 keys, 32
+    // heads to a key head of 128: 28.9 us, as units of 16 heads 37.0; of up to
+    // 8192 keys, 128 heads to a key head: 72.5 and 83.9. (A handful of short
+    // sequences loses by it, 15.3 against 11.8 us for four of up to 1000 keys.)
+    return a.group <= 16 ? launch<Tok, D, 1>(a, workspace, stream)
+                         : launch<Tok, D, 2>(a, workspace, stream);
   }
-  if (a.group <= 16) return launch<Tok, D, 1>(a, workspace, stream);
-  if (a.group <= 32) return launch<Tok, D, 2>(a, workspace, stream);
-  return launch<Tok, D, 4>(a, workspace, stream);
 }
 
 }  // namespace
