@@ -29,7 +29,11 @@
  *
  * with the last term only where sink_logits is given. Scores, softmax sums
  * and accumulators are float32; the result is rounded once to the token
- * dtype. The order of every sum is fixed, so the same call on the same
+ * dtype. On bf16 the weights exp(s_j - m) are rounded to bf16 where they
+ * multiply the values (a relative error of 2^-8 at most, as the result's own
+ * rounding); decode's sum adds the rounded weights, prefill's the float32
+ * ones. A value that is infinite or NaN gives infinities or NaN, in its
+ * column, to the queries that see its key. The order of every sum is fixed, so the same call on the same
  * inputs gives the same bits.
  */
 #ifndef MXFP4EL_ATTENTION_H

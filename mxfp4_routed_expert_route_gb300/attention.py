@@ -297,8 +297,9 @@ def paged_attention_decode(q: torch.Tensor, cache: PagedKVCache, seqs: PagedSequ
     float32 adds exp(logit) to each head's softmax sum. A sequence without
     keys gives zeros. ``workspace`` is an :func:`attention_workspace`; by
     default one per stream is kept. A call that is captured in a graph has to
-    bring one, since the graph may run beside the stream's other calls. See
-    mxfp4el_attention_decode in the C header.
+    bring one, since the graph may run beside the stream's other calls. Sums
+    are float32; bfloat16 calls round the softmax's weights to bfloat16 where
+    they multiply the values. See mxfp4el_attention_decode in the C header.
     """
     if seqs.q_offsets is not None:
         raise ValueError("decode takes one token per sequence: leave q_offsets out, or use "

@@ -258,7 +258,7 @@ extern "C" int mxfp4el_attention_prefill(const void* q, int64_t q_token_stride,
       check_attention(q, q_token_stride, q_head_stride, cache, seqs, scale, window, sinks,
                       sink_logits, out, T, num_heads, workspace, workspace_bytes, &a, &nothing);
   if (rc != MXFP4EL_OK || nothing) return rc;
-  // float32 has no tensor-core path that keeps its 24 bits.
+  // The tensor cores take no float32 operands.
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t err = a.cache.token_dtype == kTokenBF16
                               ? launch_attention_prefill(a, workspace, s)

@@ -18,7 +18,7 @@
 // powers keep up: the two tiles take turns, one in the tensor pipe while the
 // other's softmax runs. A prompt of 8192 tokens, 64 query and 8 key heads of
 // 128, in calls one after another: 743 us, 1.48 PFLOP/s of unmasked work, the
-// tensor pipe busy 66 % of the cycles at 1.95 GHz and 1.37 kW; the same with
+// tensor pipe busy 68 % of the cycles (1.95 GHz, 1.37 kW); the same with
 // softmax warps that only pass the tiles on: 641 us. Short units (a window of
 // 128) are bound by the chain of their steps: 40 us for 4096 tokens, heads of
 // 64.
@@ -48,9 +48,10 @@
 // each. (8192 tokens with nothing but NaN for values: 1.16 ms, 0.69 without; 32
 // heads with a key head each, whose units are 256 tokens: 2.6 ms, 0.40.)
 //
-// P and the sum l: P is rounded to bf16 for the second product (a relative
-// error of 2^-8 at most, as the result's own rounding); l adds the float32
-// values.
+// P and the sum l: P is rounded to bf16 for the second product, whose other
+// operand is bf16 (a relative error of 2^-8 at most, as the result's own
+// rounding); l adds the float32 values, which the softmax warps have at hand
+// (the rounded ones would have to be taken out of their pairs again).
 //
 // Few rows: where the units are at most half as many as the SMs (and the
 // sequences few), the keys of each are split over several CTAs. Each leaves
@@ -82,7 +83,13 @@ constexpr int kUnitReaders = 3 + kSoftmaxWarps;     // copies, MMA, values, soft
 // many key tiles, are ahead: short units are taken early enough to hide the
 // lookup, long ones late enough to spread the last of them over the CTAs.
 constexpr int kAheadTiles = 8;
-constexpr int kFewSeqs = 30;            // sequences that the unit warp keeps in its lanes
+// Up to so many sequences, the unit warp keeps their rows in its lanes, takes
+// the longest first and may split units over the keys. Against the form for
+// more of them, 32 query and 8 key heads of 128: 30 chunks of 100 to 500 tokens
+// behind up to 8000 keys 475 us (518), 20 of 4 tokens behind up to 2000 33 us
+// (48), 8 single tokens behind 8000 58 us (90); a chunk of 2048 tokens beside 7
+// single tokens 255 us (248), beside 29 344 (343).
+constexpr int kFewSeqs = 30;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;         // S of tile t at 128 t, O at kOCol + D t
 constexpr float kRescale = 8.f;
@@ -194,21 +201,6 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// bar_sync that tells every thread whether any brought `p`.
-__device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
-  uint32_t any;
-  asm volatile(
-      "{\n"
-      " .reg .pred p, q;\n"
-      " setp.ne.u32 p, %3, 0;\n"
-      " bar.red.or.pred q, %1, %2, p;\n"
-      " selp.u32 %0, 1, 0, q;\n"
-      "}"
-      : "=r"(any)
-      : "r"(id), "r"(threads), "r"(p ? 1u : 0u)
-      : "memory");
-  return any != 0;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
