@@ -33,6 +33,9 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 INDEX_I32 = 0
 INDEX_I64 = 1
+# And of include/mxfp4el_quantized.h.
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 # Every symbol the header declares: (name, restype, argtypes).
 _P = ctypes.c_void_p
@@ -101,6 +104,10 @@ SIGNATURES = {
                                          _I64, _P, _SZ, _P]),
     "mxfp4el_attention_workspace_size": (_SZ, []),
     "mxfp4el_page_errors": (_INT, [_P, ctypes.POINTER(_I64)]),
+    "mxfp4_route_experts": (_INT, [_P, _INT, _I64, _P, _I64, _I64, _I64, _INT, _I64, _I64, _I64,
+                                   _INT, _FLT, _P, _P, _P]),
+    "mxfp4_quantize": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P]),
+    "mxfp4_dequantize": (_INT, [_P, _P, _I64, _I64, _P, _INT, _P]),
 }
 
 _lock = threading.Lock()

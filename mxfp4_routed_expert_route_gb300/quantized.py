@@ -1,0 +1,164 @@
+"""The operators around the MXFP4 routed experts on quantised tokens: experts
+and mixture weights from router logits, and rows of values to MXFP4 and back.
+
+Like the rest of the package this is the thin Python face of the C library
+(header ``include/mxfp4el_quantized.h``): it checks and marshals arguments;
+the work is done by the library's CUDA kernels on the current stream.
+
+MXFP4 rows are two uint8 tensors, packed (..., I/32, 16) and scales (..., I/32),
+as the experts' weights are.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _native
+
+__all__ = ["route_experts", "quantize_mxfp4", "dequantize_mxfp4"]
+
+_DTYPES = {torch.float32: _native.DTYPE_F32, torch.bfloat16: _native.DTYPE_BF16}
+_SCORES = {"softmax": _native.SCORE_SOFTMAX, "sigmoid": _native.SCORE_SIGMOID}
+
+# The current stream's handle of a device by index (see attention.py).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _call(f, name: str, index: int, args: tuple) -> None:
+    """One library call on device `index`, its current stream last."""
+    if _current_device() == index:
+        rc = f(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, _raw_stream(index))
+    if rc:
+        _native.check(rc, name)
+
+
+def _output(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype,
+            like: torch.Tensor) -> torch.Tensor:
+    """The output tensor: a new one, or the caller's if it fits."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if t.shape != shape or t.dtype is not dtype or t.device != like.device \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on "
+                         f"{like.device}")
+    return t
+
+
+def route_experts(logits: torch.Tensor, K: int, *, score: str = "softmax",
+                  bias: torch.Tensor | None = None, groups: int = 1,
+                  top_groups: int | None = None, group_best: int = 2, normalize: bool = True,
+                  scaling: float = 1.0, selected_experts: torch.Tensor | None = None,
+                  mixture_weights: torch.Tensor | None = None
+                  ) -> tuple[torch.Tensor, torch.Tensor]:
+    """(selected_experts (T, K) int32, mixture_weights (T, K) float32) of the
+    router logits (T, E), float32 or bfloat16, rows of contiguous elements.
+
+    Scores are the softmax over the experts or the sigmoid of each logit;
+    ``bias`` (E) float32 is added for the choice alone. With ``groups`` > 1
+    only the experts of the ``top_groups`` best groups (default: all) take
+    part, a group's score being the sum of its ``group_best`` highest choices.
+    The K highest are selected, highest first, ties to the lower index, as
+    float64 scores rank them; their weights are their scores, normalised to
+    sum to ``scaling`` or, without ``normalize``, times ``scaling``. Slots that
+    NaN logits leave over get id -1 and weight 0. At most 1024 experts, 32
+    groups and K = 32. See mxfp4_route_experts in the C header.
+    """
+    if not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2:
+        raise ValueError("logits must be a (T, E) float32 or bfloat16 CUDA tensor")
+    T, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if groups < 1 or E < 1 or E % groups:
+        raise ValueError("groups must divide the number of experts")
+    top_groups = groups if top_groups is None else top_groups
+    if not 1 <= top_groups <= groups:
+        raise ValueError("need 1 <= top_groups <= groups")
+    if not 0 <= K <= top_groups * (E // groups):
+        raise ValueError("K must be at most the experts of top_groups groups")
+    if group_best not in (1, 2):
+        raise ValueError("group_best must be 1 or 2")
+    index = logits.get_device()
+    if bias is not None and (bias.dtype is not torch.float32 or bias.get_device() != index
+                             or bias.shape != (E,) or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous (E,) float32 tensor on the logits' device")
+    sel = _output("selected_experts", selected_experts, (T, K), torch.int32, logits)
+    p = _output("mixture_weights", mixture_weights, (T, K), torch.float32, logits)
+    if T and K:
+        _call(_native.load().mxfp4_route_experts, "route_experts", index, (
+            logits.data_ptr(), _DTYPES[logits.dtype], logits.stride(0),
+            None if bias is None else bias.data_ptr(), T, E, K, _SCORES[score], groups,
+            top_groups, group_best, 1 if normalize else 0, scaling, sel.data_ptr(),
+            p.data_ptr()))
+    return sel, p
+
+
+def quantize_mxfp4(x: torch.Tensor, packed: torch.Tensor | None = None,
+                   scales: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(packed (..., I/32, 16), scales (..., I/32)) uint8 of x (..., I), float32
+    or bfloat16, I a multiple of 32.
+
+    x may be a view whose rows of I contiguous elements lie evenly apart (a
+    slice of a wider matrix). A group of 32 with largest magnitude a has the
+    scale 2^(floor(log2 a) - 2); its values are rounded to the nearest E2M1
+    number, ties to the even code, larger ones to 6. A group with an infinity
+    or a NaN reads back as NaN. See mxfp4_quantize in the C header.
+    """
+    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() == 0:
+        raise ValueError("x must be a (..., I) float32 or bfloat16 CUDA tensor")
+    shape = x.shape
+    I = shape[-1]
+    if I == 0 or I % 32:
+        raise ValueError("the last dimension must be a positive multiple of 32")
+    if x.is_contiguous():
+        rows, stride = x.numel() // I, I
+    else:
+        try:
+            flat = x.view(-1, I) if x.dim() != 2 else x
+        except RuntimeError:
+            flat = None
+        if flat is None or flat.stride(1) != 1 or (flat.shape[0] > 1 and flat.stride(0) < I):
+            raise ValueError("the rows of x must be contiguous and evenly apart")
+        rows, stride = flat.shape[0], flat.stride(0)
+    packed = _output("packed", packed, shape[:-1] + (I // 32, 16), torch.uint8, x)
+    scales = _output("scales", scales, shape[:-1] + (I // 32,), torch.uint8, x)
+    if rows:
+        _call(_native.load().mxfp4_quantize, "quantize_mxfp4", x.get_device(), (
+            x.data_ptr(), _DTYPES[x.dtype], stride, rows, I, packed.data_ptr(),
+            scales.data_ptr()))
+    return packed, scales
+
+
+def _mxfp4_rows(what: str, packed: torch.Tensor, scales: torch.Tensor) -> None:
+    """Refuses anything but MXFP4 rows that the library can read."""
+    if not packed.is_cuda or scales.device != packed.device:
+        raise ValueError(f"{what}: packed and scales must be on one CUDA device")
+    if packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+        raise TypeError(f"{what}: packed and scales must be uint8")
+    if packed.dim() < 2 or packed.shape[-1] != 16 or packed.shape[:-1] != scales.shape \
+            or packed.shape[-2] == 0:
+        raise ValueError(f"{what}: expected packed (..., I/32, 16) and scales (..., I/32)")
+    if not packed.is_contiguous() or not scales.is_contiguous():
+        raise ValueError(f"{what}: packed and scales must be contiguous")
+
+
+def dequantize_mxfp4(packed: torch.Tensor, scales: torch.Tensor,
+                     dtype: torch.dtype = torch.bfloat16,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values (..., I) that MXFP4 rows packed (..., I/32, 16) and scales
+    (..., I/32) stand for, float32 or bfloat16: exact in both. A scale byte of
+    255 gives NaN. See mxfp4_dequantize in the C header."""
+    _mxfp4_rows("dequantize_mxfp4", packed, scales)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    I = 32 * packed.shape[-2]
+    out = _output("out", out, packed.shape[:-2] + (I,), dtype, packed)
+    rows = packed.numel() // (I // 2)
+    if rows:
+        _call(_native.load().mxfp4_dequantize, "dequantize_mxfp4", packed.get_device(), (
+            packed.data_ptr(), scales.data_ptr(), rows, I, out.data_ptr(), _DTYPES[dtype]))
+    return out
