@@ -8,6 +8,8 @@
  *   mxfp4_route_experts            experts and mixture weights from logits
  *   mxfp4_quantize                 rows of values to MXFP4
  *   mxfp4_dequantize               the values that MXFP4 rows stand for
+ *   mxfp4_linear                   product of MXFP4 tokens and MXFP4 weights
+ *   mxfp4_expert_linear_quantized  the routed expert linear on MXFP4 tokens
  *
  * MXFP4. A row of I values (I a multiple of 32) is I/32 groups of 16 bytes
  * (two E2M1 codes each, the lower value in the low nibble) and one scale byte
@@ -84,6 +86,44 @@ int mxfp4_quantize(const void* x, int dtype, int64_t row_stride, int64_t rows, i
  */
 int mxfp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows, int64_t I,
                      void* out, int dtype, void* stream);
+
+/*
+ * out[t, o] = sum_i x[t, i] w[o, i] of MXFP4 tokens (T, I) and MXFP4 weights
+ * (O, I). Products are exact and add up in float32 on the tensor cores; the
+ * result is rounded once to `out_dtype`. The order of every sum is fixed, so
+ * the same call on the same inputs gives the same bits. x_packed and
+ * packed_weights lie on 16-byte boundaries, scale bytes anywhere.
+ *
+ * workspace: mxfp4_linear_workspace_size() bytes on a 256-byte boundary (0
+ * bytes for most sizes: NULL then), not needing any contents, used by this
+ * call alone until it is done.
+ */
+size_t mxfp4_linear_workspace_size(int64_t T, int64_t I, int64_t O);
+int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales, const uint8_t* packed_weights,
+                 const uint8_t* scale_bytes, void* out, int64_t T, int64_t I, int64_t O,
+                 int out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mxfp4_expert_linear on MXFP4 tokens:
+ *
+ *   out[t] = shared_output[t] + sum_k mixture_weights[t,k] W_{selected_experts[t,k]} x_t
+ *
+ * x_packed (T, I/32, 16) and x_scales (T, I/32) are the tokens; the weights,
+ * the routing and the shared output are as there, except for scale bytes of
+ * 255 (NaN). `dtype` is that of shared_output and out. Each pair's result is
+ * a float32 sum, as in mxfp4_linear; they are added to the shared output in
+ * slot order in float32 and rounded once. An expert id out of range
+ * contributes nothing and is counted for mxfp4el_device_errors(). At most
+ * 4096 experts may have tokens: min(E, T * K) <= 4096.
+ */
+size_t mxfp4_expert_linear_quantized_workspace_size(int64_t T, int64_t E, int64_t I, int64_t O,
+                                                    int64_t K);
+int mxfp4_expert_linear_quantized(const uint8_t* x_packed, const uint8_t* x_scales,
+                                  const uint8_t* packed_weights, const uint8_t* scale_bytes,
+                                  const void* selected_experts, const float* mixture_weights,
+                                  const void* shared_output, void* out, int64_t T, int64_t E,
+                                  int64_t I, int64_t O, int64_t K, int dtype, int index_dtype,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

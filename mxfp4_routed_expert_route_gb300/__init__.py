@@ -21,7 +21,8 @@ import torch
 from . import _native, attention
 from .attention import (PagedKVCache, PagedSequences, append_kv, attention_workspace, page_errors,
                         paged_attention_decode, paged_attention_prefill)
-from .quantized import dequantize_mxfp4, quantize_mxfp4, route_experts
+from .quantized import (dequantize_mxfp4, mxfp4_expert_linear_quantized, mxfp4_linear,
+                        quantize_mxfp4, route_experts)
 
 __all__ = ["mxfp4_expert_linear", "workspace_size", "device_errors", "wait_timeouts",
            "LibraryNotBuilt", "MXFP4Error", "router_topk", "mxfp4_expert_linear_routed",
@@ -29,7 +30,8 @@ __all__ = ["mxfp4_expert_linear", "workspace_size", "device_errors", "wait_timeo
            "prepare_weights", "prepared_bytes", "mxfp4_expert_linear_prepared",
            "prepared_workspace_size", "PagedKVCache", "PagedSequences", "append_kv",
            "paged_attention_decode", "paged_attention_prefill", "attention_workspace",
-           "page_errors", "route_experts", "quantize_mxfp4", "dequantize_mxfp4"]
+           "page_errors", "route_experts", "quantize_mxfp4", "dequantize_mxfp4",
+           "mxfp4_linear", "mxfp4_expert_linear_quantized"]
 
 LibraryNotBuilt = _native.LibraryNotBuilt
 MXFP4Error = _native.MXFP4Error

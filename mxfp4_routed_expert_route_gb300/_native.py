@@ -108,6 +108,11 @@ SIGNATURES = {
                                    _INT, _FLT, _P, _P, _P]),
     "mxfp4_quantize": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P]),
     "mxfp4_dequantize": (_INT, [_P, _P, _I64, _I64, _P, _INT, _P]),
+    "mxfp4_linear": (_INT, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _SZ, _P]),
+    "mxfp4_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "mxfp4_expert_linear_quantized": (_INT, [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64,
+                                             _I64, _I64, _INT, _INT, _P, _SZ, _P]),
+    "mxfp4_expert_linear_quantized_workspace_size": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
 }
 
 _lock = threading.Lock()

@@ -23,7 +23,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "gemv.cu", "gemm_tc.cu", "combine.cu", "static_scratch.cu",
            "router.cu", "swiglu.cu", "prepare.cu", "attn_api.cu", "kv_append.cu",
            "attn_simt.cu", "attn_decode.cu", "attn_prefill.cu", "quant_api.cu", "quant.cu",
-           "route_experts.cu"]
+           "route_experts.cu", "gemm_mx.cu"]
 
 
 def nvcc() -> str:

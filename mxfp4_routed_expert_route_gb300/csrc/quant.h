@@ -29,4 +29,22 @@ cudaError_t launch_quantize(const void* x, int dtype, int64_t row_stride, int64_
 cudaError_t launch_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows,
                               int64_t I, void* out, int dtype, cudaStream_t stream);
 
+// Products of MXFP4 tokens and MXFP4 weights (gemm_mx.cu). Experts with tokens
+// that one call may have (their blocks' prefix is kept in shared memory).
+constexpr int64_t kMxMaxActive = 4096;
+
+struct MxGemm {
+  const uint8_t *x_packed, *x_scales;   // [T][I/2], [T][I/32]
+  const uint8_t *w_packed, *w_scales;   // [E][O][I/2], [E][O][I/32]
+  const RoutePlan* plan;                // routing lists, or null: dense (E = 1)
+  int64_t T, E, I, O, K;                // K: picks per token (routed)
+  int splits;                           // gemm_mx_splits(): units that share K
+  float* part;                          // [pair or token][split][O] (routed, or splits > 1)
+  void* out;                            // dense: [T][O] of out_dtype
+  int out_dtype;
+};
+int gemm_mx_splits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed);
+bool gemm_mx_supported(int64_t T, int64_t E, int64_t K);
+cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream);
+
 }  // namespace mxfp4el

@@ -32,6 +32,57 @@ size_t span_bytes(int64_t rows, int64_t stride, int64_t width, size_t esize) {
   return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * esize;
 }
 
+// Sizes of a product that every index in the kernels has room for.
+bool product_fits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
+  if (T > (1 << 30) || E > kMaxDim || I > kMaxDim / 2 || O > kMaxDim / 2 || K > kMaxDim)
+    return false;
+  if (K > 0 && T > (1 << 30) / K) return false;         // pair ids are int32
+  if (O > 0 && E > kMaxElements / I / O) return false;
+  return O == 0 || K == 0 || T * K <= kMaxElements / O;
+}
+
+// The units of a call (gemm_mx.cu numbers them in 31 bits).
+bool units_fit(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
+  const int64_t active = routed ? (E < T * K ? E : T * K) : 1;
+  const int64_t blocks = active + T * K / 32 + 1;
+  const int64_t per = (O + 127) / 128 * gemm_mx_splits(T, E, I, O, K, routed);
+  return blocks <= kMaxDim / per;
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+struct ExpertWorkspace {
+  RoutePlan plan;
+  int* wc_global;
+  float* part;
+  int splits;
+  size_t bytes;
+};
+
+// The scratch of a routed call; base == nullptr only sizes.
+ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
+  ExpertWorkspace ws = {};
+  size_t off = 0;
+  auto take = [&](size_t bytes) -> void* {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return base ? static_cast<char*>(base) + at : nullptr;
+  };
+  const size_t P = (size_t)T * K;
+  ws.plan.meta = static_cast<int*>(take(kMetaWords * sizeof(int)));
+  ws.plan.counts = static_cast<int*>(take((size_t)E * sizeof(int)));
+  ws.plan.offsets = static_cast<int*>(take((size_t)(E + 1) * sizeof(int)));
+  ws.plan.active = static_cast<int*>(take((size_t)E * sizeof(int)));
+  ws.plan.pair_list = static_cast<int*>(take(P * sizeof(int)));
+  const size_t wc = route_global_counter_words(T, K, E, false);
+  ws.wc_global = wc ? static_cast<int*>(take(wc * sizeof(int))) : nullptr;
+  ws.splits = K > 0 && E > 0 ? gemm_mx_splits(T, E, I, O, K, true) : 1;
+  ws.part = static_cast<float*>(take(P * ws.splits * (size_t)O * sizeof(float)));
+  ws.bytes = off;
+  return ws;
+}
+
 int status_of(cudaError_t err) { return err == cudaSuccess ? MXFP4EL_OK : MXFP4EL_ERR_CUDA; }
 
 }  // namespace
@@ -117,4 +168,132 @@ extern "C" int mxfp4_dequantize(const uint8_t* packed, const uint8_t* scales, in
     return MXFP4EL_ERR_ALIAS;
   return status_of(launch_dequantize(packed, scales, rows, I, out, dtype,
                                      static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t mxfp4_linear_workspace_size(int64_t T, int64_t I, int64_t O) {
+  if (T < 0 || O < 0 || I <= 0 || I % 32 != 0 || !product_fits(T, 1, I, O, 1)) return (size_t)-1;
+  if (T == 0 || O == 0) return 0;
+  const int splits = gemm_mx_splits(T, 1, I, O, 1, false);
+  return splits > 1 ? align_up((size_t)T * O * splits * sizeof(float)) : 0;
+}
+
+extern "C" int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales,
+                            const uint8_t* packed_weights, const uint8_t* scale_bytes, void* out,
+                            int64_t T, int64_t I, int64_t O, int out_dtype, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  if (!known_dtype(out_dtype)) return MXFP4EL_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || O < 0 || I <= 0 || I % 32 != 0) return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (!product_fits(T, 1, I, O, 1)) return MXFP4EL_ERR_TOO_LARGE;
+  if (T == 0 || O == 0) return MXFP4EL_OK;
+  if (!units_fit(T, 1, I, O, 1, false)) return MXFP4EL_ERR_TOO_LARGE;
+  const size_t es = size_of(out_dtype), G = (size_t)I / 32;
+  if (x_packed == nullptr || x_scales == nullptr || packed_weights == nullptr ||
+      scale_bytes == nullptr || out == nullptr || !aligned(x_packed, 16) ||
+      !aligned(packed_weights, 16) || !aligned(out, es))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
+  const size_t no = (size_t)T * O * es;
+  const size_t nw = mxfp4_linear_workspace_size(T, I, O);
+  const void* inputs[] = {x_packed, x_scales, packed_weights, scale_bytes};
+  const size_t sizes[] = {T * G * 16, T * G, O * G * 16, O * G};
+  for (int i = 0; i < 4; ++i)
+    if (overlaps(out, no, inputs[i], sizes[i])) return MXFP4EL_ERR_ALIAS;
+  if (nw > 0) {
+    if (workspace == nullptr || workspace_bytes < nw || !aligned(workspace, kAlign))
+      return MXFP4EL_ERR_WORKSPACE;
+    if (overlaps(workspace, nw, out, no)) return MXFP4EL_ERR_ALIAS;
+    for (int i = 0; i < 4; ++i)
+      if (overlaps(workspace, nw, inputs[i], sizes[i])) return MXFP4EL_ERR_ALIAS;
+  }
+  MxGemm g = {};
+  g.x_packed = x_packed;
+  g.x_scales = x_scales;
+  g.w_packed = packed_weights;
+  g.w_scales = scale_bytes;
+  g.T = T;
+  g.E = 1;
+  g.I = I;
+  g.O = O;
+  g.K = 1;
+  g.splits = gemm_mx_splits(T, 1, I, O, 1, false);
+  g.part = static_cast<float*>(workspace);
+  g.out = out;
+  g.out_dtype = out_dtype;
+  return status_of(launch_gemm_mx(g, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t mxfp4_expert_linear_quantized_workspace_size(int64_t T, int64_t E, int64_t I,
+                                                               int64_t O, int64_t K) {
+  if (T < 0 || E < 0 || O < 0 || K < 0 || I <= 0 || I % 32 != 0 || !product_fits(T, E, I, O, K))
+    return (size_t)-1;
+  if (T == 0 || O == 0) return 0;
+  return carve(nullptr, T, E, I, O, K).bytes;
+}
+
+extern "C" int mxfp4_expert_linear_quantized(
+    const uint8_t* x_packed, const uint8_t* x_scales, const uint8_t* packed_weights,
+    const uint8_t* scale_bytes, const void* selected_experts, const float* mixture_weights,
+    const void* shared_output, void* out, int64_t T, int64_t E, int64_t I, int64_t O, int64_t K,
+    int dtype, int index_dtype, void* workspace, size_t workspace_bytes, void* stream_) {
+  if (!known_dtype(dtype) ||
+      (index_dtype != MXFP4EL_INDEX_I32 && index_dtype != MXFP4EL_INDEX_I64))
+    return MXFP4EL_ERR_UNSUPPORTED_DTYPE;
+  if (T < 0 || E < 0 || O < 0 || K < 0 || I <= 0 || I % 32 != 0)
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (!product_fits(T, E, I, O, K)) return MXFP4EL_ERR_TOO_LARGE;
+  if (T == 0 || O == 0) return MXFP4EL_OK;
+  const bool product = K > 0 && E > 0;
+  if (product && (!gemm_mx_supported(T, E, K) || !units_fit(T, E, I, O, K, true)))
+    return MXFP4EL_ERR_TOO_LARGE;
+  const size_t es = size_of(dtype), is = index_dtype == MXFP4EL_INDEX_I64 ? 8 : 4;
+  const size_t G = (size_t)I / 32;
+  if (shared_output == nullptr || out == nullptr || !aligned(shared_output, es) ||
+      !aligned(out, es))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (K > 0 && (x_packed == nullptr || x_scales == nullptr || selected_experts == nullptr ||
+                mixture_weights == nullptr || !aligned(x_packed, 16) ||
+                !aligned(selected_experts, is) || !aligned(mixture_weights, 4)))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
+  if (product && (packed_weights == nullptr || scale_bytes == nullptr ||
+                  !aligned(packed_weights, 16)))
+    return MXFP4EL_ERR_INVALID_ARGUMENT;
+  const size_t no = (size_t)T * O * es;
+  const size_t nw = carve(nullptr, T, E, I, O, K).bytes;
+  const void* inputs[] = {x_packed,         x_scales,        packed_weights, scale_bytes,
+                          selected_experts, mixture_weights, shared_output};
+  const size_t sizes[] = {T * G * 16,         T * G,  (size_t)E * O * G * 16, (size_t)E * O * G,
+                          (size_t)T * K * is, (size_t)T * K * 4, no};
+  for (int i = 0; i < 7; ++i)
+    if (overlaps(out, no, inputs[i], sizes[i])) return MXFP4EL_ERR_ALIAS;
+  if (workspace == nullptr || workspace_bytes < nw || !aligned(workspace, kAlign))
+    return MXFP4EL_ERR_WORKSPACE;
+  if (overlaps(workspace, nw, out, no)) return MXFP4EL_ERR_ALIAS;
+  for (int i = 0; i < 7; ++i)
+    if (overlaps(workspace, nw, inputs[i], sizes[i])) return MXFP4EL_ERR_ALIAS;
+  const ExpertWorkspace ws = carve(workspace, T, E, I, O, K);
+  const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (K > 0) {
+    // With E == 0 every id is out of range: the bucketer counts them.
+    if (launch_route(selected_experts, index_dtype, T, K, E, ws.wc_global, ws.plan,
+                     TokenPrep{nullptr, nullptr, nullptr, I}, UnitSplit{0, 0, 0, 1000},
+                     stream) != cudaSuccess)
+      return MXFP4EL_ERR_CUDA;
+    if (product) {
+      MxGemm g = {};
+      g.x_packed = x_packed;
+      g.x_scales = x_scales;
+      g.w_packed = packed_weights;
+      g.w_scales = scale_bytes;
+      g.plan = &ws.plan;
+      g.T = T;
+      g.E = E;
+      g.I = I;
+      g.O = O;
+      g.K = K;
+      g.splits = ws.splits;
+      g.part = ws.part;
+      if (launch_gemm_mx(g, stream) != cudaSuccess) return MXFP4EL_ERR_CUDA;
+    }
+  }
+  return status_of(launch_combine(shared_output, selected_experts, index_dtype, mixture_weights,
+                                  ws.part, ws.splits, out, dtype, T, E, O, K, product, stream));
 }

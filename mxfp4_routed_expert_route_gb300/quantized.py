@@ -1,5 +1,6 @@
 """The operators around the MXFP4 routed experts on quantised tokens: experts
-and mixture weights from router logits, and rows of values to MXFP4 and back.
+and mixture weights from router logits, rows of values to MXFP4 and back, and
+products of MXFP4 tokens with MXFP4 weights, dense and routed.
 
 Like the rest of the package this is the thin Python face of the C library
 (header ``include/mxfp4el_quantized.h``): it checks and marshals arguments;
@@ -10,13 +11,18 @@ as the experts' weights are.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _native
 
-__all__ = ["route_experts", "quantize_mxfp4", "dequantize_mxfp4"]
+__all__ = ["route_experts", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_linear",
+           "mxfp4_expert_linear_quantized"]
 
 _DTYPES = {torch.float32: _native.DTYPE_F32, torch.bfloat16: _native.DTYPE_BF16}
+_INDEX_DTYPES = {torch.int32: _native.INDEX_I32, torch.int64: _native.INDEX_I64}
+_REJECTED = ctypes.c_size_t(-1).value     # a workspace size the library has no answer for
 _SCORES = {"softmax": _native.SCORE_SOFTMAX, "sigmoid": _native.SCORE_SIGMOID}
 
 # The current stream's handle of a device by index (see attention.py).
@@ -161,4 +167,88 @@ def dequantize_mxfp4(packed: torch.Tensor, scales: torch.Tensor,
     if rows:
         _call(_native.load().mxfp4_dequantize, "dequantize_mxfp4", packed.get_device(), (
             packed.data_ptr(), scales.data_ptr(), rows, I, out.data_ptr(), _DTYPES[dtype]))
+    return out
+
+
+def mxfp4_linear(x_packed: torch.Tensor, x_scales: torch.Tensor, packed_weights: torch.Tensor,
+                 scale_bytes: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """out (T, O) = X W^T of MXFP4 tokens X (x_packed (T, I/32, 16), x_scales
+    (T, I/32)) and MXFP4 weights W (packed_weights (O, I/32, 16), scale_bytes
+    (O, I/32)), in float32 or bfloat16. Products are exact, sums float32. See
+    mxfp4_linear in the C header."""
+    _mxfp4_rows("tokens", x_packed, x_scales)
+    _mxfp4_rows("weights", packed_weights, scale_bytes)
+    if x_packed.dim() != 3 or packed_weights.dim() != 3 \
+            or x_packed.shape[1] != packed_weights.shape[1]:
+        raise ValueError("expected tokens (T, I/32, 16) and weights (O, I/32, 16)")
+    if packed_weights.device != x_packed.device:
+        raise ValueError(f"weights are on {packed_weights.device}, tokens on {x_packed.device}")
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    T, G, _ = x_packed.shape
+    I, O = 32 * G, packed_weights.shape[0]
+    out = _output("out", out, (T, O), dtype, x_packed)
+    if T and O:
+        lib = _native.load()
+        need = lib.mxfp4_linear_workspace_size(T, I, O)
+        if need == _REJECTED:
+            raise ValueError("sizes rejected by the library")
+        ws = torch.empty(need, dtype=torch.uint8, device=x_packed.device) if need else None
+        _call(lib.mxfp4_linear, "mxfp4_linear", x_packed.get_device(), (
+            x_packed.data_ptr(), x_scales.data_ptr(), packed_weights.data_ptr(),
+            scale_bytes.data_ptr(), out.data_ptr(), T, I, O, _DTYPES[dtype],
+            None if ws is None else ws.data_ptr(), need))
+    return out
+
+
+def mxfp4_expert_linear_quantized(x_packed: torch.Tensor, x_scales: torch.Tensor,
+                                  packed_weights: torch.Tensor, scale_bytes: torch.Tensor,
+                                  selected_experts: torch.Tensor, mixture_weights: torch.Tensor,
+                                  shared_output: torch.Tensor,
+                                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """The routed expert linear on MXFP4 tokens: out[t] = shared_output[t] +
+    sum_k mixture_weights[t, k] W_{selected_experts[t, k]} x_t.
+
+    Tokens are x_packed (T, I/32, 16) and x_scales (T, I/32) uint8, as
+    :func:`quantize_mxfp4` makes them; packed_weights (E, O, I/32, 16) and
+    scale_bytes (E, O, I/32) uint8; selected_experts (T, K) int32 or int64;
+    mixture_weights (T, K) float32; shared_output (T, O) float32 or bfloat16,
+    whose dtype the result has. All contiguous, on one CUDA device. An expert
+    id out of range contributes nothing (see ``device_errors``). See
+    mxfp4_expert_linear_quantized in the C header.
+    """
+    sel, p, ys = selected_experts, mixture_weights, shared_output
+    _mxfp4_rows("tokens", x_packed, x_scales)
+    _mxfp4_rows("weights", packed_weights, scale_bytes)
+    if x_packed.dim() != 3 or packed_weights.dim() != 4 \
+            or x_packed.shape[1] != packed_weights.shape[2]:
+        raise ValueError("expected tokens (T, I/32, 16) and weights (E, O, I/32, 16)")
+    T, G, _ = x_packed.shape
+    E, O = packed_weights.shape[:2]
+    index = x_packed.get_device()
+    for name, t in (("weights", packed_weights), ("selected_experts", sel),
+                    ("mixture_weights", p), ("shared_output", ys)):
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, tokens on {x_packed.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if sel.dtype not in _INDEX_DTYPES or p.dtype is not torch.float32:
+        raise TypeError("selected_experts must be int32 or int64, mixture_weights float32")
+    if ys.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {ys.dtype}")
+    if sel.dim() != 2 or sel.shape[0] != T or p.shape != sel.shape or ys.shape != (T, O):
+        raise ValueError("routing or shared-output shape mismatch")
+    K, I = sel.shape[1], 32 * G
+    out = _output("out", out, (T, O), ys.dtype, ys)
+    if T and O:
+        lib = _native.load()
+        need = lib.mxfp4_expert_linear_quantized_workspace_size(T, E, I, O, K)
+        if need == _REJECTED:
+            raise ValueError("sizes rejected by the library")
+        ws = torch.empty(need, dtype=torch.uint8, device=ys.device)
+        _call(lib.mxfp4_expert_linear_quantized, "mxfp4_expert_linear_quantized", index, (
+            x_packed.data_ptr(), x_scales.data_ptr(), packed_weights.data_ptr(),
+            scale_bytes.data_ptr(), sel.data_ptr(), p.data_ptr(), ys.data_ptr(), out.data_ptr(),
+            T, E, I, O, K, _DTYPES[ys.dtype], _INDEX_DTYPES[sel.dtype], ws.data_ptr(), need))
     return out

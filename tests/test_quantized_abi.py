@@ -119,3 +119,67 @@ def test_the_reference_router():
     # NaN is never selected
     ids, w = ref.route(torch.tensor([[float("nan"), 1.0]]), 2)
     assert ids.tolist() == [[1, -1]] and w.tolist() == [[1.0, 0.0]]
+
+
+def test_linear_checks(lib):
+    from mxfp4_routed_expert_route_gb300 import _native as n
+    size = lib.mxfp4_linear_workspace_size
+    rejected = ctypes.c_size_t(-1).value
+    assert size(0, 64, 8) == 0 and size(4, 64, 0) == 0
+    for args in ((4, 48, 8), (-1, 64, 8), (4, 64, -8), (1 << 40, 64, 8), (4, 1 << 40, 8)):
+        assert size(*args) == rejected, args
+    need = size(4, 7168, 256)
+    assert need > 0 and need % 256 == 0            # few tiles: K is split over units
+
+    def f(xp=1 << 24, xs=1 << 26, wp=1 << 28, ws=1 << 30, out=1 << 32, T=4, I=7168, O=256, dtype=1,
+          work=1 << 36, nwork=need):
+        return lib.mxfp4_linear(xp, xs, wp, ws, out, T, I, O, dtype, work, nwork, None)
+
+    bad, big, alias = n.ERR_INVALID_ARGUMENT, n.ERR_TOO_LARGE, n.ERR_ALIAS
+    for code, kw in ((n.ERR_UNSUPPORTED_DTYPE, dict(dtype=3)), (bad, dict(T=-1)), (bad, dict(I=33)),
+                     (bad, dict(I=0)), (bad, dict(O=-1)), (bad, dict(xp=None)), (bad, dict(xs=None)),
+                     (bad, dict(wp=None)), (bad, dict(ws=None)), (bad, dict(out=None)),
+                     (bad, dict(xp=(1 << 24) + 8)), (bad, dict(wp=(1 << 28) + 4)),
+                     (bad, dict(out=(1 << 32) + 1)), (big, dict(T=1 << 31)), (big, dict(O=1 << 31)),
+                     (big, dict(T=1 << 30, O=1 << 29)), (alias, dict(out=(1 << 28) + 64)),
+                     (alias, dict(out=(1 << 26) - 64)), (n.ERR_WORKSPACE, dict(work=None)),
+                     (n.ERR_WORKSPACE, dict(nwork=need - 1)),
+                     (n.ERR_WORKSPACE, dict(work=(1 << 36) + 64)), (alias, dict(work=1 << 32)),
+                     (alias, dict(work=1 << 28)), (n.OK, dict(T=0)), (n.OK, dict(O=0))):
+        assert f(**kw) == code, kw
+
+
+def test_expert_linear_quantized_checks(lib):
+    from mxfp4_routed_expert_route_gb300 import _native as n
+    size = lib.mxfp4_expert_linear_quantized_workspace_size
+    rejected = ctypes.c_size_t(-1).value
+    assert size(0, 4, 64, 8, 2) == 0 and size(4, 4, 64, 0, 2) == 0
+    for args in ((4, 4, 60, 8, 2), (-1, 4, 64, 8, 2), (1 << 40, 4, 64, 8, 2),
+                 (1 << 20, 4, 64, 8, 1 << 20), (4, 1 << 20, 1 << 20, 1 << 20, 2)):
+        assert size(*args) == rejected, args
+    need = size(6, 4, 64, 70, 2)
+    assert need >= 6 * 2 * 70 * 4 and need % 256 == 0
+
+    def f(xp=1 << 24, xs=1 << 26, wp=1 << 28, ws=1 << 30, sel=1 << 31, p=1 << 32, ys=1 << 33,
+          out=1 << 34, T=6, E=4, I=64, O=70, K=2, dtype=1, idx=0, work=1 << 36, nwork=need):
+        return lib.mxfp4_expert_linear_quantized(xp, xs, wp, ws, sel, p, ys, out, T, E, I, O, K,
+                                                 dtype, idx, work, nwork, None)
+
+    bad, big, alias = n.ERR_INVALID_ARGUMENT, n.ERR_TOO_LARGE, n.ERR_ALIAS
+    dt, nows = n.ERR_UNSUPPORTED_DTYPE, n.ERR_WORKSPACE
+    for code, kw in ((dt, dict(dtype=2)), (dt, dict(idx=2)), (bad, dict(T=-1)), (bad, dict(E=-1)),
+                     (bad, dict(I=40)), (bad, dict(O=-2)), (bad, dict(K=-1)), (bad, dict(xp=None)),
+                     (bad, dict(xs=None)), (bad, dict(wp=None)), (bad, dict(ws=None)),
+                     (bad, dict(sel=None)), (bad, dict(p=None)), (bad, dict(ys=None)),
+                     (bad, dict(out=None)), (bad, dict(xp=(1 << 24) + 8)),
+                     (bad, dict(wp=(1 << 28) + 8)), (bad, dict(sel=(1 << 31) + 2)),
+                     (bad, dict(idx=1, sel=(1 << 31) + 4)), (bad, dict(p=(1 << 32) + 2)),
+                     (bad, dict(ys=(1 << 33) + 1)), (bad, dict(out=(1 << 34) + 1)),
+                     (big, dict(T=1 << 31)), (big, dict(T=1 << 20, K=1 << 20)),
+                     (big, dict(T=5000, E=5000, K=1)), (alias, dict(out=(1 << 33) + 16)),
+                     (alias, dict(out=(1 << 24) + 16)), (alias, dict(out=(1 << 28) + 16)),
+                     (alias, dict(out=(1 << 32) - 16)), (nows, dict(work=None)),
+                     (nows, dict(nwork=need - 1)), (nows, dict(work=(1 << 36) + 128)),
+                     (alias, dict(work=1 << 34)), (alias, dict(work=1 << 33)),
+                     (n.OK, dict(T=0)), (n.OK, dict(O=0))):
+        assert f(**kw) == code, kw
