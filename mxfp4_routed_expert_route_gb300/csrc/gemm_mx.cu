@@ -13,29 +13,40 @@
 // the weights alone are read from HBM, so the weights take the operand with
 // the fixed 128 rows and the tokens the one whose width can be small.
 //
-// Routed (kRouted): a block is up to kN of one expert's pairs in the lists of
-// route.cu; the token rows are gathered by the copies themselves (four rows
-// each, tile::gather4), and float32 results go to part[pair][split][o]. Dense:
-// a block is consecutive tokens and results go to out[t][o], or to
-// part[t][split][o] where K is split over several units.
+// Routed: a block is up to kN of one expert's pairs in the lists of route.cu,
+// and float32 results go to part[pair][split][o]. Narrow blocks (kN = 32)
+// gather their token rows with the copies themselves (four rows each,
+// tile::gather4); wide ones read a copy of the rows in the lists' order, since
+// gathers issue one at a time (some 75 cycles each: the skewed prefill's
+// product took 4.04 ms with them, 1.54 without the tokens). Dense: a block is
+// consecutive tokens and results go to out[t][o], or to part[t][split][o] where
+// K is split over several units.
 //
 // Scale bytes. The tensor core wants them in tensor memory, 32 lanes by 4
-// bytes of 128 rows' scales for four groups (512 bytes); tcgen05.cp brings
-// such a block from shared memory and repeats it for the four lane quarters.
-// In memory they are rows of I/32 bytes on no particular alignment, so four
-// warps read them with ordinary loads (32 bytes of a row at a time, one row
-// per thread, one chunk ahead) and store each row's four bytes of four groups
-// where the block has them: row r at 16 (r % 32) + 4 (r / 32).
+// bytes of 128 rows' scales for four groups (512 bytes, row r at 16 (r % 32) +
+// 4 (r / 32)); tcgen05.cp brings such a block from shared memory and repeats it
+// for the four lane quarters. In memory they are rows of I/32 bytes on no
+// particular alignment, so four warps read them with ordinary loads and store
+// the blocks: two teams, which take two stages at a time in turn (16 bytes of a
+// row), one warp of each for the weights' rows and one for the tokens', lane l
+// the rows l, l + 32, ..., whose four words lie together in the block. While one
+// team's loads and its fence between these stores and the tensor core are
+// under way, the other has the next two stages. (A team's next stages are four
+// on, and the ring has at least as many: a team further ahead than the ring is
+// long could not tell a stage's phases apart.)
 //
 // K that is no multiple of 256: the copies fill codes past a row's end with
 // zeros, and scale bytes past it are set to 0, so what is added is exactly 0;
 // MMAs wholly past the end are not issued.
 //
 // Warp roles in a CTA of 12 warps (one CTA per SM, persistent over units
-// (block, 128-row tile, K split) in a fixed order):
-//   warp 0      copies of codes (weights and tokens), TMEM allocation
-//   warp 1      scale copies to tensor memory and MMAs, one elected lane
+// (block, 128-row tile, K split)):
+//   warp 0      copies of codes (weights and tokens), one thread; TMEM
+//   warp 1      scale copies to tensor memory and MMAs, one thread
 //   warp 2      prefix of the experts' blocks at start (routed)
+//   warp 3      the units: finds each next one and hands it to the other roles
+//               through a ring in shared memory, ahead of them (finding one
+//               takes several dependent loads)
 //   warps 4-7   scale bytes
 //   warps 8-11  epilogue: tensor memory -> float32 or bf16 results
 // Two accumulators, so the epilogue of a unit runs beside the next unit's
@@ -65,9 +76,14 @@ constexpr uint32_t kStageA = kBM * kRowBytes;
 constexpr uint32_t kSfBlock = 512;             // 128 rows' scales of four groups
 constexpr int kSfPerStage = kGroupsPerStage / 4;
 constexpr int kMaxStages = 12;
+constexpr int kMxNarrow = 32, kMxWide = 192;   // tokens of a block, at most
 constexpr uint32_t kTmemCols = 512;
-constexpr int kScaleWarp0 = 4, kScaleWarps = 4, kEpiWarp0 = 8, kEpiWarps = 4;
-constexpr int kChunkStages = 4;                // stages whose scales one read brings (32 bytes)
+constexpr int kUnitWarp = 3, kScaleWarp0 = 4, kScaleWarps = 4, kEpiWarp0 = 8, kEpiWarps = 4;
+constexpr int kScaleTeams = 2;
+constexpr int kUnitRing = 8;
+constexpr int kUnitReaders = 2 + kScaleWarps + kEpiWarps;
+constexpr int kPairStages = 2;                 // stages whose scales one read brings (16 bytes)
+constexpr int kMinStages = kPairStages * kScaleTeams;
 constexpr size_t kSmemLimit = 227 * 1024;
 
 template <int kN>
@@ -86,25 +102,40 @@ struct Shape {
 
 struct MxMaps {
   CUtensorMap a;      // weights' codes [E][O][I/2], box {128, 128, 1}, 128-byte swizzle
-  CUtensorMap b;      // tokens' codes [T][I/2], box {128, 32} (dense) or {128, 1} (gathered)
+  CUtensorMap b;      // tokens' codes [rows][I/2], box {128, 32}, or {128, 1} (gathered)
 };
 
 struct MxKernelArgs {
   RoutePlan plan;               // routed
   const uint8_t* w_scales;      // [E][O][G]
-  const uint8_t* x_scales;      // [T][G]
+  const uint8_t* x_scales;      // [rows][x_pitch]
   void* out;
   unsigned long long* status;
-  int T, O, G, K;
-  int mtiles, splits, stages, max_active;
+  int T, O, G, K, x_pitch;
+  int mtiles, splits, blocks, stages, max_active;
 };
 
+// One unit of work.
+struct __align__(16) Unit {
+  int e;              // expert (0 when dense); -1: no more units
+  int m0;             // first weight row
+  int tok0, ntok;     // block: first position (in the lists, or token) and tokens
+  int nmma;           // MMA N: ntok rounded up to 16
+  int split;
+  int kt0, kt1;       // stages of K
+  int once;           // this block alone reads the weights
+};
+
+template <int kRows>
 struct __align__(16) MxShared {
-  uint64_t full_tma[kMaxStages], full_sf[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t d_full[2], d_empty[2];
+  uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
   uint32_t tmem_base;
   int num_units, num_active;
+  Unit units[kUnitRing];
+  int rows[kUnitRing][kRows];   // token of each row of the block (gathered)
 };
 
 __device__ __forceinline__ bool elect_one() {
@@ -184,16 +215,6 @@ struct RingPos {
   }
 };
 
-// One unit of work, derived identically by every role from its index.
-struct Unit {
-  int e;              // expert (0 when dense)
-  int m0;             // first weight row
-  int tok0, ntok;     // block: first position (in the lists, or token) and tokens
-  int nmma;           // MMA N: ntok rounded up to 16
-  int split;
-  int kt0, kt1;       // stages of K
-};
-
 template <int kN, bool kRouted>
 __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix, int num_active,
                                         int idx) {
@@ -216,7 +237,7 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix
   } else {
     w.e = 0;
     cnt = a.T;
-    nblk = (a.T + kN - 1) / kN;
+    nblk = a.blocks;
     local = idx;
   }
   // The blocks of a tile follow one another, so its codes come from L2 after
@@ -231,60 +252,194 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix
   const int nk = (a.G + kGroupsPerStage - 1) / kGroupsPerStage;
   w.kt0 = (int)((int64_t)w.split * nk / a.splits);
   w.kt1 = (int)((int64_t)(w.split + 1) * nk / a.splits);
+  w.once = nblk == 1;
   return w;
 }
 
-// 32 bytes from p as eight words; bytes at `end` and past it are 0. Reads
+// 16 bytes from p as four words; bytes at `end` and past it are 0. Reads
 // only aligned words that hold a byte before `end`.
-__device__ __forceinline__ void load_scales(const uint8_t* p, const uint8_t* end,
-                                            uint32_t (&w)[8]) {
+__device__ __forceinline__ uint4 load_scales(const uint8_t* p, const uint8_t* end) {
   const int64_t left = end - p;
-  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && left >= 32) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint4 v = *reinterpret_cast<const uint4*>(p + 16);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
-    return;
-  }
+  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && left >= 16)
+    return *reinterpret_cast<const uint4*>(p);
   const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3) * 8;
   const uint8_t* at = p - sh / 8;
-  uint32_t v[9];
+  uint32_t v[5], w[4];
 #pragma unroll
-  for (int i = 0; i < 9; ++i)
+  for (int i = 0; i < 5; ++i)
     v[i] = at + 4 * i < end ? *reinterpret_cast<const uint32_t*>(at + 4 * i) : 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     w[i] = __funnelshift_r(v[i], v[i + 1], sh);
     const int64_t n = left - 4 * i;
     if (n < 4) w[i] = n > 0 ? w[i] & ((1u << (8 * (int)n)) - 1u) : 0u;
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// The next unit of this role, by a whole warp or (kWarp = false) one thread.
+template <bool kWarp, int kRows>
+__device__ __forceinline__ bool pop_unit(MxShared<kRows>& sh, RingPos& pu, Unit* w) {
+  const bool got = kWarp ? mbar_wait_warp(&sh.u_full[pu.idx], pu.phase)
+                         : mbar_wait(&sh.u_full[pu.idx], pu.phase);
+  if (!got) return false;
+  *w = sh.units[pu.idx];
+  return true;
+}
+template <bool kWarp, int kRows>
+__device__ __forceinline__ void release_unit(MxShared<kRows>& sh, RingPos& pu) {
+  if (kWarp) __syncwarp();
+  if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.u_empty[pu.idx]);
+  pu.next(kUnitRing);
+}
+
+// Stages two at a time, in the order of the units, dealt to the scale teams in
+// turn: next() moves to this team's next two. kRows: rows per lane.
+template <int kRows, bool kTokens, bool kGather>
+struct ScaleWalk {
+  Unit w;
+  int kt;                 // first of the two stages
+  int slot;               // its place in the ring of stages
+  uint32_t phase;
+  int turn;               // whose turn it is
+  const uint8_t* base[kRows];
+  RingPos pu;
+
+  __device__ __forceinline__ void start() {
+    w.e = 0;
+    w.kt1 = kt = -kPairStages;                 // nothing yet: the first step loads a unit
+    slot = 0;
+    phase = 0;
+    turn = kScaleTeams - 1;
+  }
+  template <typename Sh>
+  __device__ __forceinline__ bool load_unit(const MxKernelArgs& a, Sh& sh, int lane) {
+    if (!pop_unit<true>(sh, pu, &w)) {
+      w.e = -2;
+      return false;
+    }
+    if (w.e >= 0) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if constexpr (kTokens) {
+          const int n = min(lane + 32 * i, w.ntok - 1);
+          const int t = kGather ? sh.rows[pu.idx][n] : w.tok0 + n;
+          base[i] = a.x_scales + (size_t)t * a.x_pitch;
+        } else {
+          base[i] = a.w_scales + ((size_t)w.e * a.O + min(w.m0 + lane + 32 * i, a.O - 1)) * a.G;
+        }
+      }
+    }
+    release_unit<true>(sh, pu);
+    return true;
+  }
+  // False at the end of the units (or after a wait that gave up: w.e == -2).
+  template <typename Sh>
+  __device__ __forceinline__ bool next(const MxKernelArgs& a, Sh& sh, int team, int lane) {
+    for (;;) {
+      slot += min(kPairStages, w.kt1 - kt);
+      if (slot >= a.stages) {
+        slot -= a.stages;
+        phase ^= 1u;
+      }
+      kt += kPairStages;
+      while (kt >= w.kt1) {
+        if (!load_unit(a, sh, lane) || w.e < 0) return false;
+        kt = w.kt0;
+      }
+      turn = turn + 1 == kScaleTeams ? 0 : turn + 1;
+      if (turn == team) return true;
+    }
+  }
+};
+
+// A scale warp's whole work. block0: the offset of its first block in a stage;
+// kBlockRows: 128-row blocks of its operand. False after a wait that gave up.
+template <int kRows, int kBlockRows, bool kTokens, bool kGather, uint32_t kStageBytes, typename Sh>
+__device__ __forceinline__ bool scale_role(const MxKernelArgs& a, Sh& sh, unsigned char* ring,
+                                           uint32_t block0, int team, int lane) {
+  static_assert(kRows == 4 || kRows == 1 || kRows == 6, "a tile, a narrow and a wide block");
+  ScaleWalk<kRows, kTokens, kGather> walk;
+  walk.start();
+  uint4 cur[kRows], nxt[kRows];
+  auto fetch = [&](uint4 (&v)[kRows]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      v[i] = load_scales(walk.base[i] + walk.kt * kGroupsPerStage, walk.base[i] + a.G);
+  };
+  bool more = walk.next(a, sh, team, lane);
+  if (more) fetch(cur);
+  while (more) {
+    // These two stages, while the next two of this warp are on their way.
+    int slot = walk.slot;
+    uint32_t phase = walk.phase;
+    const int n = min(kPairStages, walk.w.kt1 - walk.kt);
+    more = walk.next(a, sh, team, lane);
+    if (more) fetch(nxt);
+#pragma unroll
+    for (int j = 0; j < kPairStages; ++j) {
+      if (j >= n) break;
+      if (j > 0 && ++slot == a.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      if (!mbar_wait_warp(&sh.empty[slot], phase ^ 1u)) return false;
+      unsigned char* sf = ring + (size_t)slot * kStageBytes + block0 + lane * 16;
+      auto word = [&](int i, int b) {              // row lane + 32 i, groups 4 b..
+        const uint4& v = cur[i];
+        return j == 0 ? (b == 0 ? v.x : v.y) : (b == 0 ? v.z : v.w);
+      };
+#pragma unroll
+      for (int b = 0; b < kSfPerStage; ++b) {
+        unsigned char* at = sf + b * kBlockRows * kSfBlock;
+        if constexpr (kRows == 1)
+          *reinterpret_cast<uint32_t*>(at) = word(0, b);
+        else
+          *reinterpret_cast<uint4*>(at) =
+              make_uint4(word(0, b), word(1, b), word(2, b), word(3, b));
+        if constexpr (kRows == 6)
+          *reinterpret_cast<uint2*>(at + kSfBlock) = make_uint2(word(4, b), word(5, b));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[slot]);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) cur[i] = nxt[i];
+  }
+  return walk.w.e != -2;
+}
+
 template <int kN, typename Out, bool kRouted>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   using S = Shape<kN>;
+  constexpr bool kGather = kRouted && kN == kMxNarrow;
+  using Shared = MxShared<kGather ? kN : 1>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  MxShared& sh = *reinterpret_cast<MxShared*>(ring + (size_t)a.stages * S::kStage);
+  Shared& sh = *reinterpret_cast<Shared*>(ring + (size_t)a.stages * S::kStage);
   int* prefix = reinterpret_cast<int*>(&sh + 1);       // [max_active + 1] (routed)
 
   const int warp = __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sh.full_tma[s], 1);
-      mbar_init(&sh.full_sf[s], kScaleWarps);
+      mbar_init(&sh.full[s], 3);                       // the copies (bytes), two scale warps
       mbar_init(&sh.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.d_full[b], 1);
       mbar_init(&sh.d_empty[b], kEpiWarps);
     }
-    mbar_init(&sh.drain, 32);                          // every lane of the MMA warp
+    for (int r = 0; r < kUnitRing; ++r) {
+      mbar_init(&sh.u_full[r], 1);
+      mbar_init(&sh.u_empty[r], kUnitReaders);
+    }
+    mbar_init(&sh.drain, 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -323,104 +478,124 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       }
     } else if (lane == 0) {
       sh.num_active = 0;
-      sh.num_units = (a.T + kN - 1) / kN * a.mtiles * a.splits;
+      sh.num_units = a.blocks * a.mtiles * a.splits;
     }
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem_base, 0);
-  const int num_units = sh.num_units, num_active = sh.num_active;
   const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------------------------------ copies of codes
-    const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_evict_last_policy();
-    const uint64_t pol_reuse = l2_evict_normal_policy();
-    RingPos pos;
-    int issued = 0;
-    for (int idx = blockIdx.x; idx < num_units && ok; idx += gridDim.x) {
-      const Unit w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
-      if (w.ntok <= 0) continue;
-      // Weights that one block reads pass through L2 once.
-      const bool once = kRouted ? w.ntok <= kN && w.tok0 == a.plan.offsets[w.e] &&
-                                      w.ntok == a.plan.offsets[w.e + 1] - w.tok0
-                                : a.T <= kN;
-      const uint64_t pol = once ? pol_once : pol_reuse;
-      const uint32_t box = kRouted ? (uint32_t)w.nmma : (uint32_t)(w.nmma + 31) / 32 * 32;
-      // Rows of this lane's gathers, four each; past the block its last token.
-      constexpr int kGathers = (kN / 4 + 31) / 32;
-      int4 rows[kGathers];
-      if constexpr (kRouted) {
-#pragma unroll
-        for (int q = 0; q < kGathers; ++q) {
-          int r[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int n = min((lane + 32 * q) * 4 + i, w.ntok - 1);
-            r[i] = a.plan.pair_list[w.tok0 + n] / a.K;
-          }
-          rows[q] = make_int4(r[0], r[1], r[2], r[3]);
-        }
+  if (warp == kUnitWarp) {
+    // ------------------------------------------------------------ the units
+    const int num_units = sh.num_units, num_active = sh.num_active;
+    RingPos pu;
+    for (int idx = blockIdx.x;; idx += gridDim.x) {
+      Unit w;
+      w.e = -1;
+      if (idx < num_units) w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
+      if (w.e >= 0 && w.ntok <= 0) continue;
+      int t = 0;
+      if (kGather && w.e >= 0)                  // past the block its last token
+        t = a.plan.pair_list[w.tok0 + min(lane, w.ntok - 1)] / a.K;
+      if (!mbar_wait_warp(&sh.u_empty[pu.idx], pu.phase ^ 1u)) {
+        ok = false;
+        break;
       }
-      for (int kt = w.kt0; kt < w.kt1; ++kt, ++issued) {
-        if (!mbar_wait_warp(&sh.empty[pos.idx], pos.phase ^ 1u)) {
+      if (kGather) sh.rows[pu.idx][lane] = t;
+      if (lane == 0) sh.units[pu.idx] = w;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.u_full[pu.idx]);
+      pu.next(kUnitRing);
+      if (w.e < 0) break;
+    }
+    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+  } else if (warp == 0) {
+    // ------------------------------------------------------ copies of codes
+    if (elect_one()) {
+      const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_evict_last_policy();
+      const uint64_t pol_reuse = l2_evict_normal_policy();
+      RingPos pos, pu;
+      int issued = 0;
+      Unit w;
+      while (ok) {
+        if (!pop_unit<false>(sh, pu, &w)) {
           ok = false;
           break;
         }
-        unsigned char* stage = ring + (size_t)pos.idx * S::kStage;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&sh.full_tma[pos.idx], kStageA + box * kRowBytes);
-          tma_load_3d(stage, &maps.a, kt * (int)kRowBytes, w.m0, w.e, &sh.full_tma[pos.idx], pol);
-          if constexpr (!kRouted)
-            for (int r = 0; r < (int)box; r += 32)
-              tma_load_2d(stage + kStageA + r * kRowBytes, &maps.b, kt * (int)kRowBytes,
-                          w.tok0 + r, &sh.full_tma[pos.idx], pol_keep);
-        }
-        __syncwarp();
-        if constexpr (kRouted) {
+        // Weights that one block reads pass through L2 once.
+        const uint64_t pol = w.once ? pol_once : pol_reuse;
+        const uint32_t box = kGather ? (uint32_t)w.nmma : (uint32_t)(w.nmma + 31) / 32 * 32;
+        int4 rows[kGather ? kN / 4 : 1];
+        if constexpr (kGather) {
 #pragma unroll
-          for (int q = 0; q < kGathers; ++q)
-            if ((lane + 32 * q) * 4 < w.nmma)
-              tma_gather4(stage + kStageA + (lane + 32 * q) * 4 * kRowBytes, &maps.b,
-                          kt * (int)kRowBytes, rows[q], &sh.full_tma[pos.idx], pol_keep);
-          __syncwarp();
+          for (int q = 0; q < kN / 4; ++q)
+            rows[q] = *reinterpret_cast<const int4*>(&sh.rows[pu.idx][4 * q]);
         }
-        pos.next(a.stages);
+        release_unit<false>(sh, pu);
+        if (w.e < 0) break;
+        for (int kt = w.kt0; kt < w.kt1; ++kt, ++issued) {
+          if (!mbar_wait(&sh.empty[pos.idx], pos.phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          unsigned char* stage = ring + (size_t)pos.idx * S::kStage;
+          uint64_t* bar = &sh.full[pos.idx];
+          const int x = kt * (int)kRowBytes;
+          mbar_arrive_expect_tx(bar, kStageA + box * kRowBytes);
+          tma_load_3d(stage, &maps.a, x, w.m0, w.e, bar, pol);
+          if constexpr (kGather) {
+#pragma unroll
+            for (int q = 0; q < kN / 4; ++q)
+              if (4 * q < w.nmma)
+                tma_gather4(stage + kStageA + q * 4 * kRowBytes, &maps.b, x, rows[q], bar,
+                            pol_keep);
+          } else {
+            for (int r = 0; r < (int)box; r += 32)
+              tma_load_2d(stage + kStageA + r * kRowBytes, &maps.b, x, w.tok0 + r, bar, pol_keep);
+          }
+          pos.next(a.stages);
+        }
       }
-    }
-    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
-    // Wait (bounded) until the copies this warp issued have landed: the last
-    // min(issued, stages) uses of the ring.
-    if (lane == 0) {
+      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+      // Wait (bounded) until the copies have landed: the last min(issued,
+      // stages) uses of the ring.
       for (int k = 0; k < min(issued, a.stages); ++k) {
         int idx = pos.idx - 1 - k;
         uint32_t ph = pos.phase;
         if (idx < 0) { idx += a.stages; ph ^= 1u; }
-        if (!mbar_wait(&sh.full_tma[idx], ph)) break;
+        if (!mbar_wait(&sh.full[idx], ph)) break;
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    RingPos pos;
-    int it = 0;
-    for (int idx = blockIdx.x; idx < num_units && ok; idx += gridDim.x) {
-      const Unit w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
-      if (w.ntok <= 0) continue;
-      const int buf = it & 1;
-      if (!mbar_wait_warp(&sh.d_empty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u)) { ok = false; break; }
-      tc_fence_after_sync();
-      const uint32_t d = tmem + buf * kN;
-      for (int kt = w.kt0; kt < w.kt1; ++kt) {
-        if (!mbar_wait_warp(&sh.full_sf[pos.idx], pos.phase) ||
-            !mbar_wait_warp(&sh.full_tma[pos.idx], pos.phase)) {
+    if (elect_one()) {
+      RingPos pos, pu;
+      Unit w;
+      for (int it = 0; ok; ++it) {
+        if (!pop_unit<false>(sh, pu, &w)) {
+          ok = false;
+          break;
+        }
+        release_unit<false>(sh, pu);
+        if (w.e < 0) break;
+        const int buf = it & 1;
+        if (!mbar_wait(&sh.d_empty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        if (elect_one()) {
+        const uint32_t d = tmem + buf * kN;
+        const uint32_t idesc0 = mma_idesc(w.nmma, 0), idesc2 = mma_idesc(w.nmma, 2);
+        for (int kt = w.kt0; kt < w.kt1; ++kt) {
+          if (!mbar_wait(&sh.full[pos.idx], pos.phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
           const uint32_t stage = ring_addr + pos.idx * S::kStage;
           const uint32_t sf = stage + kStageA + S::kStageB;
           const uint32_t tsfa = tmem + S::kSfCol + pos.idx * (S::kSfColsA + S::kSfColsB);
@@ -437,96 +612,44 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
           const int left = a.G * 32 - kt * kBK;
 #pragma unroll
           for (int j = 0; j < kBK / kMmaK; ++j) {
-            if (j * kMmaK < left) {
-              const int b = j / 2;
-              tc_mma_mxf4(d, da + j * 2, db + j * 2, mma_idesc(w.nmma, (j & 1) * 2), tsfa + 4 * b,
-                          tsfb + 4 * b * S::kBRowBlocks, kt > w.kt0 || j > 0 ? 1u : 0u);
-            }
+            if (j * kMmaK < left)
+              tc_mma_mxf4(d, da + j * 2, db + j * 2, (j & 1) ? idesc2 : idesc0,
+                          tsfa + 4 * (j / 2), tsfb + 4 * (j / 2) * S::kBRowBlocks,
+                          kt > w.kt0 || j > 0 ? 1u : 0u);
           }
           tc_commit(&sh.empty[pos.idx]);
           if (kt == w.kt1 - 1) tc_commit(&sh.d_full[buf]);
+          pos.next(a.stages);
         }
-        __syncwarp();
-        pos.next(a.stages);
       }
-      ++it;
+      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+      tc_commit(&sh.drain);
+      mbar_wait(&sh.drain, 0);
     }
-    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
-    // Any lane may have been the elected one.
-    tc_commit(&sh.drain);
-    mbar_wait(&sh.drain, 0);
     __syncwarp();
   } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + kScaleWarps) {
     // ---------------------------------------------------------- scale bytes
-    constexpr int kRows = 1 + S::kBRowBlocks;     // rows of this thread: a weight, 1 or 2 tokens
-    const int m = (warp - kScaleWarp0) * 32 + lane;
-    RingPos pos;
-    for (int idx = blockIdx.x; idx < num_units && ok; idx += gridDim.x) {
-      const Unit w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
-      if (w.ntok <= 0) continue;
-      const uint8_t* p[kRows];
-      const uint8_t* end[kRows];
-      p[0] = a.w_scales + ((size_t)w.e * a.O + min(w.m0 + m, a.O - 1)) * a.G;
-#pragma unroll
-      for (int r = 1; r < kRows; ++r) {
-        const int n = w.tok0 + min(m + 128 * (r - 1), w.ntok - 1);
-        const int t = kRouted ? a.plan.pair_list[n] / a.K : n;
-        p[r] = a.x_scales + (size_t)t * a.G;
-      }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        end[r] = p[r] + a.G;
-        p[r] += w.kt0 * kGroupsPerStage;
-      }
-      uint32_t cur[kRows][8], nxt[kRows][8];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) load_scales(p[r], end[r], cur[r]);
-      for (int kt = w.kt0; kt < w.kt1 && ok; kt += kChunkStages) {
-        if (kt + kChunkStages < w.kt1) {
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            p[r] += kChunkStages * kGroupsPerStage;
-            load_scales(p[r], end[r], nxt[r]);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kChunkStages; ++j) {
-          if (kt + j >= w.kt1) break;
-          if (!mbar_wait_warp(&sh.empty[pos.idx], pos.phase ^ 1u)) {
-            ok = false;
-            break;
-          }
-          unsigned char* sf = ring + (size_t)pos.idx * S::kStage + kStageA + S::kStageB +
-                              (m & 31) * 16 + (m >> 5) * 4;
-#pragma unroll
-          for (int b = 0; b < kSfPerStage; ++b) {
-            *reinterpret_cast<uint32_t*>(sf + b * kSfBlock) = cur[0][kSfPerStage * j + b];
-#pragma unroll
-            for (int r = 1; r < kRows; ++r)
-              *reinterpret_cast<uint32_t*>(sf + S::kSfA +
-                                           (b * S::kBRowBlocks + r - 1) * kSfBlock) =
-                  cur[r][kSfPerStage * j + b];
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full_sf[pos.idx]);
-          pos.next(a.stages);
-        }
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) cur[r][i] = nxt[r][i];
-      }
-    }
+    const int team = (warp - kScaleWarp0) / 2;
+    constexpr uint32_t kBlocks = kStageA + S::kStageB;
+    if ((warp - kScaleWarp0) % 2 == 0)
+      ok = scale_role<4, 1, false, kGather, S::kStage>(a, sh, ring, kBlocks, team, lane);
+    else
+      ok = scale_role<kN / 32, S::kBRowBlocks, true, kGather, S::kStage>(
+          a, sh, ring, kBlocks + S::kSfA, team, lane);
     if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------- epilogue
     const int quarter = warp - kEpiWarp0;
     Out* out = static_cast<Out*>(a.out);
-    int it = 0;
-    for (int idx = blockIdx.x; idx < num_units; idx += gridDim.x) {
-      const Unit w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
-      if (w.ntok <= 0) continue;
+    RingPos pu;
+    Unit w;
+    for (int it = 0;; ++it) {
+      if (!pop_unit<true>(sh, pu, &w)) {
+        ok = false;
+        break;
+      }
+      release_unit<true>(sh, pu);
+      if (w.e < 0) break;
       const int buf = it & 1;
       if (!mbar_wait_warp(&sh.d_full[buf], (uint32_t)(it >> 1) & 1u)) { ok = false; break; }
       tc_fence_after_sync();
@@ -550,7 +673,6 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
             store_out(out + ((int64_t)r * a.splits + w.split) * a.O + o, v[c]);
         }
       }
-      ++it;
     }
     if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   }
@@ -558,6 +680,27 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+// The token rows of a wide routed call in the lists' order, scale rows on
+// 16-byte boundaries; one warp per row.
+__global__ void __launch_bounds__(256)
+group_rows_kernel(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales,
+                  RoutePlan plan, int G, int K, int pitch, int64_t max_rows,
+                  uint8_t* __restrict__ packed_out, uint8_t* __restrict__ scales_out) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = min((int64_t)plan.meta[kMetaNumPairs], max_rows);
+  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows;
+       r += (int64_t)gridDim.x * 8) {
+    const int64_t t = plan.pair_list[r] / K;
+    const uint4* src = reinterpret_cast<const uint4*>(packed) + t * G;
+    uint4* dst = reinterpret_cast<uint4*>(packed_out) + r * G;
+    for (int i = lane; i < G; i += 32) dst[i] = src[i];
+    for (int i = lane; i < pitch; i += 32)
+      scales_out[r * pitch + i] = i < G ? scales[t * G + i] : (uint8_t)0;
+  }
 }
 
 // Joins the splits of a dense product: out[t, o] = sum_s part[t][s][o], s in order.
@@ -593,7 +736,7 @@ int num_sms() {
 
 template <int kN>
 size_t smem_bytes(int stages, int max_active) {
-  return 1024 + (size_t)stages * Shape<kN>::kStage + sizeof(MxShared) +
+  return 1024 + (size_t)stages * Shape<kN>::kStage + sizeof(MxShared<kMxNarrow>) +
          ((size_t)max_active + 1) * sizeof(int);
 }
 
@@ -608,7 +751,7 @@ template <int kN, typename Out, bool kRouted>
 cudaError_t launch_typed(const MxMaps& maps, MxKernelArgs args, int64_t units,
                          cudaStream_t stream) {
   args.stages = stages_for<kN>(args.max_active);
-  if (args.stages < 2) return cudaErrorInvalidValue;
+  if (args.stages < kMinStages) return cudaErrorInvalidValue;
   const size_t smem = smem_bytes<kN>(args.stages, args.max_active);
   static std::mutex mu;
   static size_t opted[64] = {};
@@ -642,21 +785,58 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
 
 }  // namespace
 
-// Wide blocks where experts (or the dense call) average more tokens than a
-// narrow block holds; a batch of up to 32 tokens has no wider block.
-bool gemm_mx_wide(int64_t T, int64_t blocks_of, int64_t K) {
-  return T > 32 && T * K > 16 * blocks_of;
+namespace {
+
+// The shape of a call's units.
+struct Plan {
+  bool wide;            // blocks of up to kMxWide tokens, else kMxNarrow
+  int splits;
+  int64_t blocks;       // dense: blocks of tokens; routed: at most this many
+};
+Plan plan_of(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
+  Plan p;
+  const int64_t active = routed ? std::min(E, T * K) : 1;
+  // Wide blocks where experts (or the dense call) average more tokens than
+  // half a narrow block holds; a batch of up to 32 tokens has no wider block.
+  p.wide = T > kMxNarrow && T * K > 16 * active;
+  const int64_t n = p.wide ? kMxWide : kMxNarrow;
+  const int64_t mtiles = (O + kBM - 1) / kBM, nk = (I + kBK - 1) / kBK;
+  const int64_t few = routed ? active : (T + n - 1) / n;
+  p.splits = (int)std::max<int64_t>(
+      1, std::min(std::min<int64_t>(304 / (few * mtiles), nk / 2), (int64_t)8));
+  // Each expert's last block may be short.
+  p.blocks = routed ? active + T * K / n : few;
+  if (!routed) {
+    // As many blocks as fill whole rounds of the SMs best, by the width of a
+    // round's blocks (in 16 tokens, plus 2 for what a unit costs besides).
+    const int64_t sms = 152;
+    int64_t best = INT64_MAX;
+    for (int64_t b = few; b <= few + few / 4 + 1; ++b) {
+      const int64_t rounds = (b * mtiles * p.splits + sms - 1) / sms;
+      const int64_t cost = rounds * (((T + b - 1) / b + 15) / 16 + 2);
+      if (cost < best) {
+        best = cost;
+        p.blocks = b;
+      }
+    }
+    // Equal blocks of 16 may need fewer than that.
+    const int64_t size = ((T + p.blocks - 1) / p.blocks + 15) / 16 * 16;
+    p.blocks = (T + size - 1) / size;
+  }
+  return p;
 }
 
+int64_t scale_pitch(int64_t I) { return (I / 32 + 15) / 16 * 16; }
+
+}  // namespace
+
 int gemm_mx_splits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
-  const int64_t active = routed ? std::min(E, T * K) : 1;
-  const bool wide = gemm_mx_wide(T, active, routed ? K : 1);
-  const int64_t n = wide ? 192 : 32;
-  const int64_t blocks = routed ? active : (T + n - 1) / n;
-  const int64_t tiles = blocks * ((O + kBM - 1) / kBM);
-  const int64_t nk = (I + kBK - 1) / kBK;
-  return (int)std::max<int64_t>(1, std::min(std::min<int64_t>(304 / tiles, nk / 2),
-                                            (int64_t)8));
+  return plan_of(T, E, I, O, K, routed).splits;
+}
+
+size_t gemm_mx_grouped_bytes(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
+  if (!plan_of(T, E, I, O, K, true).wide) return 0;
+  return (size_t)T * K * (size_t)(I / 2 + scale_pitch(I));
 }
 
 bool gemm_mx_supported(int64_t T, int64_t E, int64_t K) {
@@ -664,6 +844,25 @@ bool gemm_mx_supported(int64_t T, int64_t E, int64_t K) {
 }
 
 cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
+  const bool routed = g.plan != nullptr;
+  const Plan plan = plan_of(g.T, g.E, g.I, g.O, g.K, routed);
+  const bool wide = plan.wide, grouped = routed && wide;
+  const int64_t G = g.I / 32, P = g.T * g.K;
+  const uint8_t *rows = g.x_packed, *scales = g.x_scales;
+  int64_t nrows = g.T, pitch = G;
+  if (grouped) {
+    nrows = P;
+    pitch = scale_pitch(g.I);
+    uint8_t* rows_out = static_cast<uint8_t*>(g.grouped);
+    uint8_t* scales_out = rows_out + (size_t)P * (size_t)(g.I / 2);
+    const unsigned blocks = (unsigned)std::min<int64_t>((P + 7) / 8, (int64_t)num_sms() * 8);
+    const cudaError_t err = launch_after_previous(
+        group_rows_kernel, dim3(blocks), dim3(256), 0, stream, g.x_packed, g.x_scales, *g.plan,
+        (int)G, (int)g.K, (int)pitch, P, rows_out, scales_out);
+    if (err != cudaSuccess) return err;
+    rows = rows_out;
+    scales = scales_out;
+  }
   MxMaps maps;
   std::memset(&maps, 0, sizeof(maps));
   const cuuint64_t row = (cuuint64_t)(g.I / 2);
@@ -673,45 +872,41 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
     const cuuint32_t box[3] = {kRowBytes, kBM, 1};
     if (!encode(&maps.a, g.w_packed, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const bool routed = g.plan != nullptr;
   {
-    const cuuint64_t dims[2] = {row, (cuuint64_t)g.T};
+    const cuuint64_t dims[2] = {row, (cuuint64_t)nrows};
     const cuuint64_t strides[1] = {row};
-    const cuuint32_t box[2] = {kRowBytes, routed ? 1u : 32u};
-    if (!encode(&maps.b, g.x_packed, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint32_t box[2] = {kRowBytes, routed && !grouped ? 1u : 32u};
+    if (!encode(&maps.b, rows, 2, dims, strides, box)) return cudaErrorInvalidValue;
   }
   MxKernelArgs a;
   std::memset(static_cast<void*>(&a), 0, sizeof(a));
   if (routed) a.plan = *g.plan;
   a.w_scales = g.w_scales;
-  a.x_scales = g.x_scales;
+  a.x_scales = scales;
+  a.x_pitch = (int)pitch;
   a.out = g.splits > 1 || routed ? static_cast<void*>(g.part) : g.out;
   a.status = device_status_words();
   if (a.status == nullptr) return cudaErrorUnknown;
   a.T = (int)g.T;
   a.O = (int)g.O;
-  a.G = (int)(g.I / 32);
+  a.G = (int)G;
   a.K = (int)g.K;
   a.mtiles = (int)((g.O + kBM - 1) / kBM);
   a.splits = g.splits;
-  const int64_t active = routed ? std::min(g.E, g.T * g.K) : 1;
-  a.max_active = routed ? (int)active : 0;
-  const bool wide = gemm_mx_wide(g.T, active, routed ? g.K : 1);
-  const int64_t n = wide ? 192 : 32;
-  // At most this many blocks: each expert's last one may be short.
-  const int64_t blocks = routed ? active + g.T * g.K / n : (g.T + n - 1) / n;
-  const int64_t units = blocks * a.mtiles * a.splits;
+  a.blocks = (int)plan.blocks;
+  a.max_active = routed ? (int)std::min(g.E, P) : 0;
+  const int64_t units = plan.blocks * a.mtiles * a.splits;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
   cudaError_t err;
   if (routed)
-    err = wide ? launch_typed<192, float, true>(maps, a, units, stream)
-               : launch_typed<32, float, true>(maps, a, units, stream);
+    err = wide ? launch_typed<kMxWide, float, true>(maps, a, units, stream)
+               : launch_typed<kMxNarrow, float, true>(maps, a, units, stream);
   else if (g.splits > 1 || g.out_dtype == kTokenF32)
-    err = wide ? launch_typed<192, float, false>(maps, a, units, stream)
-               : launch_typed<32, float, false>(maps, a, units, stream);
+    err = wide ? launch_typed<kMxWide, float, false>(maps, a, units, stream)
+               : launch_typed<kMxNarrow, float, false>(maps, a, units, stream);
   else
-    err = wide ? launch_typed<192, __nv_bfloat16, false>(maps, a, units, stream)
-               : launch_typed<32, __nv_bfloat16, false>(maps, a, units, stream);
+    err = wide ? launch_typed<kMxWide, __nv_bfloat16, false>(maps, a, units, stream)
+               : launch_typed<kMxNarrow, __nv_bfloat16, false>(maps, a, units, stream);
   if (err != cudaSuccess || routed || g.splits == 1) return err;
   const unsigned grid = (unsigned)std::min<int64_t>((g.T * g.O + 255) / 256, num_sms() * 8);
   if (g.out_dtype == kTokenF32)

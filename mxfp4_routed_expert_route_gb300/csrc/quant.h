@@ -39,11 +39,14 @@ struct MxGemm {
   const RoutePlan* plan;                // routing lists, or null: dense (E = 1)
   int64_t T, E, I, O, K;                // K: picks per token (routed)
   int splits;                           // gemm_mx_splits(): units that share K
+  void* grouped;                        // gemm_mx_grouped_bytes() of scratch (routed)
   float* part;                          // [pair or token][split][O] (routed, or splits > 1)
   void* out;                            // dense: [T][O] of out_dtype
   int out_dtype;
 };
 int gemm_mx_splits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed);
+// The token rows in the lists' order (0: the kernel gathers them itself).
+size_t gemm_mx_grouped_bytes(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K);
 bool gemm_mx_supported(int64_t T, int64_t E, int64_t K);
 cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream);
 

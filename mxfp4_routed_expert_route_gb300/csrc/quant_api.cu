@@ -44,7 +44,7 @@ bool product_fits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
 // The units of a call (gemm_mx.cu numbers them in 31 bits).
 bool units_fit(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
   const int64_t active = routed ? (E < T * K ? E : T * K) : 1;
-  const int64_t blocks = active + T * K / 32 + 1;
+  const int64_t blocks = active + T * K / 16 + 2;
   const int64_t per = (O + 127) / 128 * gemm_mx_splits(T, E, I, O, K, routed);
   return blocks <= kMaxDim / per;
 }
@@ -55,6 +55,7 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 struct ExpertWorkspace {
   RoutePlan plan;
   int* wc_global;
+  void* grouped;
   float* part;
   int splits;
   size_t bytes;
@@ -78,6 +79,8 @@ ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t I, int64_t O, in
   const size_t wc = route_global_counter_words(T, K, E, false);
   ws.wc_global = wc ? static_cast<int*>(take(wc * sizeof(int))) : nullptr;
   ws.splits = K > 0 && E > 0 ? gemm_mx_splits(T, E, I, O, K, true) : 1;
+  const size_t grouped = K > 0 && E > 0 ? gemm_mx_grouped_bytes(T, E, I, O, K) : 0;
+  ws.grouped = grouped ? take(grouped) : nullptr;
   ws.part = static_cast<float*>(take(P * ws.splits * (size_t)O * sizeof(float)));
   ws.bytes = off;
   return ws;
@@ -290,6 +293,7 @@ extern "C" int mxfp4_expert_linear_quantized(
       g.O = O;
       g.K = K;
       g.splits = ws.splits;
+      g.grouped = ws.grouped;
       g.part = ws.part;
       if (launch_gemm_mx(g, stream) != cudaSuccess) return MXFP4EL_ERR_CUDA;
     }

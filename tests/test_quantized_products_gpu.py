@@ -43,6 +43,18 @@ def test_linear(T, I, O, dtype):
     assert lib.wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("T,I,O", [(1500, 7168, 4000), (20, 7168, 30000), (2000, 256, 20000),
+                                   (3000, 2880, 2000), (31, 512, 90000)])
+def test_linear_many_units_per_sm(T, I, O):
+    """Long and short sums, more tiles than the GPU holds at once: every ring of
+    the kernel goes round many times."""
+    x, w = rows(T, I, seed=T), rows(O, I, seed=O + 1)
+    got = lib.mxfp4_linear(*x, *w, dtype=F32)
+    vx, vw = ref.values(*x), ref.values(*w)
+    check(got, vx @ vw.T, ref.product_bound(vx, vw, I, F32), F32)
+    assert lib.wait_timeouts() == 0
+
+
 def test_linear_of_whole_numbers_is_exact():
     """Sums of quarters under 2^20 fit float32, so every bit has to be right;
     each scale byte is its own, so a wrong one shows."""
@@ -149,7 +161,8 @@ def check_routed(got, x, w, sel, p, ys, I, dtype):
 @pytest.mark.parametrize("T,E,K,I,O", [
     (1, 1, 1, 32, 1), (1, 8, 2, 256, 128), (8, 128, 4, 2880, 576), (16, 40, 8, 7168, 300),
     (33, 6, 2, 1056, 257), (300, 6, 2, 288, 130), (64, 2, 1, 512, 128), (700, 5, 3, 96, 65),
-    (2000, 3, 2, 64, 40), (9000, 16, 1, 64, 8), (40, 600, 3, 64, 33), (5, 3, 3, 160, 1001)])
+    (2000, 3, 2, 64, 40), (9000, 16, 1, 64, 8), (40, 600, 3, 64, 33), (5, 3, 3, 160, 1001),
+    (3000, 24, 2, 2880, 700), (48, 100, 4, 1536, 1500)])
 def test_experts(T, E, K, I, O, dtype):
     x, w, sel, p, ys = make_routed(T, E, K, I, O, dtype, seed=T)
     got = lib.mxfp4_expert_linear_quantized(*x, *w, sel, p, ys)
