@@ -26,14 +26,15 @@
 // bytes of 128 rows' scales for four groups (512 bytes, row r at 16 (r % 32) +
 // 4 (r / 32)); tcgen05.cp brings such a block from shared memory and repeats it
 // for the four lane quarters. In memory they are rows of I/32 bytes on no
-// particular alignment, so four warps read them with ordinary loads and store
-// the blocks: two teams, which take two stages at a time in turn (16 bytes of a
-// row), one warp of each for the weights' rows and one for the tokens', lane l
-// the rows l, l + 32, ..., whose four words lie together in the block. While one
-// team's loads and its fence between these stores and the tensor core are
-// under way, the other has the next two stages. (A team's next stages are four
-// on, and the ring has at least as many: a team further ahead than the ring is
-// long could not tell a stage's phases apart.)
+// particular alignment, so a few warps read them with ordinary loads and store
+// the blocks, lane l the rows l, l + 32, ..., whose words lie together in the
+// block. A warp takes four stages at a time (32 bytes of a row) and has the next
+// four's loads under way while it stores these: with two stages at a time the
+// loads' latency bounded the product (decode: 65 us against 55 without the
+// loads). Narrow blocks have two teams of warps that take four stages in turn.
+// From a team's last stage to its next it is then five, and the ring has more
+// (from one further on than the ring is long a warp could not tell a stage's
+// phases apart, and would store into one still in use).
 //
 // K that is no multiple of 256: the copies fill codes past a row's end with
 // zeros, and scale bytes past it are set to 0, so what is added is exactly 0;
@@ -41,14 +42,20 @@
 //
 // Warp roles in a CTA of 12 warps (one CTA per SM, persistent over units
 // (block, 128-row tile, K split)):
-//   warp 0      copies of codes (weights and tokens), one thread; TMEM
-//   warp 1      scale copies to tensor memory and MMAs, one thread
+//   warp 0      copies of codes (weights and tokens), one elected lane; TMEM
+//   warp 1      scale copies to tensor memory and MMAs, one elected lane
 //   warp 2      prefix of the experts' blocks at start (routed)
 //   warp 3      the units: finds each next one and hands it to the other roles
 //               through a ring in shared memory, ahead of them (finding one
 //               takes several dependent loads)
 //   warps 4-7   scale bytes
 //   warps 8-11  epilogue: tensor memory -> float32 or bf16 results
+// Wide blocks: two CTAs, on neighbouring SMs, take two tiles of one block at a
+// time, and each loads half of the token rows of every stage for both
+// (multicast). Alone, an SM reads 40 KB of codes per stage from L2, which
+// then bounds the dense product (15 TB/s; 111 us against 9x for 8192 x 7168 x
+// 4096). A stage's slot is free when the MMAs of both CTAs are done with it.
+//
 // Two accumulators, so the epilogue of a unit runs beside the next unit's
 // MMAs. Every wait is bounded; a role whose wait gives up records it and
 // stops, and the CTA waits (bounded) for its own copies and MMAs before
@@ -66,7 +73,7 @@
 namespace mxfp4el {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 448;
 constexpr int kBM = 128;                       // weight rows per tile
 constexpr int kBK = 256;                       // K values per stage
 constexpr int kMmaK = 64;                      // K values per MMA
@@ -78,12 +85,8 @@ constexpr int kSfPerStage = kGroupsPerStage / 4;
 constexpr int kMaxStages = 12;
 constexpr int kMxNarrow = 32, kMxWide = 192;   // tokens of a block, at most
 constexpr uint32_t kTmemCols = 512;
-constexpr int kUnitWarp = 3, kScaleWarp0 = 4, kScaleWarps = 4, kEpiWarp0 = 8, kEpiWarps = 4;
-constexpr int kScaleTeams = 2;
+constexpr int kUnitWarp = 3, kScaleWarp0 = 8, kEpiWarp0 = 4, kEpiWarps = 4;
 constexpr int kUnitRing = 8;
-constexpr int kUnitReaders = 2 + kScaleWarps + kEpiWarps;
-constexpr int kPairStages = 2;                 // stages whose scales one read brings (16 bytes)
-constexpr int kMinStages = kPairStages * kScaleTeams;
 constexpr size_t kSmemLimit = 227 * 1024;
 
 template <int kN>
@@ -97,12 +100,23 @@ struct Shape {
   static constexpr uint32_t kSfColsA = kSfPerStage * 4, kSfColsB = kSfPerStage * kBRowBlocks * 4;
   static constexpr uint32_t kSfCol = 2 * kN;
   static constexpr int kTmemStages = (int)((kTmemCols - kSfCol) / (kSfColsA + kSfColsB));
+  // Scale warps: narrow blocks two teams of a weights' and a tokens' warp, wide
+  // ones a team of one warp for the weights and two for the tokens (128, 64 rows).
+  static constexpr int kCluster = kN == kMxWide ? 2 : 1;
+  static constexpr int kTeams = 2;
+  static constexpr int kChunk = 2;                         // stages whose scales one read brings
+  static constexpr int kTeamWarps = kN == kMxNarrow ? 2 : 3;
+  static constexpr int kUnitReaders = 2 + kTeams * kTeamWarps + kEpiWarps;
+  static constexpr int kMinStages = (kTeams - 1) * kChunk + 2;
+  static_assert(kN == kMxNarrow || kN == kMxWide, "a narrow and a wide form");
   static_assert(kStage % 1024 == 0 && kStageB % 1024 == 0, "stages keep 1024-byte alignment");
 };
 
 struct MxMaps {
   CUtensorMap a;      // weights' codes [E][O][I/2], box {128, 128, 1}, 128-byte swizzle
-  CUtensorMap b;      // tokens' codes [rows][I/2], box {128, 32}, or {128, 1} (gathered)
+  CUtensorMap b[kMxWide / 32];   // tokens' codes [rows][I/2], boxes {128, 16 (i + 1)} (half
+                                 // a block) when wide; else the first alone, {128, 32}, or
+                                 // {128, 1} (gathered)
 };
 
 struct MxKernelArgs {
@@ -149,6 +163,36 @@ __device__ __forceinline__ bool elect_one() {
       "}"
       : "=r"(e));
   return e != 0;
+}
+
+// A 2-D tiled load into the same place of every CTA of the cluster in `mask`; each
+// CTA's own barrier (at the same place too) gets the bytes.
+__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const void* tmap, int x, int y,
+                                                      uint64_t* bar, uint16_t mask,
+                                                      uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(
+          smem_addr(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(mask), "l"(policy)
+      : "memory");
+}
+// tc_commit on the barrier at this place in every CTA of the cluster in `mask`.
+__device__ __forceinline__ void tc_commit_multicast(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(mask)
+      : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
 }
 
 // Four rows of 128 bytes by their row indices, one after another at dst.
@@ -217,9 +261,11 @@ struct RingPos {
 
 template <int kN, bool kRouted>
 __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix, int num_active,
-                                        int idx) {
+                                        int idx, int rank) {
+  constexpr int kPair = Shape<kN>::kCluster;   // tiles of a unit, one per CTA of the cluster
   Unit w;
-  const int per_block = a.mtiles * a.splits;
+  const int mtiles = (a.mtiles + kPair - 1) / kPair;
+  const int per_block = mtiles * a.splits;
   int first = 0, nblk, cnt, local;
   if constexpr (kRouted) {
     const int blk = idx / per_block;
@@ -247,8 +293,8 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix
   w.tok0 = first + j * bsz;
   w.ntok = max(0, min(bsz, cnt - j * bsz));
   w.nmma = (w.ntok + 15) / 16 * 16;
-  w.split = rest / a.mtiles;
-  w.m0 = (rest - w.split * a.mtiles) * kBM;
+  w.split = rest / mtiles;
+  w.m0 = ((rest - w.split * mtiles) * kPair + rank) * kBM;     // may be past the last row
   const int nk = (a.G + kGroupsPerStage - 1) / kGroupsPerStage;
   w.kt0 = (int)((int64_t)w.split * nk / a.splits);
   w.kt1 = (int)((int64_t)(w.split + 1) * nk / a.splits);
@@ -256,156 +302,202 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix
   return w;
 }
 
-// 16 bytes from p as four words; bytes at `end` and past it are 0. Reads
-// only aligned words that hold a byte before `end`.
-__device__ __forceinline__ uint4 load_scales(const uint8_t* p, const uint8_t* end) {
-  const int64_t left = end - p;
-  if ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && left >= 16)
-    return *reinterpret_cast<const uint4*>(p);
-  const uint32_t sh = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 3) * 8;
-  const uint8_t* at = p - sh / 8;
-  uint32_t v[5], w[4];
+// The scales of kChunk stages from any address: aligned words and one more while
+// they are on their way (load), then the words themselves (settle). Reads only
+// aligned words that hold one of the row's bytes, `left` from p on; bytes past
+// them are 0. wide: p is 16-byte aligned, as the row's end is.
+template <int kChunk>
+struct RawScales {
+  static constexpr int kWords = 2 * kChunk;
+  uint32_t v[kWords + 1];
+  uint32_t shift;
+  __device__ __forceinline__ void load(const uint8_t* p, int left, bool wide) {
+    if (wide) {
 #pragma unroll
-  for (int i = 0; i < 5; ++i)
-    v[i] = at + 4 * i < end ? *reinterpret_cast<const uint32_t*>(at + 4 * i) : 0u;
+      for (int i = 0; i < kWords; i += 4) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (i == 0 || left > 4 * i) u = *reinterpret_cast<const uint4*>(p + 4 * i);
+        v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
+      }
+    } else {
+      const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+      const uint32_t* at = reinterpret_cast<const uint32_t*>(p - skip);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = __funnelshift_r(v[i], v[i + 1], sh);
-    const int64_t n = left - 4 * i;
-    if (n < 4) w[i] = n > 0 ? w[i] & ((1u << (8 * (int)n)) - 1u) : 0u;
+      for (int i = 0; i <= kWords; ++i) v[i] = 4 * i < left + skip ? at[i] : 0u;
+      shift = 8u * (uint32_t)skip;
+    }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ void settle(int left) {     // not after a wide load
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], shift);
+    if (left < 4 * kWords) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const int n = left - 4 * i;
+        if (n < 4) v[i] = n > 0 ? v[i] & ((1u << (8 * n)) - 1u) : 0u;
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The next unit of this role, by a whole warp or (kWarp = false) one thread.
-template <bool kWarp, int kRows>
+// A warp's wait. The first test alone is inline: a stage of the copies and
+// MMAs is a few hundred cycles, of which loops and clock reads took a third.
+__device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFullMask, mbar_wait_suspend(bar, parity)) != 0;
+}
+__device__ __forceinline__ bool wait_short(uint64_t* bar, uint32_t parity) {
+  if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+  return wait_longer(bar, parity);
+}
+
+// The next unit of this role; its fields are the same in every lane, and known
+// to be (values that feed the copies and tcgen05 otherwise have to be made
+// uniform at every issue).
+template <int kRows>
 __device__ __forceinline__ bool pop_unit(MxShared<kRows>& sh, RingPos& pu, Unit* w) {
-  const bool got = kWarp ? mbar_wait_warp(&sh.u_full[pu.idx], pu.phase)
-                         : mbar_wait(&sh.u_full[pu.idx], pu.phase);
-  if (!got) return false;
-  *w = sh.units[pu.idx];
+  if (!wait_short(&sh.u_full[pu.idx], pu.phase)) return false;
+  const Unit u = sh.units[pu.idx];
+  w->e = __shfl_sync(kFullMask, u.e, 0);
+  w->m0 = __shfl_sync(kFullMask, u.m0, 0);
+  w->tok0 = __shfl_sync(kFullMask, u.tok0, 0);
+  w->ntok = __shfl_sync(kFullMask, u.ntok, 0);
+  w->nmma = __shfl_sync(kFullMask, u.nmma, 0);
+  w->split = __shfl_sync(kFullMask, u.split, 0);
+  w->kt0 = __shfl_sync(kFullMask, u.kt0, 0);
+  w->kt1 = __shfl_sync(kFullMask, u.kt1, 0);
+  w->once = __shfl_sync(kFullMask, u.once, 0);
   return true;
 }
-template <bool kWarp, int kRows>
+template <int kRows>
 __device__ __forceinline__ void release_unit(MxShared<kRows>& sh, RingPos& pu) {
-  if (kWarp) __syncwarp();
-  if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.u_empty[pu.idx]);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.u_empty[pu.idx]);
   pu.next(kUnitRing);
 }
 
-// Stages two at a time, in the order of the units, dealt to the scale teams in
-// turn: next() moves to this team's next two. kRows: rows per lane.
-template <int kRows, bool kTokens, bool kGather>
+// Stages four at a time, in the order of the units, dealt to kTeams teams in
+// turn: next() moves to this team's next ones. Lane l has the rows row0 + l + 32 i
+// of the tile (kTokens: of the block), i < kRows.
+template <int kRows, int kTeams, int kChunk, bool kTokens, bool kGather>
 struct ScaleWalk {
   Unit w;
-  int kt;                 // first of the two stages
+  int kt;                 // first of the stages
   int slot;               // its place in the ring of stages
   uint32_t phase;
   int turn;               // whose turn it is
+  bool wide;              // every row on 16-byte boundaries
   const uint8_t* base[kRows];
   RingPos pu;
 
   __device__ __forceinline__ void start() {
     w.e = 0;
-    w.kt1 = kt = -kPairStages;                 // nothing yet: the first step loads a unit
+    w.kt1 = kt = -kChunk;                      // nothing yet: the first step loads a unit
     slot = 0;
     phase = 0;
-    turn = kScaleTeams - 1;
+    turn = kTeams - 1;
   }
   template <typename Sh>
-  __device__ __forceinline__ bool load_unit(const MxKernelArgs& a, Sh& sh, int lane) {
-    if (!pop_unit<true>(sh, pu, &w)) {
+  __device__ __forceinline__ bool load_unit(const MxKernelArgs& a, Sh& sh, int row0, int lane) {
+    if (!pop_unit(sh, pu, &w)) {
       w.e = -2;
       return false;
     }
     if (w.e >= 0) {
+      const uint8_t* from = kTokens ? a.x_scales : a.w_scales;
+      const int pitch = kTokens ? a.x_pitch : a.G;
+      wide = (reinterpret_cast<uintptr_t>(from) | (uintptr_t)pitch | (uintptr_t)(8 * w.kt0)) % 16 == 0 &&
+             a.G % 16 == 0;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         if constexpr (kTokens) {
-          const int n = min(lane + 32 * i, w.ntok - 1);
+          const int n = min(row0 + lane + 32 * i, w.ntok - 1);
           const int t = kGather ? sh.rows[pu.idx][n] : w.tok0 + n;
-          base[i] = a.x_scales + (size_t)t * a.x_pitch;
+          base[i] = from + (size_t)t * pitch;
         } else {
-          base[i] = a.w_scales + ((size_t)w.e * a.O + min(w.m0 + lane + 32 * i, a.O - 1)) * a.G;
+          base[i] = from + ((size_t)w.e * a.O + min(w.m0 + lane + 32 * i, a.O - 1)) * pitch;
         }
       }
     }
-    release_unit<true>(sh, pu);
+    release_unit(sh, pu);
     return true;
   }
   // False at the end of the units (or after a wait that gave up: w.e == -2).
   template <typename Sh>
-  __device__ __forceinline__ bool next(const MxKernelArgs& a, Sh& sh, int team, int lane) {
+  __device__ __forceinline__ bool next(const MxKernelArgs& a, Sh& sh, int team, int row0,
+                                       int lane) {
     for (;;) {
-      slot += min(kPairStages, w.kt1 - kt);
-      if (slot >= a.stages) {
+      slot += min(kChunk, w.kt1 - kt);
+      while (slot >= a.stages) {
         slot -= a.stages;
         phase ^= 1u;
       }
-      kt += kPairStages;
+      kt += kChunk;
       while (kt >= w.kt1) {
-        if (!load_unit(a, sh, lane) || w.e < 0) return false;
+        if (!load_unit(a, sh, row0, lane) || w.e < 0) return false;
         kt = w.kt0;
       }
-      turn = turn + 1 == kScaleTeams ? 0 : turn + 1;
+      turn = turn + 1 == kTeams ? 0 : turn + 1;
       if (turn == team) return true;
     }
   }
 };
 
-// A scale warp's whole work. block0: the offset of its first block in a stage;
-// kBlockRows: 128-row blocks of its operand. False after a wait that gave up.
-template <int kRows, int kBlockRows, bool kTokens, bool kGather, uint32_t kStageBytes, typename Sh>
+// A scale warp's whole work. block0: the offset of its first block in a stage,
+// kStride that of the next four groups' block. False after a wait that gave up.
+template <int kRows, int kTeams, int kChunk, bool kTokens, bool kGather, uint32_t kStageBytes,
+          uint32_t kStride, typename Sh>
 __device__ __forceinline__ bool scale_role(const MxKernelArgs& a, Sh& sh, unsigned char* ring,
-                                           uint32_t block0, int team, int lane) {
-  static_assert(kRows == 4 || kRows == 1 || kRows == 6, "a tile, a narrow and a wide block");
-  ScaleWalk<kRows, kTokens, kGather> walk;
+                                           uint32_t block0, int team, int row0, int lane) {
+  ScaleWalk<kRows, kTeams, kChunk, kTokens, kGather> walk;
   walk.start();
-  uint4 cur[kRows], nxt[kRows];
-  auto fetch = [&](uint4 (&v)[kRows]) {
+  RawScales<kChunk> cur[kRows], nxt[kRows];
+  auto fetch = [&](RawScales<kChunk> (&v)[kRows]) {
+    const int at = walk.kt * kGroupsPerStage;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      v[i] = load_scales(walk.base[i] + walk.kt * kGroupsPerStage, walk.base[i] + a.G);
+    for (int i = 0; i < kRows; ++i) v[i].load(walk.base[i] + at, a.G - at, walk.wide);
   };
-  bool more = walk.next(a, sh, team, lane);
+  bool more = walk.next(a, sh, team, row0, lane);
   if (more) fetch(cur);
   while (more) {
-    // These two stages, while the next two of this warp are on their way.
     int slot = walk.slot;
     uint32_t phase = walk.phase;
-    const int n = min(kPairStages, walk.w.kt1 - walk.kt);
-    more = walk.next(a, sh, team, lane);
+    const int n = min(kChunk, walk.w.kt1 - walk.kt);
+    const int left = a.G - walk.kt * kGroupsPerStage;
+    const bool settled = walk.wide;
+    more = walk.next(a, sh, team, row0, lane);
     if (more) fetch(nxt);
+    if (!settled) {
 #pragma unroll
-    for (int j = 0; j < kPairStages; ++j) {
+      for (int i = 0; i < kRows; ++i) cur[i].settle(left);
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
       if (j >= n) break;
-      if (j > 0 && ++slot == a.stages) {
+      if (!wait_short(&sh.empty[slot], phase ^ 1u)) return false;
+      unsigned char* sf = ring + (size_t)slot * kStageBytes + block0 + lane * 16;
+#pragma unroll
+      for (int b = 0; b < kSfPerStage; ++b) {
+        uint32_t w[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) w[i] = cur[i].v[kSfPerStage * j + b];
+        unsigned char* at = sf + b * kStride;
+        if constexpr (kRows == 4)
+          *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kRows == 2)
+          *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(at) = w[0];
+      }
+      // The MMA warp has the fence between these stores and the tensor core.
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[slot]);
+      if (++slot == a.stages) {
         slot = 0;
         phase ^= 1u;
       }
-      if (!mbar_wait_warp(&sh.empty[slot], phase ^ 1u)) return false;
-      unsigned char* sf = ring + (size_t)slot * kStageBytes + block0 + lane * 16;
-      auto word = [&](int i, int b) {              // row lane + 32 i, groups 4 b..
-        const uint4& v = cur[i];
-        return j == 0 ? (b == 0 ? v.x : v.y) : (b == 0 ? v.z : v.w);
-      };
-#pragma unroll
-      for (int b = 0; b < kSfPerStage; ++b) {
-        unsigned char* at = sf + b * kBlockRows * kSfBlock;
-        if constexpr (kRows == 1)
-          *reinterpret_cast<uint32_t*>(at) = word(0, b);
-        else
-          *reinterpret_cast<uint4*>(at) =
-              make_uint4(word(0, b), word(1, b), word(2, b), word(3, b));
-        if constexpr (kRows == 6)
-          *reinterpret_cast<uint2*>(at + kSfBlock) = make_uint2(word(4, b), word(5, b));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[slot]);
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i) cur[i] = nxt[i];
@@ -428,18 +520,18 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&sh.full[s], 3);                       // the copies (bytes), two scale warps
-      mbar_init(&sh.empty[s], 1);
-    }
+      mbar_init(&sh.full[s], 1 + S::kTeamWarps);       // the copies (bytes), a team's warps
+      mbar_init(&sh.empty[s], S::kCluster);            // the MMAs of every CTA that the
+    }                                                  // copies of this one write to
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.d_full[b], 1);
       mbar_init(&sh.d_empty[b], kEpiWarps);
     }
     for (int r = 0; r < kUnitRing; ++r) {
       mbar_init(&sh.u_full[r], 1);
-      mbar_init(&sh.u_empty[r], kUnitReaders);
+      mbar_init(&sh.u_empty[r], S::kUnitReaders);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 32);                          // every lane of the MMA warp
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -447,7 +539,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     tmem_relinquish();
     if (lane == 0) {
       prefetch_tensor_map(&maps.a);
-      prefetch_tensor_map(&maps.b);
+      prefetch_tensor_map(&maps.b[0]);
     }
   }
   pdl_wait();                    // the operands and the routing lists are ready
@@ -474,16 +566,18 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       if (lane == 0) {
         prefix[na] = run;
         sh.num_active = na;
-        sh.num_units = run * a.mtiles * a.splits;
+        sh.num_units = run * ((a.mtiles + S::kCluster - 1) / S::kCluster) * a.splits;
       }
     } else if (lane == 0) {
       sh.num_active = 0;
-      sh.num_units = a.blocks * a.mtiles * a.splits;
+      sh.num_units = a.blocks * ((a.mtiles + S::kCluster - 1) / S::kCluster) * a.splits;
     }
   }
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (S::kCluster > 1) cluster_sync();       // the other's barriers are ready too
   tc_fence_after_sync();
+  const int rank = S::kCluster > 1 ? __shfl_sync(kFullMask, cluster_rank(), 0) : 0;
   const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem_base, 0);
   const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
   bool ok = true;
@@ -492,19 +586,28 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     // ------------------------------------------------------------ the units
     const int num_units = sh.num_units, num_active = sh.num_active;
     RingPos pu;
-    for (int idx = blockIdx.x;; idx += gridDim.x) {
+    for (int idx = blockIdx.x / S::kCluster;; idx += gridDim.x / S::kCluster) {
       Unit w;
       w.e = -1;
-      if (idx < num_units) w = unit_at<kN, kRouted>(a, prefix, num_active, idx);
+      if (idx < num_units) w = unit_at<kN, kRouted>(a, prefix, num_active, idx, rank);
       if (w.e >= 0 && w.ntok <= 0) continue;
       int t = 0;
       if (kGather && w.e >= 0)                  // past the block its last token
         t = a.plan.pair_list[w.tok0 + min(lane, w.ntok - 1)] / a.K;
-      if (!mbar_wait_warp(&sh.u_empty[pu.idx], pu.phase ^ 1u)) {
+      if (!wait_short(&sh.u_empty[pu.idx], pu.phase ^ 1u)) {
         ok = false;
         break;
       }
       if (kGather) sh.rows[pu.idx][lane] = t;
+      // The tile's scale bytes lie together: have them in L2 by the time the
+      // scale warps ask, which they do only a few stages ahead.
+      if (lane == 0 && w.e >= 0 && w.m0 < a.O) {
+        const uint8_t* from = a.w_scales + ((size_t)w.e * a.O + w.m0) * a.G;
+        const uintptr_t lo = (reinterpret_cast<uintptr_t>(from) + 15) & ~(uintptr_t)15;
+        const uintptr_t hi =
+            reinterpret_cast<uintptr_t>(from + (size_t)min(kBM, a.O - w.m0) * a.G) & ~(uintptr_t)15;
+        if (hi > lo) prefetch_l2(reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo));
+      }
       if (lane == 0) sh.units[pu.idx] = w;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.u_full[pu.idx]);
@@ -514,33 +617,37 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   } else if (warp == 0) {
     // ------------------------------------------------------ copies of codes
-    if (elect_one()) {
-      const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_evict_last_policy();
-      const uint64_t pol_reuse = l2_evict_normal_policy();
-      RingPos pos, pu;
-      int issued = 0;
-      Unit w;
-      while (ok) {
-        if (!pop_unit<false>(sh, pu, &w)) {
+    const uint64_t pol_once = l2_evict_first_policy(), pol_keep = l2_evict_last_policy();
+    const uint64_t pol_reuse = l2_evict_normal_policy();
+    RingPos pos, pu;
+    int issued = 0;
+    Unit w;
+    while (ok) {
+      if (!pop_unit(sh, pu, &w)) {
+        ok = false;
+        break;
+      }
+      // Weights that one block reads pass through L2 once.
+      const uint64_t pol = w.once ? pol_once : pol_reuse;
+      const int load = (w.nmma + 31) / 32 - 1;           // the token box: 32 (load + 1) rows
+      const uint32_t box = kGather ? (uint32_t)w.nmma : 32u * (uint32_t)(load + 1);
+      int4 rows[kGather ? kN / 4 : 1];
+      if constexpr (kGather) {
+        const int t = sh.rows[pu.idx][lane];
+#pragma unroll
+        for (int q = 0; q < kN / 4; ++q)
+          rows[q] = make_int4(__shfl_sync(kFullMask, t, 4 * q), __shfl_sync(kFullMask, t, 4 * q + 1),
+                              __shfl_sync(kFullMask, t, 4 * q + 2),
+                              __shfl_sync(kFullMask, t, 4 * q + 3));
+      }
+      release_unit(sh, pu);
+      if (w.e < 0) break;
+      for (int kt = w.kt0; kt < w.kt1; ++kt, ++issued) {
+        if (!wait_short(&sh.empty[pos.idx], pos.phase ^ 1u)) {
           ok = false;
           break;
         }
-        // Weights that one block reads pass through L2 once.
-        const uint64_t pol = w.once ? pol_once : pol_reuse;
-        const uint32_t box = kGather ? (uint32_t)w.nmma : (uint32_t)(w.nmma + 31) / 32 * 32;
-        int4 rows[kGather ? kN / 4 : 1];
-        if constexpr (kGather) {
-#pragma unroll
-          for (int q = 0; q < kN / 4; ++q)
-            rows[q] = *reinterpret_cast<const int4*>(&sh.rows[pu.idx][4 * q]);
-        }
-        release_unit<false>(sh, pu);
-        if (w.e < 0) break;
-        for (int kt = w.kt0; kt < w.kt1; ++kt, ++issued) {
-          if (!mbar_wait(&sh.empty[pos.idx], pos.phase ^ 1u)) {
-            ok = false;
-            break;
-          }
+        if (elect_one()) {
           unsigned char* stage = ring + (size_t)pos.idx * S::kStage;
           uint64_t* bar = &sh.full[pos.idx];
           const int x = kt * (int)kRowBytes;
@@ -550,108 +657,139 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
 #pragma unroll
             for (int q = 0; q < kN / 4; ++q)
               if (4 * q < w.nmma)
-                tma_gather4(stage + kStageA + q * 4 * kRowBytes, &maps.b, x, rows[q], bar,
+                tma_gather4(stage + kStageA + q * 4 * kRowBytes, &maps.b[0], x, rows[q], bar,
                             pol_keep);
           } else {
-            for (int r = 0; r < (int)box; r += 32)
-              tma_load_2d(stage + kStageA + r * kRowBytes, &maps.b, x, w.tok0 + r, bar, pol_keep);
+            // Each CTA of the pair loads half of the token rows for both.
+            static_assert(S::kCluster == 1 || S::kCluster == 2, "halves");
+            if constexpr (S::kCluster == 2) {
+              const int half = 16 * (load + 1);
+              tma_load_2d_multicast(stage + kStageA + rank * half * kRowBytes, &maps.b[load], x,
+                                    w.tok0 + rank * half, bar, (uint16_t)3, pol_keep);
+            } else {
+              tma_load_2d(stage + kStageA, &maps.b[load], x, w.tok0, bar, pol_keep);
+            }
           }
-          pos.next(a.stages);
         }
-      }
-      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
-      // Wait (bounded) until the copies have landed: the last min(issued,
-      // stages) uses of the ring.
-      for (int k = 0; k < min(issued, a.stages); ++k) {
-        int idx = pos.idx - 1 - k;
-        uint32_t ph = pos.phase;
-        if (idx < 0) { idx += a.stages; ph ^= 1u; }
-        if (!mbar_wait(&sh.full[idx], ph)) break;
+        __syncwarp();
+        pos.next(a.stages);
       }
     }
-    __syncwarp();
+    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+    // Wait (bounded) until the copies have landed: the last min(issued,
+    // stages) uses of the ring.
+    for (int k = 0; k < min(issued, a.stages); ++k) {
+      int idx = pos.idx - 1 - k;
+      uint32_t ph = pos.phase;
+      if (idx < 0) { idx += a.stages; ph ^= 1u; }
+      if (!wait_short(&sh.full[idx], ph)) break;
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA
-    if (elect_one()) {
-      RingPos pos, pu;
-      Unit w;
-      for (int it = 0; ok; ++it) {
-        if (!pop_unit<false>(sh, pu, &w)) {
-          ok = false;
-          break;
-        }
-        release_unit<false>(sh, pu);
-        if (w.e < 0) break;
-        const int buf = it & 1;
-        if (!mbar_wait(&sh.d_empty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u)) {
+    RingPos pos, pu;
+    Unit w;
+    const uint64_t da0 = smem_desc_sw128(ring_addr);
+    const uint64_t dsf0 = smem_desc_rows16(ring_addr + kStageA + S::kStageB);
+    for (int it = 0; ok; ++it) {
+      if (!pop_unit(sh, pu, &w)) {
+        ok = false;
+        break;
+      }
+      release_unit(sh, pu);
+      if (w.e < 0) break;
+      const int buf = it & 1;
+      if (!wait_short(&sh.d_empty[buf], ((uint32_t)(it >> 1) & 1u) ^ 1u)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t d = tmem + buf * kN;
+      const uint32_t idesc0 = mma_idesc(w.nmma, 0), idesc2 = mma_idesc(w.nmma, 2);
+      // MMAs of the last stage: K may end in it.
+      const int last = min(kBK / kMmaK, (a.G * 32 - (w.kt1 - 1) * kBK + kMmaK - 1) / kMmaK);
+      const bool second = S::kBRowBlocks > 1 && w.nmma > 128;   // token scales' second block
+      bool ready = mbar_try_wait(&sh.full[pos.idx], pos.phase);
+      for (int kt = w.kt0; kt < w.kt1; ++kt) {
+        if (!__all_sync(kFullMask, ready) && !wait_longer(&sh.full[pos.idx], pos.phase)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + buf * kN;
-        const uint32_t idesc0 = mma_idesc(w.nmma, 0), idesc2 = mma_idesc(w.nmma, 2);
-        for (int kt = w.kt0; kt < w.kt1; ++kt) {
-          if (!mbar_wait(&sh.full[pos.idx], pos.phase)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          const uint32_t stage = ring_addr + pos.idx * S::kStage;
-          const uint32_t sf = stage + kStageA + S::kStageB;
-          const uint32_t tsfa = tmem + S::kSfCol + pos.idx * (S::kSfColsA + S::kSfColsB);
+        const int idx = pos.idx;
+        pos.next(a.stages);
+        // The next stage's state is asked for before this one's MMAs are issued.
+        ready = kt + 1 < w.kt1 && mbar_try_wait(&sh.full[pos.idx], pos.phase);
+        if (elect_one()) {
+          fence_proxy_async_smem();              // the scale warps' stores
+          // Descriptors differ in the address alone (16-byte units in the low bits).
+          const uint32_t at = (uint32_t)idx * (S::kStage >> 4);
+          const uint64_t da = da0 + at, db = da + (kStageA >> 4), dsf = dsf0 + at;
+          const uint32_t tsfa = tmem + S::kSfCol + idx * (S::kSfColsA + S::kSfColsB);
           const uint32_t tsfb = tsfa + S::kSfColsA;
 #pragma unroll
           for (int b = 0; b < kSfPerStage; ++b) {
-            tc_copy_scales(tsfa + 4 * b, smem_desc_rows16(sf + b * kSfBlock));
+            tc_copy_scales(tsfa + 4 * b, dsf + b * (kSfBlock >> 4));
 #pragma unroll
             for (int r = 0; r < S::kBRowBlocks; ++r)
-              tc_copy_scales(tsfb + 4 * (b * S::kBRowBlocks + r),
-                             smem_desc_rows16(sf + S::kSfA + (b * S::kBRowBlocks + r) * kSfBlock));
+              if (r == 0 || second) tc_copy_scales(tsfb + 4 * (b * S::kBRowBlocks + r),
+                             dsf + ((S::kSfA + (b * S::kBRowBlocks + r) * kSfBlock) >> 4));
           }
-          const uint64_t da = smem_desc_sw128(stage), db = smem_desc_sw128(stage + kStageA);
-          const int left = a.G * 32 - kt * kBK;
+          const bool end = kt == w.kt1 - 1;
+          tc_mma_mxf4(d, da, db, idesc0, tsfa, tsfb, kt > w.kt0 ? 1u : 0u);
 #pragma unroll
-          for (int j = 0; j < kBK / kMmaK; ++j) {
-            if (j * kMmaK < left)
+          for (int j = 1; j < kBK / kMmaK; ++j)
+            if (!end || j < last)
               tc_mma_mxf4(d, da + j * 2, db + j * 2, (j & 1) ? idesc2 : idesc0,
-                          tsfa + 4 * (j / 2), tsfb + 4 * (j / 2) * S::kBRowBlocks,
-                          kt > w.kt0 || j > 0 ? 1u : 0u);
-          }
-          tc_commit(&sh.empty[pos.idx]);
-          if (kt == w.kt1 - 1) tc_commit(&sh.d_full[buf]);
-          pos.next(a.stages);
+                          tsfa + 4 * (j / 2), tsfb + 4 * (j / 2) * S::kBRowBlocks, 1u);
+          if constexpr (S::kCluster > 1)
+            tc_commit_multicast(&sh.empty[idx], (uint16_t)((1 << S::kCluster) - 1));
+          else
+            tc_commit(&sh.empty[idx]);
+          if (end) tc_commit(&sh.d_full[buf]);
         }
+        __syncwarp();
       }
-      if (!ok) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
-      tc_commit(&sh.drain);
-      mbar_wait(&sh.drain, 0);
     }
+    if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
+    tc_commit(&sh.drain);                          // every lane: any may have been elected
+    mbar_wait(&sh.drain, 0);
     __syncwarp();
-  } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + kScaleWarps) {
+  } else if (warp >= kScaleWarp0) {
     // ---------------------------------------------------------- scale bytes
-    const int team = (warp - kScaleWarp0) / 2;
-    constexpr uint32_t kBlocks = kStageA + S::kStageB;
-    if ((warp - kScaleWarp0) % 2 == 0)
-      ok = scale_role<4, 1, false, kGather, S::kStage>(a, sh, ring, kBlocks, team, lane);
-    else
-      ok = scale_role<kN / 32, S::kBRowBlocks, true, kGather, S::kStage>(
-          a, sh, ring, kBlocks + S::kSfA, team, lane);
+    constexpr uint32_t kBlocks = kStageA + S::kStageB, kTokenBlocks = kBlocks + S::kSfA;
+    constexpr uint32_t kStrideB = S::kBRowBlocks * kSfBlock;
+    const int me = warp - kScaleWarp0, team = me / S::kTeamWarps;
+    if (team < S::kTeams) {
+      if (me % S::kTeamWarps == 0)
+        ok = scale_role<4, S::kTeams, S::kChunk, false, kGather, S::kStage, kSfBlock>(a, sh, ring, kBlocks,
+                                                                         team, 0, lane);
+      else if constexpr (kN == kMxNarrow)
+        ok = scale_role<1, S::kTeams, S::kChunk, true, kGather, S::kStage, kStrideB>(a, sh, ring, kTokenBlocks,
+                                                                        team, 0, lane);
+      else if (me % S::kTeamWarps == 1)
+        ok = scale_role<4, S::kTeams, S::kChunk, true, kGather, S::kStage, kStrideB>(a, sh, ring, kTokenBlocks,
+                                                                        team, 0, lane);
+      else
+        ok = scale_role<2, S::kTeams, S::kChunk, true, kGather, S::kStage, kStrideB>(
+            a, sh, ring, kTokenBlocks + kSfBlock, team, 128, lane);
+    }
     if (!ok && lane == 0) atomicAdd(&a.status[kStatusWaitTimeouts], 1ull);
   } else if (warp >= kEpiWarp0) {
     // ------------------------------------------------------------- epilogue
     const int quarter = warp - kEpiWarp0;
     Out* out = static_cast<Out*>(a.out);
+    const bool pairs = a.O % 2 == 0 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0;
     RingPos pu;
     Unit w;
     for (int it = 0;; ++it) {
-      if (!pop_unit<true>(sh, pu, &w)) {
+      if (!pop_unit(sh, pu, &w)) {
         ok = false;
         break;
       }
-      release_unit<true>(sh, pu);
+      release_unit(sh, pu);
       if (w.e < 0) break;
       const int buf = it & 1;
-      if (!mbar_wait_warp(&sh.d_full[buf], (uint32_t)(it >> 1) & 1u)) { ok = false; break; }
+      if (!wait_short(&sh.d_full[buf], (uint32_t)(it >> 1) & 1u)) { ok = false; break; }
       tc_fence_after_sync();
       const int o = w.m0 + quarter * 32 + lane;
       for (int c0 = 0; c0 < w.ntok; c0 += 32) {
@@ -666,11 +804,32 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
         }
+        if constexpr (sizeof(Out) == 2) {        // bf16 is dense and unsplit
+          Out* to = out + (int64_t)(w.tok0 + c0) * a.O;
+          if (pairs) {
+            // Neighbouring lanes share out two columns, so that each stores two rows.
+            const bool odd = (lane & 1) != 0;
+            to += (odd ? a.O : 0) + (o & ~1);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int r = __shfl_sync(kFullMask, row, c);
-          if (c < n && o < a.O)
-            store_out(out + ((int64_t)r * a.splits + w.split) * a.O + o, v[c]);
+            for (int c = 0; c < 32; c += 2) {
+              const float other = __shfl_xor_sync(kFullMask, odd ? v[c] : v[c + 1], 1);
+              const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(other, v[c + 1])
+                                             : __floats2bfloat162_rn(v[c], other);
+              if (c + (odd ? 1 : 0) < n && o < a.O)
+                *reinterpret_cast<__nv_bfloat162*>(to + (int64_t)c * a.O) = two;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < n && o < a.O) store_out(to + (int64_t)c * a.O + o, v[c]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int r = __shfl_sync(kFullMask, row, c);
+            if (c < n && o < a.O)
+              store_out(out + ((int64_t)r * a.splits + w.split) * a.O + o, v[c]);
+          }
         }
       }
     }
@@ -680,6 +839,11 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+  // No CTA goes while the other may still copy to it or arrive on its barriers.
+  if constexpr (S::kCluster > 1) {
+    __syncwarp();
+    cluster_sync();
+  }
 }
 
 // The token rows of a wide routed call in the lists' order, scale rows on
@@ -751,7 +915,7 @@ template <int kN, typename Out, bool kRouted>
 cudaError_t launch_typed(const MxMaps& maps, MxKernelArgs args, int64_t units,
                          cudaStream_t stream) {
   args.stages = stages_for<kN>(args.max_active);
-  if (args.stages < kMinStages) return cudaErrorInvalidValue;
+  if (args.stages < Shape<kN>::kMinStages) return cudaErrorInvalidValue;
   const size_t smem = smem_bytes<kN>(args.stages, args.max_active);
   static std::mutex mu;
   static size_t opted[64] = {};
@@ -767,9 +931,25 @@ cudaError_t launch_typed(const MxMaps& maps, MxKernelArgs args, int64_t units,
       opted[dev] = smem;
     }
   }
-  const unsigned grid = (unsigned)std::min<int64_t>(units, num_sms());
-  return launch_after_previous(gemm_mx_kernel<kN, Out, kRouted>, dim3(grid), dim3(kThreads), smem,
-                               stream, maps, args);
+  constexpr int kCluster = Shape<kN>::kCluster;
+  const int64_t most = num_sms() / kCluster;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min(units, most) * kCluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster > 1 ? 2 : 1;
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, gemm_mx_kernel<kN, Out, kRouted>, maps, args);
+  if (err == cudaSuccess) note_launch();
+  return err;
 }
 
 bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
@@ -809,10 +989,11 @@ Plan plan_of(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed)
   if (!routed) {
     // As many blocks as fill whole rounds of the SMs best, by the width of a
     // round's blocks (in 16 tokens, plus 2 for what a unit costs besides).
-    const int64_t sms = 152;
+    const int64_t pair = p.wide ? Shape<kMxWide>::kCluster : 1;
+    const int64_t sms = 152 / pair, tiles = (mtiles + pair - 1) / pair;
     int64_t best = INT64_MAX;
     for (int64_t b = few; b <= few + few / 4 + 1; ++b) {
-      const int64_t rounds = (b * mtiles * p.splits + sms - 1) / sms;
+      const int64_t rounds = (b * tiles * p.splits + sms - 1) / sms;
       const int64_t cost = rounds * (((T + b - 1) / b + 15) / 16 + 2);
       if (cost < best) {
         best = cost;
@@ -875,8 +1056,11 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   {
     const cuuint64_t dims[2] = {row, (cuuint64_t)nrows};
     const cuuint64_t strides[1] = {row};
-    const cuuint32_t box[2] = {kRowBytes, routed && !grouped ? 1u : 32u};
-    if (!encode(&maps.b, rows, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    const bool gather = routed && !grouped;
+    for (int i = 0; i < (wide ? kMxWide / 32 : 1); ++i) {
+      const cuuint32_t box[2] = {kRowBytes, gather ? 1u : wide ? 16u * (unsigned)(i + 1) : 32u};
+      if (!encode(&maps.b[i], rows, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    }
   }
   MxKernelArgs a;
   std::memset(static_cast<void*>(&a), 0, sizeof(a));
@@ -895,7 +1079,8 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   a.splits = g.splits;
   a.blocks = (int)plan.blocks;
   a.max_active = routed ? (int)std::min(g.E, P) : 0;
-  const int64_t units = plan.blocks * a.mtiles * a.splits;
+  const int64_t pair = wide ? Shape<kMxWide>::kCluster : 1;
+  const int64_t units = plan.blocks * ((a.mtiles + pair - 1) / pair) * a.splits;
   if (units > 0x7fffffff) return cudaErrorInvalidValue;
   cudaError_t err;
   if (routed)
