@@ -12,6 +12,7 @@ as the experts' weights are.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -22,15 +23,18 @@ __all__ = ["route_experts", "quantize_mxfp4", "dequantize_mxfp4", "mxfp4_linear"
 
 _DTYPES = {torch.float32: _native.DTYPE_F32, torch.bfloat16: _native.DTYPE_BF16}
 _INDEX_DTYPES = {torch.int32: _native.INDEX_I32, torch.int64: _native.INDEX_I64}
-_REJECTED = ctypes.c_size_t(-1).value     # a workspace size the library has no answer for
 _SCORES = {"softmax": _native.SCORE_SOFTMAX, "sigmoid": _native.SCORE_SIGMOID}
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
 
 # The current stream's handle of a device by index (see attention.py).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_empty = torch.empty
 
 
-def _call(f, name: str, index: int, args: tuple) -> None:
+# As in attention.py: the calls are short next to what Python spends on them, so
+# each writes its checks out once, and what it refuses is worked out only then.
+def _call(f, name: str, index: int, *args) -> None:
     """One library call on device `index`, its current stream last."""
     if _current_device() == index:
         rc = f(*args, _raw_stream(index))
@@ -41,16 +45,11 @@ def _call(f, name: str, index: int, args: tuple) -> None:
         _native.check(rc, name)
 
 
-def _output(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype,
-            like: torch.Tensor) -> torch.Tensor:
-    """The output tensor: a new one, or the caller's if it fits."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if t.shape != shape or t.dtype is not dtype or t.device != like.device \
+def _check_out(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, index: int) -> None:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index \
             or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on "
-                         f"{like.device}")
-    return t
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on the "
+                         "inputs' device")
 
 
 def route_experts(logits: torch.Tensor, K: int, *, score: str = "softmax",
@@ -72,35 +71,43 @@ def route_experts(logits: torch.Tensor, K: int, *, score: str = "softmax",
     NaN logits leave over get id -1 and weight 0. At most 1024 experts, 32
     groups and K = 32. See mxfp4_route_experts in the C header.
     """
-    if not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2:
+    shape, stride, dtype, index = logits.shape, logits.stride(), logits.dtype, logits.get_device()
+    if index < 0 or dtype not in _DTYPES or len(shape) != 2:
         raise ValueError("logits must be a (T, E) float32 or bfloat16 CUDA tensor")
-    T, E = logits.shape
-    if E > 1 and logits.stride(1) != 1:
+    T, E = shape
+    if stride[1] != 1 and E > 1:
         raise ValueError("the rows of logits must be contiguous")
     if score not in _SCORES:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     if groups < 1 or E < 1 or E % groups:
         raise ValueError("groups must divide the number of experts")
-    top_groups = groups if top_groups is None else top_groups
+    if top_groups is None:
+        top_groups = groups
     if not 1 <= top_groups <= groups:
         raise ValueError("need 1 <= top_groups <= groups")
     if not 0 <= K <= top_groups * (E // groups):
         raise ValueError("K must be at most the experts of top_groups groups")
-    if group_best not in (1, 2):
+    if group_best != 2 and group_best != 1:
         raise ValueError("group_best must be 1 or 2")
-    index = logits.get_device()
-    if bias is not None and (bias.dtype is not torch.float32 or bias.get_device() != index
+    if bias is not None and (bias.dtype is not _F32 or bias.get_device() != index
                              or bias.shape != (E,) or not bias.is_contiguous()):
         raise ValueError("bias must be a contiguous (E,) float32 tensor on the logits' device")
-    sel = _output("selected_experts", selected_experts, (T, K), torch.int32, logits)
-    p = _output("mixture_weights", mixture_weights, (T, K), torch.float32, logits)
+    device = logits.device
+    if selected_experts is None:
+        selected_experts = _empty((T, K), dtype=_I32, device=device)
+    else:
+        _check_out("selected_experts", selected_experts, (T, K), _I32, index)
+    if mixture_weights is None:
+        mixture_weights = _empty((T, K), dtype=_F32, device=device)
+    else:
+        _check_out("mixture_weights", mixture_weights, (T, K), _F32, index)
     if T and K:
-        _call(_native.load().mxfp4_route_experts, "route_experts", index, (
-            logits.data_ptr(), _DTYPES[logits.dtype], logits.stride(0),
-            None if bias is None else bias.data_ptr(), T, E, K, _SCORES[score], groups,
-            top_groups, group_best, 1 if normalize else 0, scaling, sel.data_ptr(),
-            p.data_ptr()))
-    return sel, p
+        _call(_native.load().mxfp4_route_experts, "route_experts", index,
+              logits.data_ptr(), _DTYPES[dtype], stride[0],
+              None if bias is None else bias.data_ptr(), T, E, K, _SCORES[score], groups,
+              top_groups, group_best, 1 if normalize else 0, scaling,
+              selected_experts.data_ptr(), mixture_weights.data_ptr())
+    return selected_experts, mixture_weights
 
 
 def quantize_mxfp4(x: torch.Tensor, packed: torch.Tensor | None = None,
@@ -114,11 +121,11 @@ def quantize_mxfp4(x: torch.Tensor, packed: torch.Tensor | None = None,
     number, ties to the even code, larger ones to 6. A group with an infinity
     or a NaN reads back as NaN. See mxfp4_quantize in the C header.
     """
-    if not x.is_cuda or x.dtype not in _DTYPES or x.dim() == 0:
+    *lead, I = x.shape if x.dim() else (0,)
+    dtype, index = x.dtype, x.get_device()
+    if index < 0 or dtype not in _DTYPES or x.dim() == 0:
         raise ValueError("x must be a (..., I) float32 or bfloat16 CUDA tensor")
-    shape = x.shape
-    I = shape[-1]
-    if I == 0 or I % 32:
+    if I == 0 or I & 31:
         raise ValueError("the last dimension must be a positive multiple of 32")
     if x.is_contiguous():
         rows, stride = x.numel() // I, I
@@ -130,26 +137,37 @@ def quantize_mxfp4(x: torch.Tensor, packed: torch.Tensor | None = None,
         if flat is None or flat.stride(1) != 1 or (flat.shape[0] > 1 and flat.stride(0) < I):
             raise ValueError("the rows of x must be contiguous and evenly apart")
         rows, stride = flat.shape[0], flat.stride(0)
-    packed = _output("packed", packed, shape[:-1] + (I // 32, 16), torch.uint8, x)
-    scales = _output("scales", scales, shape[:-1] + (I // 32,), torch.uint8, x)
+    G, device = I >> 5, x.device
+    if packed is None:
+        packed = _empty((*lead, G, 16), dtype=_U8, device=device)
+    else:
+        _check_out("packed", packed, (*lead, G, 16), _U8, index)
+    if scales is None:
+        scales = _empty((*lead, G), dtype=_U8, device=device)
+    else:
+        _check_out("scales", scales, (*lead, G), _U8, index)
     if rows:
-        _call(_native.load().mxfp4_quantize, "quantize_mxfp4", x.get_device(), (
-            x.data_ptr(), _DTYPES[x.dtype], stride, rows, I, packed.data_ptr(),
-            scales.data_ptr()))
+        _call(_native.load().mxfp4_quantize, "quantize_mxfp4", index, x.data_ptr(),
+              _DTYPES[dtype], stride, rows, I, packed.data_ptr(), scales.data_ptr())
     return packed, scales
 
 
-def _mxfp4_rows(what: str, packed: torch.Tensor, scales: torch.Tensor) -> None:
-    """Refuses anything but MXFP4 rows that the library can read."""
-    if not packed.is_cuda or scales.device != packed.device:
-        raise ValueError(f"{what}: packed and scales must be on one CUDA device")
-    if packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+def _mxfp4_rows(what: str, packed: torch.Tensor, scales: torch.Tensor, index: int) -> torch.Size:
+    """The shape of packed; refuses anything but MXFP4 rows of device `index`
+    that the library can read."""
+    shape = packed.shape
+    if packed.dtype is _U8 and scales.dtype is _U8 and len(shape) > 1 and shape[-1] == 16 \
+            and shape[:-1] == scales.shape and shape[-2] and packed.get_device() == index \
+            and scales.get_device() == index and index >= 0 and packed.is_contiguous() \
+            and scales.is_contiguous():
+        return shape
+    if packed.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError(f"{what}: packed and scales must be uint8")
-    if packed.dim() < 2 or packed.shape[-1] != 16 or packed.shape[:-1] != scales.shape \
-            or packed.shape[-2] == 0:
-        raise ValueError(f"{what}: expected packed (..., I/32, 16) and scales (..., I/32)")
+    if index < 0 or packed.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{what}: packed and scales must be on one CUDA device with the rest")
     if not packed.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{what}: packed and scales must be contiguous")
+    raise ValueError(f"{what}: expected packed (..., I/32, 16) and scales (..., I/32)")
 
 
 def dequantize_mxfp4(packed: torch.Tensor, scales: torch.Tensor,
@@ -158,16 +176,29 @@ def dequantize_mxfp4(packed: torch.Tensor, scales: torch.Tensor,
     """The values (..., I) that MXFP4 rows packed (..., I/32, 16) and scales
     (..., I/32) stand for, float32 or bfloat16: exact in both. A scale byte of
     255 gives NaN. See mxfp4_dequantize in the C header."""
-    _mxfp4_rows("dequantize_mxfp4", packed, scales)
+    index = packed.get_device()
+    *lead, G, _ = _mxfp4_rows("dequantize_mxfp4", packed, scales, index)
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
-    I = 32 * packed.shape[-2]
-    out = _output("out", out, packed.shape[:-2] + (I,), dtype, packed)
-    rows = packed.numel() // (I // 2)
+    I = 32 * G
+    if out is None:
+        out = _empty((*lead, I), dtype=dtype, device=packed.device)
+    else:
+        _check_out("out", out, (*lead, I), dtype, index)
+    rows = packed.numel() // (16 * G)
     if rows:
-        _call(_native.load().mxfp4_dequantize, "dequantize_mxfp4", packed.get_device(), (
-            packed.data_ptr(), scales.data_ptr(), rows, I, out.data_ptr(), _DTYPES[dtype]))
+        _call(_native.load().mxfp4_dequantize, "dequantize_mxfp4", index, packed.data_ptr(),
+              scales.data_ptr(), rows, I, out.data_ptr(), _DTYPES[dtype])
     return out
+
+
+# The scratch of a call depends on its sizes alone.
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, *sizes: int) -> int:
+    n = getattr(_native.load(), name)(*sizes)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("sizes rejected by the library")
+    return n
 
 
 def mxfp4_linear(x_packed: torch.Tensor, x_scales: torch.Tensor, packed_weights: torch.Tensor,
@@ -177,28 +208,25 @@ def mxfp4_linear(x_packed: torch.Tensor, x_scales: torch.Tensor, packed_weights:
     (T, I/32)) and MXFP4 weights W (packed_weights (O, I/32, 16), scale_bytes
     (O, I/32)), in float32 or bfloat16. Products are exact, sums float32. See
     mxfp4_linear in the C header."""
-    _mxfp4_rows("tokens", x_packed, x_scales)
-    _mxfp4_rows("weights", packed_weights, scale_bytes)
-    if x_packed.dim() != 3 or packed_weights.dim() != 3 \
-            or x_packed.shape[1] != packed_weights.shape[1]:
+    index = x_packed.get_device()
+    xs = _mxfp4_rows("tokens", x_packed, x_scales, index)
+    ws = _mxfp4_rows("weights", packed_weights, scale_bytes, index)
+    if len(xs) != 3 or len(ws) != 3 or xs[1] != ws[1]:
         raise ValueError("expected tokens (T, I/32, 16) and weights (O, I/32, 16)")
-    if packed_weights.device != x_packed.device:
-        raise ValueError(f"weights are on {packed_weights.device}, tokens on {x_packed.device}")
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
-    T, G, _ = x_packed.shape
-    I, O = 32 * G, packed_weights.shape[0]
-    out = _output("out", out, (T, O), dtype, x_packed)
+    T, I, O = xs[0], 32 * xs[1], ws[0]
+    if out is None:
+        out = _empty((T, O), dtype=dtype, device=x_packed.device)
+    else:
+        _check_out("out", out, (T, O), dtype, index)
     if T and O:
-        lib = _native.load()
-        need = lib.mxfp4_linear_workspace_size(T, I, O)
-        if need == _REJECTED:
-            raise ValueError("sizes rejected by the library")
-        ws = torch.empty(need, dtype=torch.uint8, device=x_packed.device) if need else None
-        _call(lib.mxfp4_linear, "mxfp4_linear", x_packed.get_device(), (
-            x_packed.data_ptr(), x_scales.data_ptr(), packed_weights.data_ptr(),
-            scale_bytes.data_ptr(), out.data_ptr(), T, I, O, _DTYPES[dtype],
-            None if ws is None else ws.data_ptr(), need))
+        need = _workspace_bytes("mxfp4_linear_workspace_size", T, I, O)
+        work = _empty(need, dtype=_U8, device=x_packed.device) if need else None
+        _call(_native.load().mxfp4_linear, "mxfp4_linear", index, x_packed.data_ptr(),
+              x_scales.data_ptr(), packed_weights.data_ptr(), scale_bytes.data_ptr(),
+              out.data_ptr(), T, I, O, _DTYPES[dtype],
+              None if work is None else work.data_ptr(), need)
     return out
 
 
@@ -219,36 +247,34 @@ def mxfp4_expert_linear_quantized(x_packed: torch.Tensor, x_scales: torch.Tensor
     mxfp4_expert_linear_quantized in the C header.
     """
     sel, p, ys = selected_experts, mixture_weights, shared_output
-    _mxfp4_rows("tokens", x_packed, x_scales)
-    _mxfp4_rows("weights", packed_weights, scale_bytes)
-    if x_packed.dim() != 3 or packed_weights.dim() != 4 \
-            or x_packed.shape[1] != packed_weights.shape[2]:
-        raise ValueError("expected tokens (T, I/32, 16) and weights (E, O, I/32, 16)")
-    T, G, _ = x_packed.shape
-    E, O = packed_weights.shape[:2]
     index = x_packed.get_device()
-    for name, t in (("weights", packed_weights), ("selected_experts", sel),
-                    ("mixture_weights", p), ("shared_output", ys)):
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, tokens on {x_packed.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if sel.dtype not in _INDEX_DTYPES or p.dtype is not torch.float32:
-        raise TypeError("selected_experts must be int32 or int64, mixture_weights float32")
-    if ys.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {ys.dtype}")
-    if sel.dim() != 2 or sel.shape[0] != T or p.shape != sel.shape or ys.shape != (T, O):
+    xs = _mxfp4_rows("tokens", x_packed, x_scales, index)
+    ws = _mxfp4_rows("weights", packed_weights, scale_bytes, index)
+    if len(xs) != 3 or len(ws) != 4 or xs[1] != ws[2]:
+        raise ValueError("expected tokens (T, I/32, 16) and weights (E, O, I/32, 16)")
+    T, I, (E, O) = xs[0], 32 * xs[1], ws[:2]
+    shape = sel.shape
+    if len(shape) != 2 or shape[0] != T or p.shape != shape or ys.shape != (T, O):
         raise ValueError("routing or shared-output shape mismatch")
-    K, I = sel.shape[1], 32 * G
-    out = _output("out", out, (T, O), ys.dtype, ys)
+    if sel.dtype not in _INDEX_DTYPES or p.dtype is not _F32:
+        raise TypeError("selected_experts must be int32 or int64, mixture_weights float32")
+    dtype, K = ys.dtype, shape[1]
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    if sel.get_device() != index or p.get_device() != index or ys.get_device() != index:
+        raise ValueError("routing and shared_output must be on the tokens' device")
+    if not (sel.is_contiguous() and p.is_contiguous() and ys.is_contiguous()):
+        raise ValueError("routing and shared_output must be contiguous")
+    if out is None:
+        out = torch.empty_like(ys)
+    else:
+        _check_out("out", out, (T, O), dtype, index)
     if T and O:
-        lib = _native.load()
-        need = lib.mxfp4_expert_linear_quantized_workspace_size(T, E, I, O, K)
-        if need == _REJECTED:
-            raise ValueError("sizes rejected by the library")
-        ws = torch.empty(need, dtype=torch.uint8, device=ys.device)
-        _call(lib.mxfp4_expert_linear_quantized, "mxfp4_expert_linear_quantized", index, (
-            x_packed.data_ptr(), x_scales.data_ptr(), packed_weights.data_ptr(),
-            scale_bytes.data_ptr(), sel.data_ptr(), p.data_ptr(), ys.data_ptr(), out.data_ptr(),
-            T, E, I, O, K, _DTYPES[ys.dtype], _INDEX_DTYPES[sel.dtype], ws.data_ptr(), need))
+        need = _workspace_bytes("mxfp4_expert_linear_quantized_workspace_size", T, E, I, O, K)
+        work = _empty(need, dtype=_U8, device=ys.device)
+        _call(_native.load().mxfp4_expert_linear_quantized, "mxfp4_expert_linear_quantized",
+              index, x_packed.data_ptr(), x_scales.data_ptr(), packed_weights.data_ptr(),
+              scale_bytes.data_ptr(), sel.data_ptr(), p.data_ptr(), ys.data_ptr(),
+              out.data_ptr(), T, E, I, O, K, _DTYPES[dtype], _INDEX_DTYPES[sel.dtype],
+              work.data_ptr(), need)
     return out
