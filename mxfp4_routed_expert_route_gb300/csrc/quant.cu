@@ -10,8 +10,11 @@
 // Largest magnitudes compare as integers, so a NaN or an infinity shows as a
 // maximum of 0x7f800000 or more.
 //
-// Both directions only move bytes: kPerThread values per thread, one 16-byte
-// access wherever alignment allows.
+// Both directions only move bytes. A warp takes 1024 values at a time, eight
+// per lane four times over, so that four loads per lane are in flight (one at a
+// time, with a division for the row of every eight values: 37 us for 8192 x 7168
+// bf16, against 22 us for its 149 MB at the rate of a copy); the 32 scale bytes
+// of a task are stored together.
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,7 +24,10 @@ namespace mxfp4el {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPerThread = 8;                 // values per thread: four threads share a group
+constexpr int kPerThread = 8;                 // values per thread and step: four threads share a group
+constexpr int kSteps = 4;                     // steps of a task
+constexpr int kStep = 32 * kPerThread;        // values of a warp's step
+constexpr int kTask = kStep * kSteps;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 // Eight float32 values to eight E2M1 codes, the first in the low nibble.
@@ -69,38 +75,47 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   }
 }
 
+// rows x I values as rows x segs tasks; a contiguous matrix is one row.
 template <typename Tok, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 quantize_kernel(const Tok* __restrict__ x, int64_t row_stride, int64_t rows, int64_t I,
-                uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
+                int64_t segs, uint8_t* __restrict__ packed, uint8_t* __restrict__ scales) {
   pdl_launch_dependents();
-  const int64_t per_row = I / kPerThread;
-  const int64_t n = rows * per_row;           // a multiple of four: groups are never cut
-  // Whole warps step together, since the threads of a group exchange maxima.
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-       at - (threadIdx.x & 31) < n; at += step) {
-    const bool in = at < n;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in) {
-      const int64_t r = at / per_row;
-      load8<kVec>(x + r * row_stride + (at - r * per_row) * kPerThread, v);
-    }
-    uint32_t m = 0;
+  const int lane = threadIdx.x & 31;
+  const int64_t tasks = rows * segs, step = (int64_t)gridDim.x * (kThreads / 32);
+  for (int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); task < tasks;
+       task += step) {
+    const int64_t r = rows == 1 ? 0 : task / segs;
+    const int64_t col = (task - r * segs) * kTask;         // first value of the task
+    const Tok* from = x + r * row_stride + col + lane * kPerThread;
+    const int left = (int)min((int64_t)kTask, I - col);    // its values, a multiple of 32
+    float v[kSteps][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(kFullMask, m, 1));
-    m = max(m, __shfl_xor_sync(kFullMask, m, 2));
-    const bool finite = m < kInfBits;
-    const int s = finite ? max((int)(m >> 23) - 2, 0) : 255;
-    const float up = __uint_as_float((uint32_t)(254 - min(s, 252)) << 23);   // 2^(127 - s)
+    for (int j = 0; j < kSteps; ++j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= up;
-    const uint32_t q = finite ? f32x8_to_e2m1(v) : 0u;
-    if (in) {
-      reinterpret_cast<uint32_t*>(packed)[at] = q;
-      if ((at & 3) == 0) scales[at >> 2] = (uint8_t)s;
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+      if (j * kStep + lane * kPerThread < left) load8<kVec>(from + j * kStep, v[j]);
     }
+    uint32_t* to = reinterpret_cast<uint32_t*>(packed) + (r * I + col) / 8 + lane;
+    int scale = 0;                                         // of group `lane` of the task
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[j][i]) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(kFullMask, m, 1));
+      m = max(m, __shfl_xor_sync(kFullMask, m, 2));
+      const bool finite = m < kInfBits;
+      const int s = finite ? max((int)(m >> 23) - 2, 0) : 255;
+      const float up = __uint_as_float((uint32_t)(254 - min(s, 252)) << 23);   // 2^(127 - s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] *= up;
+      const uint32_t q = finite ? f32x8_to_e2m1(v[j]) : 0u;
+      if (j * kStep + lane * kPerThread < left) to[j * 32] = q;
+      const int moved = __shfl_sync(kFullMask, s, 4 * (lane & 7));
+      if (lane >> 3 == j) scale = moved;
+    }
+    if (lane * 32 < left) scales[(r * I + col) / 32 + lane] = (uint8_t)scale;
   }
 }
 
@@ -125,42 +140,60 @@ dequantize_kernel(const uint8_t* __restrict__ packed, const uint8_t* __restrict_
   pdl_launch_dependents();
   pdl_wait();                                 // the codes may come from the kernel before
   const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < n; at += step) {
-    const uint32_t q = reinterpret_cast<const uint32_t*>(packed)[at];
-    const uint32_t s = scales[at >> 2];
-    uint32_t f = s << 23;                     // 2^(s - 127)
-    if (s == 0) f = 0x00400000u;              // a subnormal float32
-    if (s == 255) f = 0x7fc00000u;            // NaN
-    const float by = __uint_as_float(f);
-    uint32_t h[4];
-    e2m1x8_to_f16x2x4(q, h);
-    float2 v[4];
+  for (int64_t at0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; at0 < n; at0 += kSteps * step) {
+    uint32_t q[kSteps], s[kSteps];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = f16x2_to_f32x2(h[i]);
-      v[i].x *= by;
-      v[i].y *= by;
+    for (int j = 0; j < kSteps; ++j) {
+      const int64_t at = at0 + j * step;
+      q[j] = at < n ? reinterpret_cast<const uint32_t*>(packed)[at] : 0u;
+      s[j] = at < n ? scales[at >> 2] : 0u;
     }
-    store8(out + at * kPerThread, v);
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+      const int64_t at = at0 + j * step;
+      if (at >= n) break;
+      uint32_t f = s[j] << 23;                // 2^(s - 127)
+      if (s[j] == 0) f = 0x00400000u;         // a subnormal float32
+      if (s[j] == 255) f = 0x7fc00000u;       // NaN
+      const float by = __uint_as_float(f);
+      uint32_t h[4];
+      e2m1x8_to_f16x2x4(q[j], h);
+      float2 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = f16x2_to_f32x2(h[i]);
+        v[i].x *= by;
+        v[i].y *= by;
+      }
+      store8(out + at * kPerThread, v);
+    }
   }
 }
 
+// Blocks for n threads' first steps: few enough for a second round where there
+// is work for the whole GPU.
 unsigned grid_for(int64_t n) {
-  return (unsigned)std::min<int64_t>((n + kThreads - 1) / kThreads, 152 * 64);
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + kThreads - 1) / kThreads, 152 * 8));
 }
 
 template <typename Tok>
 cudaError_t quantize_typed(const Tok* x, int64_t row_stride, int64_t rows, int64_t I,
                            uint8_t* packed, uint8_t* scales, cudaStream_t stream) {
-  const int64_t n = rows * (I / kPerThread);
+  if (rows > 1 && row_stride == I) {
+    I *= rows;
+    rows = 1;
+  }
+  const int64_t segs = (I + kTask - 1) / kTask, tasks = rows * segs;
   const bool vec = reinterpret_cast<uintptr_t>(x) % 16 == 0 &&
                    (rows == 1 || row_stride * (int64_t)sizeof(Tok) % 16 == 0);
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((tasks + kThreads / 32 - 1) / (kThreads / 32), 1 << 20);
   if (vec)
-    quantize_kernel<Tok, true><<<grid_for(n), kThreads, 0, stream>>>(x, row_stride, rows, I,
-                                                                     packed, scales);
+    quantize_kernel<Tok, true><<<grid, kThreads, 0, stream>>>(x, row_stride, rows, I, segs, packed,
+                                                              scales);
   else
-    quantize_kernel<Tok, false><<<grid_for(n), kThreads, 0, stream>>>(x, row_stride, rows, I,
-                                                                      packed, scales);
+    quantize_kernel<Tok, false><<<grid, kThreads, 0, stream>>>(x, row_stride, rows, I, segs,
+                                                               packed, scales);
   const cudaError_t err = cudaGetLastError();
   if (err == cudaSuccess) note_launch();
   return err;

@@ -38,54 +38,63 @@ __device__ __forceinline__ double softmax_term(float logit, float top) {
   return logit == top ? 1.0 : logit < top ? exp((double)logit - (double)top) : 0.0;
 }
 
-// Lane and value of the highest value among lanes with `has`, ties to the lower
-// index; index -1 where no lane has one.
-struct Best {
-  double value;
-  int index;
-};
-__device__ __forceinline__ Best warp_best(Best b) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const double v = __shfl_xor_sync(kFullMask, b.value, o);
-    const int i = __shfl_xor_sync(kFullMask, b.index, o);
-    if (i >= 0 && (b.index < 0 || v > b.value || (v == b.value && i < b.index))) b = {v, i};
-  }
-  return b;
+// A double as an unsigned integer of the same order, at least 1; 0 for NaN.
+// (Comparisons of doubles go through the float64 pipe, which is slow.)
+__device__ __forceinline__ unsigned long long order_key(double v) {
+  const long long u = __double_as_longlong(v + 0.0);
+  return v == v ? (unsigned long long)u ^ ((unsigned long long)(u >> 63) | (1ull << 63)) : 0ull;
 }
 
-// One token by one warp, in float64. choice: E doubles of shared memory.
+// The highest key of the warp, and the lowest index that has it; -1 where every
+// key is 0.
+__device__ __forceinline__ int warp_best(unsigned long long key, int index) {
+  const unsigned hi = __reduce_max_sync(kFullMask, (unsigned)(key >> 32));
+  const bool in = (unsigned)(key >> 32) == hi;
+  const unsigned lo = __reduce_max_sync(kFullMask, in ? (unsigned)key : 0u);
+  if ((hi | lo) == 0u) return -1;
+  return (int)__reduce_min_sync(kFullMask, in && (unsigned)key == lo ? (unsigned)index : ~0u);
+}
+
+// One token by one warp, in float64. scratch: E doubles of shared memory.
 template <typename Tok>
-__device__ __noinline__ void route_token(const RouteArgs& a, const Tok* row, double* choice, int64_t t) {
+__device__ __noinline__ void route_token(const RouteArgs& a, const Tok* row, double* scratch,
+                                         int64_t t) {
   const int lane = threadIdx.x & 31;
+  unsigned long long* key = reinterpret_cast<unsigned long long*>(scratch);
   float top = -INFINITY;
-  double sum = 0.0;
+  double inv = 1.0;
   if (a.softmax) {
+    double sum = 0.0;
     for (int e = lane; e < a.E; e += 32) top = fmaxf(top, to_f32(row[e]));   // NaN loses
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-    for (int e = lane; e < a.E; e += 32) sum += softmax_term(to_f32(row[e]), top);
+    for (int e = lane; e < a.E; e += 32) {
+      scratch[e] = softmax_term(to_f32(row[e]), top);
+      sum += scratch[e];
+    }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+    inv = 1.0 / sum;
   }
   auto score_of = [&](float logit) {
-    return a.softmax ? softmax_term(logit, top) / sum : 1.0 / (1.0 + exp(-(double)logit));
+    return a.softmax ? softmax_term(logit, top) * inv : 1.0 / (1.0 + exp(-(double)logit));
   };
-  // NaN marks an expert that cannot be taken (any more).
+  // A choice that is NaN cannot be taken; nor, later on, one that is 0.
   for (int e = lane; e < a.E; e += 32) {
     const float l = to_f32(row[e]);
-    const double c = score_of(l) + (a.bias != nullptr ? (double)a.bias[e] : 0.0);
-    choice[e] = l == l ? c : (double)NAN;
+    const double score = a.softmax ? scratch[e] * inv : score_of(l);
+    const double c = l == l ? score + (a.bias != nullptr ? (double)a.bias[e] : 0.0) : (double)NAN;
+    if (a.groups > 1) scratch[e] = c;
+    else key[e] = order_key(a.bias != nullptr || !(c == c) ? c : (double)l);
   }
   __syncwarp();
-  unsigned kept = ~0u;
   if (a.groups > 1) {
-    Best mine = {0.0, -1};
+    double v = (double)NAN;
     if (lane < a.groups) {
       double b0 = 0.0, b1 = 0.0;
       int n = 0;
       for (int j = 0; j < a.group_size; ++j) {
-        const double c = choice[lane * a.group_size + j];
+        const double c = scratch[lane * a.group_size + j];
         if (!(c == c)) continue;
         if (n == 0 || c > b0) {
           b1 = b0;
@@ -95,30 +104,37 @@ __device__ __noinline__ void route_token(const RouteArgs& a, const Tok* row, dou
         }
         ++n;
       }
-      const double v = a.group_best > 1 && n > 1 ? b0 + b1 : b0;
-      if (n > 0 && v == v) mine = {v, lane};
+      if (n > 0) v = a.group_best > 1 && n > 1 ? b0 + b1 : b0;
     }
-    kept = 0u;
+    unsigned kept = 0u;
+    unsigned long long mine = order_key(v);
     for (int i = 0; i < a.top_groups; ++i) {
-      const Best b = warp_best(mine);
-      if (b.index < 0) break;
-      kept |= 1u << b.index;
-      if (lane == b.index) mine.index = -1;
+      const int g = warp_best(mine, lane);
+      if (g < 0) break;
+      kept |= 1u << g;
+      if (lane == g) mine = 0ull;
     }
+    __syncwarp();
+    for (int e = lane; e < a.E; e += 32) {
+      const double c = scratch[e];
+      const bool in = (kept >> (e / a.group_size) & 1u) != 0u && c == c;
+      key[e] = in ? order_key(a.bias != nullptr ? c : (double)to_f32(row[e])) : 0ull;
+    }
+    __syncwarp();
   }
   int pick = -1;                                   // lane k: the k-th pick
   for (int k = 0; k < a.K; ++k) {
-    Best mine = {0.0, -1};
-    for (int e = lane; e < a.E; e += 32) {
-      double v = choice[e];
-      if (!(v == v) || (a.groups > 1 && !(kept >> (e / a.group_size) & 1u))) continue;
-      if (a.bias == nullptr) v = (double)to_f32(row[e]);
-      if (mine.index < 0 || v > mine.value) mine = {v, e};
-    }
-    const Best b = warp_best(mine);
-    if (b.index < 0) break;
-    if (lane == k) pick = b.index;
-    if (lane == (b.index & 31)) choice[b.index] = (double)NAN;
+    unsigned long long best = 0ull;
+    int at = 0;
+    for (int e = lane; e < a.E; e += 32)
+      if (key[e] > best) {
+        best = key[e];
+        at = e;
+      }
+    const int e = warp_best(best, at);
+    if (e < 0) break;
+    if (lane == k) pick = e;
+    if (lane == (e & 31)) key[e] = 0ull;
     __syncwarp();
   }
   double w = pick >= 0 ? score_of(to_f32(row[pick])) : 0.0;
@@ -157,9 +173,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// The kept groups of one token as a bit mask. choice: the warp's E choices
-// (NaN: not to be taken). *sure: the border between kept and other groups is
-// wider than the choices' error `err` plus the roundings of their sums.
+// The kept groups of one token as a bit mask. choice: the warp's E choices, or
+// logits where they rank as the choices do (NaN: not to be taken). *sure: the
+// border between kept and other groups is wider than the choices' error `err`
+// plus the roundings of their sums; err = 0: exact.
 __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float* choice,
                                                  float err, bool* sure) {
   const int lane = threadIdx.x & 31;
@@ -198,7 +215,7 @@ __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float
   const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? order_key(v) : 0u);
   if (hi != 0u && kept != 0u) {
     const float a_lo = key_value(lo), a_hi = key_value(hi);
-    *sure = a_lo - a_hi > 4.f * err + (fabsf(a_lo) + fabsf(a_hi)) * 0x1p-22f;
+    *sure = err == 0.f || a_lo - a_hi > 4.f * err + (fabsf(a_lo) + fabsf(a_hi)) * 0x1p-22f;
   }
   return kept;
 }
@@ -211,6 +228,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
                                            int64_t t) {
   const int lane = threadIdx.x & 31;
   const bool by_choice = a.bias != nullptr;
+  // Groups by their best expert alone, without a bias: logits rank them too.
+  const bool by_logit = !by_choice && (a.group_best == 1 || a.group_size == 1);
   uint32_t key[kPer];                              // expert 32 i + lane; 0: none
   float top = 0.f, inv = 1.f;
   // An error bound of every score (the bias adds half an ulp of the choice).
@@ -218,13 +237,13 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
   // product with log2 e) + 1.41 (ex2.approx), which the score sees times e /
   // (1 + e)^2, 0.41 at most over all l; the sum adds 0.5, the reciprocal 0.5
   // (1 ulp of at most 2^-24), and what flushes to 0 is under 2^-126. Softmax,
-  // in units of the largest score 1/sum and 2^-23: the exponential 1.41, the
-  // terms' errors in the sum 16 (|d| exp(-|d|) is small for the far ones), 40
-  // half ulps of the sum and the division.
+  // in units of the largest score 1/sum and 2^-23: the exponential 1 (expf), the
+  // same for the sum's terms, kPer + 5 half ulps of their additions, the
+  // reciprocal and the product 1: at most 8 for kPer <= 4, 16 for 16, 32 for 32.
   float err = 0x1p-22f;
   auto in_range = [&](int i) { return kFull || 32 * i + lane < a.E; };
   auto choice_of = [&](float l, int e) {
-    const float c = kSoftmax ? exp_approx(l - top) * inv : rcp_approx(1.f + exp_approx(-l));
+    const float c = kSoftmax ? expf(l - top) * inv : rcp_approx(1.f + exp_approx(-l));
     return by_choice ? c + a.bias[e] : c;
   };
   {
@@ -240,11 +259,11 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
       if (!(fabsf(top) < INFINITY)) return false;  // infinite or NaN
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) sum += exp_approx(l[i] - top);
+      for (int i = 0; i < kPer; ++i) sum += expf(l[i] - top);
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
       inv = 1.f / sum;
-      err = inv * 0x1p-17f;
+      err = inv * (kPer <= 4 ? 0x1p-20f : kPer <= 16 ? 0x1p-19f : 0x1p-18f);
     }
     if (by_choice) {
 #pragma unroll
@@ -256,7 +275,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
     } else {                                       // the logits' own order
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (a.groups > 1 && in_range(i)) scratch[32 * i + lane] = choice_of(l[i], 32 * i + lane);
+        if (a.groups > 1 && in_range(i))
+          scratch[32 * i + lane] = by_logit ? l[i] + 0.f : choice_of(l[i], 32 * i + lane);
         key[i] = in_range(i) ? order_key(l[i] + 0.f) : 0u;
       }
     }
@@ -268,7 +288,7 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
   if (a.groups > 1) {
     __syncwarp();
     bool sure = true;
-    const unsigned kept = route_groups(a, scratch, err, &sure);
+    const unsigned kept = route_groups(a, scratch, by_logit ? 0.f : err, &sure);
     if (!sure) return false;
     // e / group_size by a multiplication: exact for e * group_size < 2^20.
     const uint32_t mul = ((1u << 20) + a.group_size - 1) / a.group_size;
@@ -410,7 +430,9 @@ auto kernel_for(int E) {
     case 384: return route_experts_kernel<12, true, kSoftmax, Tok>;
     case 512: return route_experts_kernel<16, true, kSoftmax, Tok>;
   }
-  return E <= 128   ? route_experts_kernel<4, false, kSoftmax, Tok>
+  return E <= 32    ? route_experts_kernel<1, false, kSoftmax, Tok>
+         : E <= 64  ? route_experts_kernel<2, false, kSoftmax, Tok>
+         : E <= 128 ? route_experts_kernel<4, false, kSoftmax, Tok>
          : E <= 256 ? route_experts_kernel<8, false, kSoftmax, Tok>
          : E <= 512 ? route_experts_kernel<16, false, kSoftmax, Tok>
                     : route_experts_kernel<32, false, kSoftmax, Tok>;
