@@ -44,7 +44,7 @@
 // (block, 128-row tile, K split)):
 //   warp 0      copies of codes (weights and tokens), one elected lane; TMEM
 //   warp 1      scale copies to tensor memory and MMAs, one elected lane
-//   warp 2      prefix of the experts' blocks at start (routed)
+//   warp 2      lists of the experts with tokens at start (routed)
 //   warp 3      the units: finds each next one and hands it to the other roles
 //               through a ring in shared memory, ahead of them (finding one
 //               takes several dependent loads)
@@ -139,6 +139,16 @@ struct __align__(16) Unit {
   int kt0, kt1;       // stages of K
   int once;           // this block alone reads the weights
 };
+
+// The experts with tokens, in shared memory: id, first position in the lists
+// and blocks before, with one entry more of the latter two for the end.
+struct ExpertLists {
+  int *blocks, *first, *id;
+  __device__ __forceinline__ ExpertLists(void* base, int max_active)
+      : blocks(static_cast<int*>(base)), first(blocks + max_active + 1),
+        id(first + max_active + 1) {}
+};
+constexpr size_t list_bytes(int max_active) { return (3 * (size_t)max_active + 2) * sizeof(int); }
 
 template <int kRows>
 struct __align__(16) MxShared {
@@ -260,8 +270,8 @@ struct RingPos {
 };
 
 template <int kN, bool kRouted>
-__device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix, int num_active,
-                                        int idx, int rank) {
+__device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const ExpertLists& ex,
+                                        int num_active, int idx, int rank) {
   constexpr int kPair = Shape<kN>::kCluster;   // tiles of a unit, one per CTA of the cluster
   Unit w;
   const int mtiles = (a.mtiles + kPair - 1) / kPair;
@@ -269,17 +279,17 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const int* prefix
   int first = 0, nblk, cnt, local;
   if constexpr (kRouted) {
     const int blk = idx / per_block;
-    int lo = 0, hi = num_active;           // prefix[u] <= blk < prefix[u + 1]
+    int lo = 0, hi = num_active;           // blocks[lo] <= blk < blocks[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= blk) lo = mid;
+      if (ex.blocks[mid] <= blk) lo = mid;
       else hi = mid;
     }
-    w.e = a.plan.active[lo];
-    first = a.plan.offsets[w.e];
-    cnt = a.plan.offsets[w.e + 1] - first;
-    nblk = prefix[lo + 1] - prefix[lo];
-    local = idx - prefix[lo] * per_block;
+    w.e = ex.id[lo];
+    first = ex.first[lo];
+    cnt = ex.first[lo + 1] - first;
+    nblk = ex.blocks[lo + 1] - ex.blocks[lo];
+    local = idx - ex.blocks[lo] * per_block;
   } else {
     w.e = 0;
     cnt = a.T;
@@ -514,7 +524,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   Shared& sh = *reinterpret_cast<Shared*>(ring + (size_t)a.stages * S::kStage);
-  int* prefix = reinterpret_cast<int*>(&sh + 1);       // [max_active + 1] (routed)
+  const ExpertLists ex(&sh + 1, a.max_active);
 
   const int warp = __shfl_sync(kFullMask, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   pdl_launch_dependents();
@@ -552,7 +562,11 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
         int nb = 0;
         if (u < na) {
           const int e = a.plan.active[u];
-          nb = (a.plan.offsets[e + 1] - a.plan.offsets[e] + kN - 1) / kN;
+          const int beg = a.plan.offsets[e], end = a.plan.offsets[e + 1];
+          nb = (end - beg + kN - 1) / kN;
+          ex.id[u] = e;
+          ex.first[u] = beg;
+          if (u == na - 1) ex.first[na] = end;       // the lists have no gaps
         }
         int incl = nb;
 #pragma unroll
@@ -560,11 +574,11 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
           const int v = __shfl_up_sync(kFullMask, incl, off);
           if (lane >= off) incl += v;
         }
-        if (u < na) prefix[u] = run + incl - nb;
+        if (u < na) ex.blocks[u] = run + incl - nb;
         run += __shfl_sync(kFullMask, incl, 31);
       }
       if (lane == 0) {
-        prefix[na] = run;
+        ex.blocks[na] = run;
         sh.num_active = na;
         sh.num_units = run * ((a.mtiles + S::kCluster - 1) / S::kCluster) * a.splits;
       }
@@ -589,7 +603,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     for (int idx = blockIdx.x / S::kCluster;; idx += gridDim.x / S::kCluster) {
       Unit w;
       w.e = -1;
-      if (idx < num_units) w = unit_at<kN, kRouted>(a, prefix, num_active, idx, rank);
+      if (idx < num_units) w = unit_at<kN, kRouted>(a, ex, num_active, idx, rank);
       if (w.e >= 0 && w.ntok <= 0) continue;
       int t = 0;
       if (kGather && w.e >= 0)                  // past the block its last token
@@ -901,7 +915,7 @@ int num_sms() {
 template <int kN>
 size_t smem_bytes(int stages, int max_active) {
   return 1024 + (size_t)stages * Shape<kN>::kStage + sizeof(MxShared<kMxNarrow>) +
-         ((size_t)max_active + 1) * sizeof(int);
+         list_bytes(max_active);
 }
 
 template <int kN>

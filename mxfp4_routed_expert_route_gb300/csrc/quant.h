@@ -30,7 +30,7 @@ cudaError_t launch_dequantize(const uint8_t* packed, const uint8_t* scales, int6
                               int64_t I, void* out, int dtype, cudaStream_t stream);
 
 // Products of MXFP4 tokens and MXFP4 weights (gemm_mx.cu). Experts with tokens
-// that one call may have (their blocks' prefix is kept in shared memory).
+// that one call may have (their lists are kept in shared memory).
 constexpr int64_t kMxMaxActive = 4096;
 
 struct MxGemm {
