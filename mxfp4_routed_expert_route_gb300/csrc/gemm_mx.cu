@@ -981,66 +981,80 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
 
 namespace {
 
-// The shape of a call's units.
-struct Plan {
-  bool wide;            // blocks of up to kMxWide tokens, else kMxNarrow
-  int splits;
-  int64_t blocks;       // dense: blocks of tokens; routed: at most this many
-};
-Plan plan_of(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
-  Plan p;
-  const int64_t active = routed ? std::min(E, T * K) : 1;
-  // Wide blocks where experts (or the dense call) average more tokens than
-  // half a narrow block holds; a batch of up to 32 tokens has no wider block.
-  p.wide = T > kMxNarrow && T * K > 16 * active;
-  const int64_t n = p.wide ? kMxWide : kMxNarrow;
-  const int64_t mtiles = (O + kBM - 1) / kBM, nk = (I + kBK - 1) / kBK;
-  const int64_t few = routed ? active : (T + n - 1) / n;
-  p.splits = (int)std::max<int64_t>(
-      1, std::min(std::min<int64_t>(304 / (few * mtiles), nk / 2), (int64_t)8));
-  // Each expert's last block may be short.
-  p.blocks = routed ? active + T * K / n : few;
-  if (!routed) {
-    // As many blocks as fill whole rounds of the SMs best, by the width of a
-    // round's blocks (in 16 tokens, plus 2 for what a unit costs besides).
-    const int64_t pair = p.wide ? Shape<kMxWide>::kCluster : 1;
-    const int64_t sms = 152 / pair, tiles = (mtiles + pair - 1) / pair;
-    int64_t best = INT64_MAX;
-    for (int64_t b = few; b <= few + few / 4 + 1; ++b) {
-      const int64_t rounds = (b * tiles * p.splits + sms - 1) / sms;
-      const int64_t cost = rounds * (((T + b - 1) / b + 15) / 16 + 2);
-      if (cost < best) {
-        best = cost;
-        p.blocks = b;
-      }
-    }
-    // Equal blocks of 16 may need fewer than that.
-    const int64_t size = ((T + p.blocks - 1) / p.blocks + 15) / 16 * 16;
-    p.blocks = (T + size - 1) / size;
-  }
-  return p;
+// What units of this shape take, in quarters of a narrow stage (a quarter is
+// about 0.07 us). A round of units takes every SM (or pair of SMs) one unit: a
+// stage, narrow or wide with its MMAs' share of the width, and about a stage for
+// the unit itself. Splits of K are written, read and joined, 4 bytes a result
+// and split at some 3 MB a stage each way, by one launch more when dense.
+int64_t plan_cost(bool wide, int64_t blocks, int64_t width, int64_t mtiles, int64_t nk,
+                  int64_t splits, int64_t results, bool routed) {
+  const int64_t pair = wide ? Shape<kMxWide>::kCluster : 1, sms = 152 / pair;
+  const int64_t units = blocks * ((mtiles + pair - 1) / pair) * splits;
+  const int64_t rounds = (units + sms - 1) / sms;
+  const int64_t stage = wide ? 4 + width / 96 : 4;
+  int64_t cost = rounds * ((nk + splits - 1) / splits * stage + 4);
+  if (splits > 1) cost += (routed ? 0 : 24) + results * splits / 100000;
+  return cost;
 }
 
 int64_t scale_pitch(int64_t I) { return (I / 32 + 15) / 16 * 16; }
 
 }  // namespace
 
-int gemm_mx_splits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
-  return plan_of(T, E, I, O, K, routed).splits;
-}
-
-size_t gemm_mx_grouped_bytes(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
-  if (!plan_of(T, E, I, O, K, true).wide) return 0;
-  return (size_t)T * K * (size_t)(I / 2 + scale_pitch(I));
-}
-
-bool gemm_mx_supported(int64_t T, int64_t E, int64_t K) {
-  return std::min(E, T * K) <= kMxMaxActive;
+MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
+  const int64_t mtiles = (O + kBM - 1) / kBM, nk = (I + kBK - 1) / kBK;
+  const int64_t most_splits = std::max<int64_t>(1, std::min<int64_t>(nk / 2, 8));
+  MxPlan best = {false, 1, 1, 0, 0};
+  int64_t least = INT64_MAX;
+  // Splits are for calls of few units.
+  auto splits_for = [&](int64_t units) { return units > 4 * 152 ? 1 : most_splits; };
+  if (routed) {
+    // Wide blocks where experts average more tokens than half a narrow block
+    // holds (32 experts of 2880 x 2880, 8 / 16 / 32 tokens each: narrow 38, 44,
+    // 61 us, wide 41, 44, 51); a batch of up to 32 tokens has no wider block.
+    const int64_t active = std::min(E, T * K);
+    best.wide = T > kMxNarrow && T * K > 16 * active;
+    const int64_t n = best.wide ? kMxWide : kMxNarrow;
+    const int64_t width = std::min(n, (T * K + active - 1) / active);
+    // Each expert's last block may be short.
+    best.blocks = active + T * K / n;
+    for (int64_t s = 1; s <= splits_for(active * mtiles); ++s) {
+      const int64_t cost = plan_cost(best.wide, active, width, mtiles, nk, s, T * K * O, true);
+      if (cost < least) {
+        least = cost;
+        best.splits = (int)s;
+      }
+    }
+    if (best.wide) best.grouped_bytes = (size_t)T * K * (size_t)(I / 2 + scale_pitch(I));
+  } else {
+    // Up to 512 tokens either form (2880 x 5760: narrow blocks up to 256 tokens,
+    // 9 to 12 us against 15 to 30 in wide ones; 7168 x 16384: wide from 64 on).
+    for (int wide = T <= 512 ? 0 : 1; wide < 2; ++wide) {
+      const int64_t n = wide ? kMxWide : kMxNarrow, few = (T + n - 1) / n;
+      // More blocks than needed may fill whole rounds of the SMs better.
+      for (int64_t b = few; b <= few + std::min<int64_t>(few / 4 + 1, 12); ++b) {
+        const int64_t width = ((T + b - 1) / b + 15) / 16 * 16;
+        const int64_t blocks = (T + width - 1) / width;   // equal ones, multiples of 16 tokens
+        for (int64_t s = 1; s <= splits_for(blocks * mtiles); ++s) {
+          const int64_t cost = plan_cost(wide != 0, blocks, width, mtiles, nk, s, T * O, false);
+          if (cost < least) {
+            least = cost;
+            best.wide = wide != 0;
+            best.splits = (int)s;
+            best.blocks = blocks;
+          }
+        }
+      }
+    }
+  }
+  const int64_t pair = best.wide ? Shape<kMxWide>::kCluster : 1;
+  best.units = best.blocks * ((mtiles + pair - 1) / pair) * best.splits;
+  return best;
 }
 
 cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   const bool routed = g.plan != nullptr;
-  const Plan plan = plan_of(g.T, g.E, g.I, g.O, g.K, routed);
+  const MxPlan& plan = g.shape;
   const bool wide = plan.wide, grouped = routed && wide;
   const int64_t G = g.I / 32, P = g.T * g.K;
   const uint8_t *rows = g.x_packed, *scales = g.x_scales;
@@ -1082,7 +1096,7 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   a.w_scales = g.w_scales;
   a.x_scales = scales;
   a.x_pitch = (int)pitch;
-  a.out = g.splits > 1 || routed ? static_cast<void*>(g.part) : g.out;
+  a.out = plan.splits > 1 || routed ? static_cast<void*>(g.part) : g.out;
   a.status = device_status_words();
   if (a.status == nullptr) return cudaErrorUnknown;
   a.T = (int)g.T;
@@ -1090,30 +1104,27 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   a.G = (int)G;
   a.K = (int)g.K;
   a.mtiles = (int)((g.O + kBM - 1) / kBM);
-  a.splits = g.splits;
+  a.splits = plan.splits;
   a.blocks = (int)plan.blocks;
   a.max_active = routed ? (int)std::min(g.E, P) : 0;
-  const int64_t pair = wide ? Shape<kMxWide>::kCluster : 1;
-  const int64_t units = plan.blocks * ((a.mtiles + pair - 1) / pair) * a.splits;
-  if (units > 0x7fffffff) return cudaErrorInvalidValue;
   cudaError_t err;
   if (routed)
-    err = wide ? launch_typed<kMxWide, float, true>(maps, a, units, stream)
-               : launch_typed<kMxNarrow, float, true>(maps, a, units, stream);
-  else if (g.splits > 1 || g.out_dtype == kTokenF32)
-    err = wide ? launch_typed<kMxWide, float, false>(maps, a, units, stream)
-               : launch_typed<kMxNarrow, float, false>(maps, a, units, stream);
+    err = wide ? launch_typed<kMxWide, float, true>(maps, a, plan.units, stream)
+               : launch_typed<kMxNarrow, float, true>(maps, a, plan.units, stream);
+  else if (plan.splits > 1 || g.out_dtype == kTokenF32)
+    err = wide ? launch_typed<kMxWide, float, false>(maps, a, plan.units, stream)
+               : launch_typed<kMxNarrow, float, false>(maps, a, plan.units, stream);
   else
-    err = wide ? launch_typed<kMxWide, __nv_bfloat16, false>(maps, a, units, stream)
-               : launch_typed<kMxNarrow, __nv_bfloat16, false>(maps, a, units, stream);
-  if (err != cudaSuccess || routed || g.splits == 1) return err;
+    err = wide ? launch_typed<kMxWide, __nv_bfloat16, false>(maps, a, plan.units, stream)
+               : launch_typed<kMxNarrow, __nv_bfloat16, false>(maps, a, plan.units, stream);
+  if (err != cudaSuccess || routed || plan.splits == 1) return err;
   const unsigned grid = (unsigned)std::min<int64_t>((g.T * g.O + 255) / 256, num_sms() * 8);
   if (g.out_dtype == kTokenF32)
     return launch_after_previous(join_splits_kernel<float>, dim3(grid), dim3(256), 0, stream,
-                                 static_cast<const float*>(g.part), g.splits, g.T, g.O,
+                                 static_cast<const float*>(g.part), plan.splits, g.T, g.O,
                                  static_cast<float*>(g.out));
   return launch_after_previous(join_splits_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, stream,
-                               static_cast<const float*>(g.part), g.splits, g.T, g.O,
+                               static_cast<const float*>(g.part), plan.splits, g.T, g.O,
                                static_cast<__nv_bfloat16*>(g.out));
 }
 

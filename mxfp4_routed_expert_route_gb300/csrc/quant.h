@@ -33,21 +33,28 @@ cudaError_t launch_dequantize(const uint8_t* packed, const uint8_t* scales, int6
 // that one call may have (their lists are kept in shared memory).
 constexpr int64_t kMxMaxActive = 4096;
 
+// The shape of a call's units of work.
+struct MxPlan {
+  bool wide;              // blocks of up to 192 tokens, else 32
+  int splits;             // units that share K
+  int64_t blocks;         // dense: blocks of tokens; routed: at most this many
+  int64_t units;          // blocks x 128-row tiles (pairs of them when wide) x splits
+  size_t grouped_bytes;   // routed: the token rows in the lists' order (0: the kernel
+                          // gathers them itself)
+};
+MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed);
+
 struct MxGemm {
   const uint8_t *x_packed, *x_scales;   // [T][I/2], [T][I/32]
   const uint8_t *w_packed, *w_scales;   // [E][O][I/2], [E][O][I/32]
   const RoutePlan* plan;                // routing lists, or null: dense (E = 1)
   int64_t T, E, I, O, K;                // K: picks per token (routed)
-  int splits;                           // gemm_mx_splits(): units that share K
-  void* grouped;                        // gemm_mx_grouped_bytes() of scratch (routed)
+  MxPlan shape;                         // gemm_mx_plan() of these sizes
+  void* grouped;                        // shape.grouped_bytes of scratch (routed)
   float* part;                          // [pair or token][split][O] (routed, or splits > 1)
   void* out;                            // dense: [T][O] of out_dtype
   int out_dtype;
 };
-int gemm_mx_splits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed);
-// The token rows in the lists' order (0: the kernel gathers them itself).
-size_t gemm_mx_grouped_bytes(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K);
-bool gemm_mx_supported(int64_t T, int64_t E, int64_t K);
 cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream);
 
 }  // namespace mxfp4el

@@ -32,22 +32,20 @@ size_t span_bytes(int64_t rows, int64_t stride, int64_t width, size_t esize) {
   return rows == 0 ? 0 : ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * esize;
 }
 
+// Values of one expert's matrix: a tensor map's strides end before 2^40 bytes.
+constexpr int64_t kMaxMatrix = (int64_t)1 << 40;
+
 // Sizes of a product that every index in the kernels has room for.
 bool product_fits(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
   if (T > (1 << 30) || E > kMaxDim || I > kMaxDim / 2 || O > kMaxDim / 2 || K > kMaxDim)
     return false;
   if (K > 0 && T > (1 << 30) / K) return false;         // pair ids are int32
-  if (O > 0 && E > kMaxElements / I / O) return false;
+  if (O > 0 && (E > kMaxElements / I / O || O > kMaxMatrix / I)) return false;
   return O == 0 || K == 0 || T * K <= kMaxElements / O;
 }
 
-// The units of a call (gemm_mx.cu numbers them in 31 bits).
-bool units_fit(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
-  const int64_t active = routed ? (E < T * K ? E : T * K) : 1;
-  const int64_t blocks = active + T * K / 16 + 2;
-  const int64_t per = (O + 127) / 128 * gemm_mx_splits(T, E, I, O, K, routed);
-  return blocks <= kMaxDim / per;
-}
+// gemm_mx.cu numbers a call's units in 31 bits, with room for a grid past the last.
+bool units_fit(const MxPlan& p) { return p.units <= kMaxDim - (1 << 20); }
 
 constexpr size_t kAlign = 256;
 size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
@@ -57,12 +55,11 @@ struct ExpertWorkspace {
   int* wc_global;
   void* grouped;
   float* part;
-  int splits;
   size_t bytes;
 };
 
 // The scratch of a routed call; base == nullptr only sizes.
-ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
+ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t O, int64_t K, const MxPlan& p) {
   ExpertWorkspace ws = {};
   size_t off = 0;
   auto take = [&](size_t bytes) -> void* {
@@ -78,12 +75,19 @@ ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t I, int64_t O, in
   ws.plan.pair_list = static_cast<int*>(take(P * sizeof(int)));
   const size_t wc = route_global_counter_words(T, K, E, false);
   ws.wc_global = wc ? static_cast<int*>(take(wc * sizeof(int))) : nullptr;
-  ws.splits = K > 0 && E > 0 ? gemm_mx_splits(T, E, I, O, K, true) : 1;
-  const size_t grouped = K > 0 && E > 0 ? gemm_mx_grouped_bytes(T, E, I, O, K) : 0;
-  ws.grouped = grouped ? take(grouped) : nullptr;
-  ws.part = static_cast<float*>(take(P * ws.splits * (size_t)O * sizeof(float)));
+  ws.grouped = p.grouped_bytes ? take(p.grouped_bytes) : nullptr;
+  ws.part = static_cast<float*>(take(P * p.splits * (size_t)O * sizeof(float)));
   ws.bytes = off;
   return ws;
+}
+
+// The units of a routed call; none without pairs or experts.
+MxPlan routed_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
+  return K > 0 && E > 0 ? gemm_mx_plan(T, E, I, O, K, true) : MxPlan{false, 1, 0, 0, 0};
+}
+
+size_t linear_workspace(const MxPlan& p, int64_t T, int64_t O) {
+  return p.splits > 1 ? align_up((size_t)T * O * p.splits * sizeof(float)) : 0;
 }
 
 int status_of(cudaError_t err) { return err == cudaSuccess ? MXFP4EL_OK : MXFP4EL_ERR_CUDA; }
@@ -176,8 +180,7 @@ extern "C" int mxfp4_dequantize(const uint8_t* packed, const uint8_t* scales, in
 extern "C" size_t mxfp4_linear_workspace_size(int64_t T, int64_t I, int64_t O) {
   if (T < 0 || O < 0 || I <= 0 || I % 32 != 0 || !product_fits(T, 1, I, O, 1)) return (size_t)-1;
   if (T == 0 || O == 0) return 0;
-  const int splits = gemm_mx_splits(T, 1, I, O, 1, false);
-  return splits > 1 ? align_up((size_t)T * O * splits * sizeof(float)) : 0;
+  return linear_workspace(gemm_mx_plan(T, 1, I, O, 1, false), T, O);
 }
 
 extern "C" int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales,
@@ -188,14 +191,15 @@ extern "C" int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales,
   if (T < 0 || O < 0 || I <= 0 || I % 32 != 0) return MXFP4EL_ERR_INVALID_ARGUMENT;
   if (!product_fits(T, 1, I, O, 1)) return MXFP4EL_ERR_TOO_LARGE;
   if (T == 0 || O == 0) return MXFP4EL_OK;
-  if (!units_fit(T, 1, I, O, 1, false)) return MXFP4EL_ERR_TOO_LARGE;
+  const MxPlan plan = gemm_mx_plan(T, 1, I, O, 1, false);
+  if (!units_fit(plan)) return MXFP4EL_ERR_TOO_LARGE;
   const size_t es = size_of(out_dtype), G = (size_t)I / 32;
   if (x_packed == nullptr || x_scales == nullptr || packed_weights == nullptr ||
       scale_bytes == nullptr || out == nullptr || !aligned(x_packed, 16) ||
       !aligned(packed_weights, 16) || !aligned(out, es))
     return MXFP4EL_ERR_INVALID_ARGUMENT;
   const size_t no = (size_t)T * O * es;
-  const size_t nw = mxfp4_linear_workspace_size(T, I, O);
+  const size_t nw = linear_workspace(plan, T, O);
   const void* inputs[] = {x_packed, x_scales, packed_weights, scale_bytes};
   const size_t sizes[] = {T * G * 16, T * G, O * G * 16, O * G};
   for (int i = 0; i < 4; ++i)
@@ -217,7 +221,7 @@ extern "C" int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales,
   g.I = I;
   g.O = O;
   g.K = 1;
-  g.splits = gemm_mx_splits(T, 1, I, O, 1, false);
+  g.shape = plan;
   g.part = static_cast<float*>(workspace);
   g.out = out;
   g.out_dtype = out_dtype;
@@ -229,7 +233,7 @@ extern "C" size_t mxfp4_expert_linear_quantized_workspace_size(int64_t T, int64_
   if (T < 0 || E < 0 || O < 0 || K < 0 || I <= 0 || I % 32 != 0 || !product_fits(T, E, I, O, K))
     return (size_t)-1;
   if (T == 0 || O == 0) return 0;
-  return carve(nullptr, T, E, I, O, K).bytes;
+  return carve(nullptr, T, E, O, K, routed_plan(T, E, I, O, K)).bytes;
 }
 
 extern "C" int mxfp4_expert_linear_quantized(
@@ -245,7 +249,8 @@ extern "C" int mxfp4_expert_linear_quantized(
   if (!product_fits(T, E, I, O, K)) return MXFP4EL_ERR_TOO_LARGE;
   if (T == 0 || O == 0) return MXFP4EL_OK;
   const bool product = K > 0 && E > 0;
-  if (product && (!gemm_mx_supported(T, E, K) || !units_fit(T, E, I, O, K, true)))
+  const MxPlan plan = routed_plan(T, E, I, O, K);
+  if (product && ((E < T * K ? E : T * K) > kMxMaxActive || !units_fit(plan)))
     return MXFP4EL_ERR_TOO_LARGE;
   const size_t es = size_of(dtype), is = index_dtype == MXFP4EL_INDEX_I64 ? 8 : 4;
   const size_t G = (size_t)I / 32;
@@ -260,7 +265,7 @@ extern "C" int mxfp4_expert_linear_quantized(
                   !aligned(packed_weights, 16)))
     return MXFP4EL_ERR_INVALID_ARGUMENT;
   const size_t no = (size_t)T * O * es;
-  const size_t nw = carve(nullptr, T, E, I, O, K).bytes;
+  const size_t nw = carve(nullptr, T, E, O, K, plan).bytes;
   const void* inputs[] = {x_packed,         x_scales,        packed_weights, scale_bytes,
                           selected_experts, mixture_weights, shared_output};
   const size_t sizes[] = {T * G * 16,         T * G,  (size_t)E * O * G * 16, (size_t)E * O * G,
@@ -272,7 +277,7 @@ extern "C" int mxfp4_expert_linear_quantized(
   if (overlaps(workspace, nw, out, no)) return MXFP4EL_ERR_ALIAS;
   for (int i = 0; i < 7; ++i)
     if (overlaps(workspace, nw, inputs[i], sizes[i])) return MXFP4EL_ERR_ALIAS;
-  const ExpertWorkspace ws = carve(workspace, T, E, I, O, K);
+  const ExpertWorkspace ws = carve(workspace, T, E, O, K, plan);
   const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (K > 0) {
     // With E == 0 every id is out of range: the bucketer counts them.
@@ -292,12 +297,12 @@ extern "C" int mxfp4_expert_linear_quantized(
       g.I = I;
       g.O = O;
       g.K = K;
-      g.splits = ws.splits;
+      g.shape = plan;
       g.grouped = ws.grouped;
       g.part = ws.part;
       if (launch_gemm_mx(g, stream) != cudaSuccess) return MXFP4EL_ERR_CUDA;
     }
   }
   return status_of(launch_combine(shared_output, selected_experts, index_dtype, mixture_weights,
-                                  ws.part, ws.splits, out, dtype, T, E, O, K, product, stream));
+                                  ws.part, plan.splits, out, dtype, T, E, O, K, product, stream));
 }

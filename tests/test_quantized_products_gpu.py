@@ -194,6 +194,43 @@ def test_experts_the_same_id_twice_and_ids_out_of_range(T):
     assert lib.device_errors() == bad
 
 
+@pytest.mark.parametrize("T,E,K,I,O", [(4100, 4000, 1, 64, 40), (3000, 3500, 2, 32, 20),
+                                       (50000, 2500, 1, 32, 136)])
+def test_experts_long_lists(T, E, K, I, O):
+    """Thousands of experts with tokens, narrow and wide blocks: the kernel's
+    lists take shared memory from its ring of stages."""
+    x, w, sel, p, ys = make_routed(T, E, K, I, O, F32, seed=1,
+                                   picks=[[(t * 7 + k * 3) % E for k in range(K)] for t in range(T)])
+    got = lib.mxfp4_expert_linear_quantized(*x, *w, sel, p, ys)
+    vx, vw = ref.values(*x), ref.values(*w)
+    want, bound = ys.double(), (K + 1) * 2.0 ** -24 * ys.double().abs()
+    for k in range(K):
+        m = vw[sel[:, k].long()]
+        y = (m @ vx[:, :, None])[..., 0] * p[:, k:k + 1].double()
+        want = want + y
+        terms = (m.abs() @ vx.abs()[:, :, None])[..., 0] * p[:, k:k + 1].double()
+        bound = bound + (I / 64 + 5) * 2.0 ** -22 * terms + (K + 1) * 2.0 ** -24 * y.abs()
+    check(got, want, bound, F32)
+    assert lib.wait_timeouts() == 0 and lib.device_errors() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    x1, w1, sel1, p1, ys1 = make_routed(300, 6, 2, 288, 130, F32, seed=1)
+    x2, w2 = rows(500, 2880, seed=2), rows(1500, 2880, seed=3)
+    want1 = lib.mxfp4_expert_linear_quantized(*x1, *w1, sel1, p1, ys1)
+    want2 = lib.mxfp4_linear(*x2, *w2, dtype=F32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got1, got2 = [], []
+    for _ in range(10):
+        with torch.cuda.stream(streams[0]):
+            got1.append(lib.mxfp4_expert_linear_quantized(*x1, *w1, sel1, p1, ys1))
+        with torch.cuda.stream(streams[1]):
+            got2.append(lib.mxfp4_linear(*x2, *w2, dtype=F32))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want1) for g in got1) and all(torch.equal(g, want2) for g in got2)
+
+
 def test_experts_nothing_to_add():
     x, w, sel, p, ys = make_routed(5, 4, 2, 64, 70, BF16)
     none = torch.empty(5, 0, device="cuda")
