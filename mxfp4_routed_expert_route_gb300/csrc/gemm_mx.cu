@@ -82,7 +82,6 @@ constexpr uint32_t kRowBytes = kBK / 2;        // codes of a row per stage
 constexpr uint32_t kStageA = kBM * kRowBytes;
 constexpr uint32_t kSfBlock = 512;             // 128 rows' scales of four groups
 constexpr int kSfPerStage = kGroupsPerStage / 4;
-constexpr int kMaxStages = 12;
 constexpr int kMxNarrow = 32, kMxWide = 192;   // tokens of a block, at most
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitWarp = 3, kScaleWarp0 = 8, kEpiWarp0 = 4, kEpiWarps = 4;
@@ -103,6 +102,9 @@ struct Shape {
   // Scale warps: narrow blocks two teams of a weights' and a tokens' warp, wide
   // ones a team of one warp for the weights and two for the tokens (128, 64 rows).
   static constexpr int kCluster = kN == kMxWide ? 2 : 1;
+  // More stages would fit, and do not help: what they leave of the SM's memory
+  // caches the scale bytes (8192 x 7168 x 4096: 5 stages 104 us, 4 stages 98).
+  static constexpr int kStages = kN == kMxNarrow ? 8 : 4;
   static constexpr int kTeams = 2;
   static constexpr int kChunk = 2;                         // stages whose scales one read brings
   static constexpr int kTeamWarps = kN == kMxNarrow ? 2 : 3;
@@ -152,7 +154,7 @@ constexpr size_t list_bytes(int max_active) { return (3 * (size_t)max_active + 2
 
 template <int kRows>
 struct __align__(16) MxShared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[8], empty[8];
   uint64_t d_full[2], d_empty[2];
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
@@ -920,7 +922,7 @@ size_t smem_bytes(int stages, int max_active) {
 
 template <int kN>
 int stages_for(int max_active) {
-  int s = std::min(kMaxStages, Shape<kN>::kTmemStages);
+  int s = std::min(Shape<kN>::kStages, Shape<kN>::kTmemStages);
   while (s > 0 && smem_bytes<kN>(s, max_active) > kSmemLimit) --s;
   return s;
 }
