@@ -17,10 +17,10 @@
 // and float32 results go to part[pair][split][o]. Narrow blocks (kN = 32)
 // gather their token rows with the copies themselves (four rows each,
 // tile::gather4); wide ones read a copy of the rows in the lists' order, since
-// gathers issue one at a time (some 75 cycles each: the skewed prefill's
-// product took 4.04 ms with them, 1.54 without the tokens). Dense: a block is
+// gathers issue one at a time (some 75 cycles each; with them the skewed
+// prefill's product took 4.0 ms, without the tokens 1.5). Dense: a block is
 // consecutive tokens and results go to out[t][o], or to part[t][split][o] where
-// K is split over several units.
+// K is split over several units (gemm_mx_plan).
 //
 // Scale bytes. The tensor core wants them in tensor memory, 32 lanes by 4
 // bytes of 128 rows' scales for four groups (512 bytes, row r at 16 (r % 32) +
@@ -28,38 +28,51 @@
 // for the four lane quarters. In memory they are rows of I/32 bytes on no
 // particular alignment, so a few warps read them with ordinary loads and store
 // the blocks, lane l the rows l, l + 32, ..., whose words lie together in the
-// block. A warp takes four stages at a time (32 bytes of a row) and has the next
-// four's loads under way while it stores these: with two stages at a time the
-// loads' latency bounded the product (decode: 65 us against 55 without the
-// loads). Narrow blocks have two teams of warps that take four stages in turn.
-// From a team's last stage to its next it is then five, and the ring has more
-// (from one further on than the ring is long a warp could not tell a stage's
-// phases apart, and would store into one still in use).
+// block. A warp takes two stages at a time (16 bytes of a row) and has its next
+// two stages' loads under way while it stores these. Two teams of warps take two
+// stages in turn. From a team's last stage to its next it is then three, and the
+// ring has more (from one further on than the ring is long a warp could not
+// tell a stage's phases apart, and would store into one still in use).
 //
 // K that is no multiple of 256: the copies fill codes past a row's end with
 // zeros, and scale bytes past it are set to 0, so what is added is exactly 0;
 // MMAs wholly past the end are not issued.
 //
-// Warp roles in a CTA of 12 warps (one CTA per SM, persistent over units
-// (block, 128-row tile, K split)):
+// Wide blocks: two CTAs, on neighbouring SMs, take two tiles of one block at a
+// time, and each loads half of the token rows of every stage for both
+// (multicast). Alone, an SM reads 40 KB of codes per stage from L2, which
+// then bounds the dense product (15 TB/s). A stage's slot is free when the MMAs
+// of both CTAs are done with it.
+//
+// Warp roles in a CTA of 14 warps (one CTA per SM, persistent over units
+// (block, 128-row tile or pair of tiles, K split)):
 //   warp 0      copies of codes (weights and tokens), one elected lane; TMEM
 //   warp 1      scale copies to tensor memory and MMAs, one elected lane
 //   warp 2      lists of the experts with tokens at start (routed)
 //   warp 3      the units: finds each next one and hands it to the other roles
-//               through a ring in shared memory, ahead of them (finding one
-//               takes several dependent loads)
-//   warps 4-7   scale bytes
-//   warps 8-11  epilogue: tensor memory -> float32 or bf16 results
-// Wide blocks: two CTAs, on neighbouring SMs, take two tiles of one block at a
-// time, and each loads half of the token rows of every stage for both
-// (multicast). Alone, an SM reads 40 KB of codes per stage from L2, which
-// then bounds the dense product (15 TB/s; 111 us against 9x for 8192 x 7168 x
-// 4096). A stage's slot is free when the MMAs of both CTAs are done with it.
-//
+//               through a ring in shared memory, ahead of them
+//   warps 4-7   epilogue: tensor memory -> float32 or bf16 results
+//   warps 8-13  scale bytes (8-11 for narrow blocks)
 // Two accumulators, so the epilogue of a unit runs beside the next unit's
 // MMAs. Every wait is bounded; a role whose wait gives up records it and
 // stops, and the CTA waits (bounded) for its own copies and MMAs before
 // freeing TMEM.
+//
+// What bounds it, on one GB300. Few tokens: the weights' bytes (16 tokens over
+// 384 experts of 7168 x 4096, 1.71 GB: 277 us, 6.2 TB/s, 93 % of a plain copy;
+// 8 tokens over 128 experts of 2880 x 5760, 253 MB: 53 us with routing and
+// combine, of which some 8 us are the chain ids -> lists -> units -> first
+// copies). Many: dense 8192 x 7168 x 4096 in 95 us, 5.1 PFLOP/s; the tensor pipe
+// is active 54 % of the time, and the scale copies, which it runs in turn with
+// the MMAs, take a third as long again (six of about 28 cycles beside four MMAs
+// of 88 a stage); with neither copies nor scales the MMAs alone take 82 us. The
+// skewed prefill (8192 tokens, 8 of 384 experts) takes 1.55 ms here, 7.3 GB
+// of weights, rows and float32 results at 4.8 TB/s.
+// Measured on the way (dense 8192 x 7168 x 4096): copies and MMAs from loops of
+// one thread 114 us, from uniform warps 108 (the operands of copies and tcgen05
+// otherwise have to be made uniform at every issue); scales in two teams'
+// stages with the token rows read by each CTA alone 116, by the pair 102; four
+// stages instead of five 98; a third read of scales under way 115.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -85,7 +98,8 @@ constexpr int kSfPerStage = kGroupsPerStage / 4;
 constexpr int kMxNarrow = 32, kMxWide = 192;   // tokens of a block, at most
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitWarp = 3, kScaleWarp0 = 8, kEpiWarp0 = 4, kEpiWarps = 4;
-constexpr int kUnitRing = 8;
+constexpr int kUnitRing = 8;                   // a scale warp looks a few short units ahead
+constexpr int kRingMax = 8;                    // stages, at most
 constexpr size_t kSmemLimit = 227 * 1024;
 
 template <int kN>
@@ -99,14 +113,14 @@ struct Shape {
   static constexpr uint32_t kSfColsA = kSfPerStage * 4, kSfColsB = kSfPerStage * kBRowBlocks * 4;
   static constexpr uint32_t kSfCol = 2 * kN;
   static constexpr int kTmemStages = (int)((kTmemCols - kSfCol) / (kSfColsA + kSfColsB));
-  // Scale warps: narrow blocks two teams of a weights' and a tokens' warp, wide
-  // ones a team of one warp for the weights and two for the tokens (128, 64 rows).
   static constexpr int kCluster = kN == kMxWide ? 2 : 1;
   // More stages would fit, and do not help: what they leave of the SM's memory
   // caches the scale bytes (8192 x 7168 x 4096: 5 stages 104 us, 4 stages 98).
   static constexpr int kStages = kN == kMxNarrow ? 8 : 4;
+  // Scale warps: two teams of one warp for the weights' rows and one for the
+  // tokens', or two (128 and 64 rows) when wide.
   static constexpr int kTeams = 2;
-  static constexpr int kChunk = 2;                         // stages whose scales one read brings
+  static constexpr int kChunk = 2;               // stages whose scales one read brings
   static constexpr int kTeamWarps = kN == kMxNarrow ? 2 : 3;
   static constexpr int kUnitReaders = 2 + kTeams * kTeamWarps + kEpiWarps;
   static constexpr int kMinStages = (kTeams - 1) * kChunk + 2;
@@ -154,7 +168,7 @@ constexpr size_t list_bytes(int max_active) { return (3 * (size_t)max_active + 2
 
 template <int kRows>
 struct __align__(16) MxShared {
-  uint64_t full[8], empty[8];
+  uint64_t full[kRingMax], empty[kRingMax];
   uint64_t d_full[2], d_empty[2];
   uint64_t u_full[kUnitRing], u_empty[kUnitRing];
   uint64_t drain;
@@ -390,7 +404,7 @@ __device__ __forceinline__ void release_unit(MxShared<kRows>& sh, RingPos& pu) {
   pu.next(kUnitRing);
 }
 
-// Stages four at a time, in the order of the units, dealt to kTeams teams in
+// Stages kChunk at a time, in the order of the units, dealt to kTeams teams in
 // turn: next() moves to this team's next ones. Lane l has the rows row0 + l + 32 i
 // of the tile (kTokens: of the block), i < kRows.
 template <int kRows, int kTeams, int kChunk, bool kTokens, bool kGather>

@@ -13,8 +13,9 @@
 // Both directions only move bytes. A warp takes 1024 values at a time, eight
 // per lane four times over, so that four loads per lane are in flight (one at a
 // time, with a division for the row of every eight values: 37 us for 8192 x 7168
-// bf16, against 22 us for its 149 MB at the rate of a copy); the 32 scale bytes
-// of a task are stored together.
+// bf16); the 32 scale bytes of a task are stored together. 8192 x 7168 bf16, from
+// DRAM: 29 us, and 25 us back, against 22 us for the 149 MB of each at the rate
+// of a copy.
 #include <algorithm>
 
 #include "common.cuh"

@@ -15,9 +15,10 @@
 // integers. The (K+1)-th largest of the 32 lanes' maxima is at most the
 // (K+1)-th largest choice, so the choices from there up are candidates, a few
 // more than K; they are gathered to one lane each and ranked by counting.
-// 32768 x 384 with a bias: 30 us against 7.8 us for reading the logits, 690
-// instructions a token at 70 % of the issue rate (K rounds of a warp-wide
-// maximum over all E: 48 us).
+// 32768 x 384 with a bias: 28 to 30 us against 7.8 us for reading the logits,
+// 690 instructions a token at 70 % of the issue rate (38 us and 840 with both
+// kinds of score in one kernel, 48 us and 1120 with a NaN check per expert
+// besides).
 #include <algorithm>
 
 #include "common.cuh"
