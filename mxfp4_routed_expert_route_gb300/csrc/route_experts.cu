@@ -216,7 +216,9 @@ __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float
   const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? order_key(v) : 0u);
   if (hi != 0u && kept != 0u) {
     const float a_lo = key_value(lo), a_hi = key_value(hi);
-    *sure = err == 0.f || a_lo - a_hi > 4.f * err + (fabsf(a_lo) + fabsf(a_hi)) * 0x1p-22f;
+    // (Experts may be kept out by a bias of -infinity.)
+    *sure = err == 0.f || (a_hi == -INFINITY && a_lo > -INFINITY) ||
+            a_lo - a_hi > 4.f * err + (fabsf(a_lo) + fabsf(a_hi)) * 0x1p-22f;
   }
   return kept;
 }

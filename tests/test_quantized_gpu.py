@@ -203,6 +203,20 @@ def test_route_what_is_not_finite(score, groups):
             assert not p.isnan().any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_experts_kept_out_by_the_bias(score):
+    logits = normal(200, 64, seed=6)
+    bias = normal(64, seed=7, by=0.05)
+    bias[8:24] = -math.inf                     # two groups of eight
+    bias[40] = -math.inf
+    for top in (3, 6):
+        sel, p = lib.route_experts(logits, 8, score=score, bias=bias, groups=8, top_groups=top)
+        check_routed(logits, 8, sel, p, score=score, bias=bias, groups=8, top_groups=top)
+        assert not ((sel >= 8) & (sel < 24)).any() and not (sel == 40).any()
+    sel, p = lib.route_experts(logits, 8, score=score, bias=bias)
+    check_routed(logits, 8, sel, p, score=score, bias=bias)
+
+
 def test_route_rows_of_a_wider_matrix_and_given_outputs():
     wide = normal(21, 70, seed=1, dtype=BF16)
     logits = wide[:, 3:67]
