@@ -115,6 +115,9 @@ int mxfp4_linear(const uint8_t* x_packed, const uint8_t* x_scales, const uint8_t
  * slot order in float32 and rounded once. An expert id out of range
  * contributes nothing and is counted for mxfp4el_device_errors(). At most
  * 4096 experts may have tokens: min(E, T * K) <= 4096.
+ *
+ * workspace: mxfp4_expert_linear_quantized_workspace_size() bytes on a
+ * 256-byte boundary, as in mxfp4_linear.
  */
 size_t mxfp4_expert_linear_quantized_workspace_size(int64_t T, int64_t E, int64_t I, int64_t O,
                                                     int64_t K);

@@ -48,7 +48,10 @@
 // (block, 128-row tile or pair of tiles, K split)):
 //   warp 0      copies of codes (weights and tokens), one elected lane; TMEM
 //   warp 1      scale copies to tensor memory and MMAs, one elected lane
-//   warp 2      lists of the experts with tokens at start (routed)
+//   warp 2      lists of the experts with tokens at start (routed; for up to 256
+//               pairs all warps have made the routing lists before, which saves
+//               route.cu's launch: 16 tokens over 384 experts 281 -> 268 us, 8 over
+//               128 57 -> 55 us, a call among others)
 //   warp 3      the units: finds each next one and hands it to the other roles
 //               through a ring in shared memory, ahead of them
 //   warps 4-7   epilogue: tensor memory -> float32 or bf16 results
@@ -59,10 +62,10 @@
 // freeing TMEM.
 //
 // What bounds it, on one GB300. Few tokens: the weights' bytes (16 tokens over
-// 384 experts of 7168 x 4096, 1.71 GB: 277 us, 6.2 TB/s, 93 % of a plain copy;
-// 8 tokens over 128 experts of 2880 x 5760, 253 MB: 53 us with routing and
+// 384 experts of 7168 x 4096, 1.71 GB: 273 us, 6.3 TB/s, 94 % of a plain copy;
+// 8 tokens over 128 experts of 2880 x 5760, 253 MB: 54 us with lists and
 // combine, of which some 8 us are the chain ids -> lists -> units -> first
-// copies). Many: dense 8192 x 7168 x 4096 in 95 us, 5.1 PFLOP/s; the tensor pipe
+// copies). Many: dense 8192 x 7168 x 4096 in 94 us, 5.1 PFLOP/s; the tensor pipe
 // is active 54 % of the time, and the scale copies, which it runs in turn with
 // the MMAs, take a third as long again (six of about 28 cycles beside four MMAs
 // of 88 a stage); with neither copies nor scales the MMAs alone take 82 us. The
@@ -136,7 +139,9 @@ struct MxMaps {
 };
 
 struct MxKernelArgs {
-  RoutePlan plan;               // routed
+  RoutePlan plan;               // routed, unless the kernel makes its own lists:
+  const void* sel;              // the T * K ids, or null
+  int sel64, E;
   const uint8_t* w_scales;      // [E][O][G]
   const uint8_t* x_scales;      // [rows][x_pitch]
   void* out;
@@ -157,14 +162,17 @@ struct __align__(16) Unit {
 };
 
 // The experts with tokens, in shared memory: id, first position in the lists
-// and blocks before, with one entry more of the latter two for the end.
+// and blocks before, with one entry more of the latter two for the end; behind
+// them room for the kernel's own lists.
 struct ExpertLists {
-  int *blocks, *first, *id;
+  int *blocks, *first, *id, *own;
   __device__ __forceinline__ ExpertLists(void* base, int max_active)
       : blocks(static_cast<int*>(base)), first(blocks + max_active + 1),
-        id(first + max_active + 1) {}
+        id(first + max_active + 1), own(id + max_active) {}
 };
-constexpr size_t list_bytes(int max_active) { return (3 * (size_t)max_active + 2) * sizeof(int); }
+constexpr size_t list_bytes(int max_active, int own_pairs) {
+  return (3 * (size_t)max_active + 2 + 3 * (size_t)own_pairs) * sizeof(int);
+}
 
 template <int kRows>
 struct __align__(16) MxShared {
@@ -531,6 +539,49 @@ __device__ __forceinline__ bool scale_role(const MxKernelArgs& a, Sh& sh, unsign
   return walk.w.e != -2;
 }
 
+// The lists of route.cu for up to kMxOwnPairs pairs, by one block, a thread per
+// pair: its place is the number of pairs before it by (expert, pair). Ids out
+// of range are left out (and counted by block 0). Returns the experts' number;
+// ex.own: the pairs in the lists' order, then scratch.
+__device__ __forceinline__ int own_lists(const MxKernelArgs& a, const ExpertLists& ex, int P) {
+  static_assert(kMxOwnPairs <= kThreads, "a thread per pair");
+  int *list = ex.own, *key = list + P, *head = key + P;
+  const int i = (int)threadIdx.x;
+  long long e = -1;
+  if (i < P)
+    e = a.sel64 ? (long long)static_cast<const int64_t*>(a.sel)[i]
+                : (long long)static_cast<const int32_t*>(a.sel)[i];
+  const bool valid = e >= 0 && e < a.E;
+  const int k = valid ? (int)e : 0x7fffffff;           // beyond every id
+  if (i < P) key[i] = k;
+  const int total = __syncthreads_count(valid);
+  int less = 0, before = 0;
+  if (valid) {
+    for (int j = 0; j < P; ++j) {
+      const int other = key[j];
+      less += other < k;
+      before += other == k && j < i;
+    }
+    list[less + before] = i;
+  }
+  const bool first = valid && before == 0;
+  if (i < P) head[i] = first;
+  const int experts = __syncthreads_count(first);
+  if (first) {
+    int u = 0;
+    for (int j = 0; j < P; ++j) u += head[j] && key[j] < k;
+    ex.id[u] = k;
+    ex.first[u] = less;
+  }
+  if (i == 0) {
+    ex.first[experts] = total;
+    if (blockIdx.x == 0 && total < P)
+      atomicAdd(&a.status[kStatusBadPairs], (unsigned long long)(P - total));
+  }
+  __syncthreads();
+  return experts;
+}
+
 template <int kN, typename Out, bool kRouted>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
@@ -569,20 +620,34 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     }
   }
   pdl_wait();                    // the operands and the routing lists are ready
+  const bool own = kGather && a.sel != nullptr;
+  int own_experts = 0;
+  if constexpr (kGather) {
+    __syncwarp();
+    if (own) own_experts = own_lists(a, ex, a.T * a.K);
+  }
+  const int* pairs_by_expert = own ? ex.own : a.plan.pair_list;
   if (warp == 2) {
     if constexpr (kRouted) {
-      const int na = a.plan.meta[kMetaNumActive];
+      const int na = own ? own_experts : a.plan.meta[kMetaNumActive];
       int run = 0;
       for (int base = 0; base < na; base += 32) {
         const int u = base + lane;
         int nb = 0;
         if (u < na) {
-          const int e = a.plan.active[u];
-          const int beg = a.plan.offsets[e], end = a.plan.offsets[e + 1];
+          int beg, end;
+          if (own) {
+            beg = ex.first[u];
+            end = ex.first[u + 1];
+          } else {
+            const int e = a.plan.active[u];
+            beg = a.plan.offsets[e];
+            end = a.plan.offsets[e + 1];
+            ex.id[u] = e;
+            ex.first[u] = beg;
+            if (u == na - 1) ex.first[na] = end;     // the lists have no gaps
+          }
           nb = (end - beg + kN - 1) / kN;
-          ex.id[u] = e;
-          ex.first[u] = beg;
-          if (u == na - 1) ex.first[na] = end;       // the lists have no gaps
         }
         int incl = nb;
 #pragma unroll
@@ -623,7 +688,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       if (w.e >= 0 && w.ntok <= 0) continue;
       int t = 0;
       if (kGather && w.e >= 0)                  // past the block its last token
-        t = a.plan.pair_list[w.tok0 + min(lane, w.ntok - 1)] / a.K;
+        t = pairs_by_expert[w.tok0 + min(lane, w.ntok - 1)] / a.K;
       if (!wait_short(&sh.u_empty[pu.idx], pu.phase ^ 1u)) {
         ok = false;
         break;
@@ -825,7 +890,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       for (int c0 = 0; c0 < w.ntok; c0 += 32) {
         const int n = min(32, w.ntok - c0);
         int row = w.tok0 + c0 + min(lane, n - 1);
-        if constexpr (kRouted) row = a.plan.pair_list[row];
+        if constexpr (kRouted) row = pairs_by_expert[row];
         float v[32];
         tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kN + c0, v);
         tmem_wait_ld();
@@ -841,17 +906,17 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
             const bool odd = (lane & 1) != 0;
             to += (odd ? a.O : 0) + (o & ~1);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
+            for (int c = 0; c < 32; c += 2, to += 2 * (int64_t)a.O) {
               const float other = __shfl_xor_sync(kFullMask, odd ? v[c] : v[c + 1], 1);
               const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(other, v[c + 1])
                                              : __floats2bfloat162_rn(v[c], other);
               if (c + (odd ? 1 : 0) < n && o < a.O)
-                *reinterpret_cast<__nv_bfloat162*>(to + (int64_t)c * a.O) = two;
+                *reinterpret_cast<__nv_bfloat162*>(to) = two;
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c < n && o < a.O) store_out(to + (int64_t)c * a.O + o, v[c]);
+            for (int c = 0; c < 32; ++c, to += a.O)
+              if (c < n && o < a.O) store_out(to + o, v[c]);
           }
         } else {
 #pragma unroll
@@ -929,24 +994,25 @@ int num_sms() {
 }
 
 template <int kN>
-size_t smem_bytes(int stages, int max_active) {
+size_t smem_bytes(int stages, int max_active, int own_pairs) {
   return 1024 + (size_t)stages * Shape<kN>::kStage + sizeof(MxShared<kMxNarrow>) +
-         list_bytes(max_active);
+         list_bytes(max_active, own_pairs);
 }
 
 template <int kN>
-int stages_for(int max_active) {
+int stages_for(int max_active, int own_pairs) {
   int s = std::min(Shape<kN>::kStages, Shape<kN>::kTmemStages);
-  while (s > 0 && smem_bytes<kN>(s, max_active) > kSmemLimit) --s;
+  while (s > 0 && smem_bytes<kN>(s, max_active, own_pairs) > kSmemLimit) --s;
   return s;
 }
 
 template <int kN, typename Out, bool kRouted>
 cudaError_t launch_typed(const MxMaps& maps, MxKernelArgs args, int64_t units,
                          cudaStream_t stream) {
-  args.stages = stages_for<kN>(args.max_active);
+  const int own_pairs = args.sel != nullptr ? args.T * args.K : 0;
+  args.stages = stages_for<kN>(args.max_active, own_pairs);
   if (args.stages < Shape<kN>::kMinStages) return cudaErrorInvalidValue;
-  const size_t smem = smem_bytes<kN>(args.stages, args.max_active);
+  const size_t smem = smem_bytes<kN>(args.stages, args.max_active, own_pairs);
   static std::mutex mu;
   static size_t opted[64] = {};
   int dev = 0;
@@ -1020,7 +1086,7 @@ int64_t scale_pitch(int64_t I) { return (I / 32 + 15) / 16 * 16; }
 MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed) {
   const int64_t mtiles = (O + kBM - 1) / kBM, nk = (I + kBK - 1) / kBK;
   const int64_t most_splits = std::max<int64_t>(1, std::min<int64_t>(nk / 2, 8));
-  MxPlan best = {false, 1, 1, 0, 0};
+  MxPlan best = {false, 1, 1, 0, 0, false};
   int64_t least = INT64_MAX;
   // Splits are for calls of few units.
   auto splits_for = [&](int64_t units) { return units > 4 * 152 ? 1 : most_splits; };
@@ -1041,6 +1107,7 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
         best.splits = (int)s;
       }
     }
+    best.own_lists = !best.wide && T * K <= kMxOwnPairs;
     if (best.wide) best.grouped_bytes = (size_t)T * K * (size_t)(I / 2 + scale_pitch(I));
   } else {
     // Up to 512 tokens either form (2880 x 5760: narrow blocks up to 256 tokens,
@@ -1069,7 +1136,7 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
 }
 
 cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
-  const bool routed = g.plan != nullptr;
+  const bool routed = g.plan != nullptr || g.shape.own_lists;
   const MxPlan& plan = g.shape;
   const bool wide = plan.wide, grouped = routed && wide;
   const int64_t G = g.I / 32, P = g.T * g.K;
@@ -1108,7 +1175,13 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
   }
   MxKernelArgs a;
   std::memset(static_cast<void*>(&a), 0, sizeof(a));
-  if (routed) a.plan = *g.plan;
+  if (plan.own_lists) {
+    a.sel = g.sel;
+    a.sel64 = g.sel64 ? 1 : 0;
+    a.E = (int)g.E;
+  } else if (routed) {
+    a.plan = *g.plan;
+  }
   a.w_scales = g.w_scales;
   a.x_scales = scales;
   a.x_pitch = (int)pitch;

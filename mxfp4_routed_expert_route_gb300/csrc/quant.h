@@ -32,6 +32,8 @@ cudaError_t launch_dequantize(const uint8_t* packed, const uint8_t* scales, int6
 // Products of MXFP4 tokens and MXFP4 weights (gemm_mx.cu). Experts with tokens
 // that one call may have (their lists are kept in shared memory).
 constexpr int64_t kMxMaxActive = 4096;
+// Up to this many pairs the kernel makes its routing lists itself.
+constexpr int kMxOwnPairs = 256;
 
 // The shape of a call's units of work.
 struct MxPlan {
@@ -41,13 +43,16 @@ struct MxPlan {
   int64_t units;          // blocks x 128-row tiles (pairs of them when wide) x splits
   size_t grouped_bytes;   // routed: the token rows in the lists' order (0: the kernel
                           // gathers them itself)
+  bool own_lists;         // routed: the kernel routes for itself
 };
 MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool routed);
 
 struct MxGemm {
   const uint8_t *x_packed, *x_scales;   // [T][I/2], [T][I/32]
   const uint8_t *w_packed, *w_scales;   // [E][O][I/2], [E][O][I/32]
-  const RoutePlan* plan;                // routing lists, or null: dense (E = 1)
+  const RoutePlan* plan;                // routing lists, or null: dense (E = 1), or
+  const void* sel;                      // shape.own_lists: the ids
+  bool sel64;
   int64_t T, E, I, O, K;                // K: picks per token (routed)
   MxPlan shape;                         // gemm_mx_plan() of these sizes
   void* grouped;                        // shape.grouped_bytes of scratch (routed)

@@ -68,13 +68,15 @@ ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t O, int64_t K, co
     return base ? static_cast<char*>(base) + at : nullptr;
   };
   const size_t P = (size_t)T * K;
-  ws.plan.meta = static_cast<int*>(take(kMetaWords * sizeof(int)));
-  ws.plan.counts = static_cast<int*>(take((size_t)E * sizeof(int)));
-  ws.plan.offsets = static_cast<int*>(take((size_t)(E + 1) * sizeof(int)));
-  ws.plan.active = static_cast<int*>(take((size_t)E * sizeof(int)));
-  ws.plan.pair_list = static_cast<int*>(take(P * sizeof(int)));
-  const size_t wc = route_global_counter_words(T, K, E, false);
-  ws.wc_global = wc ? static_cast<int*>(take(wc * sizeof(int))) : nullptr;
+  if (!p.own_lists) {
+    ws.plan.meta = static_cast<int*>(take(kMetaWords * sizeof(int)));
+    ws.plan.counts = static_cast<int*>(take((size_t)E * sizeof(int)));
+    ws.plan.offsets = static_cast<int*>(take((size_t)(E + 1) * sizeof(int)));
+    ws.plan.active = static_cast<int*>(take((size_t)E * sizeof(int)));
+    ws.plan.pair_list = static_cast<int*>(take(P * sizeof(int)));
+    const size_t wc = route_global_counter_words(T, K, E, false);
+    ws.wc_global = wc ? static_cast<int*>(take(wc * sizeof(int))) : nullptr;
+  }
   ws.grouped = p.grouped_bytes ? take(p.grouped_bytes) : nullptr;
   ws.part = static_cast<float*>(take(P * p.splits * (size_t)O * sizeof(float)));
   ws.bytes = off;
@@ -83,7 +85,7 @@ ExpertWorkspace carve(void* base, int64_t T, int64_t E, int64_t O, int64_t K, co
 
 // The units of a routed call; none without pairs or experts.
 MxPlan routed_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K) {
-  return K > 0 && E > 0 ? gemm_mx_plan(T, E, I, O, K, true) : MxPlan{false, 1, 0, 0, 0};
+  return K > 0 && E > 0 ? gemm_mx_plan(T, E, I, O, K, true) : MxPlan{false, 1, 0, 0, 0, false};
 }
 
 size_t linear_workspace(const MxPlan& p, int64_t T, int64_t O) {
@@ -281,7 +283,8 @@ extern "C" int mxfp4_expert_linear_quantized(
   const cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (K > 0) {
     // With E == 0 every id is out of range: the bucketer counts them.
-    if (launch_route(selected_experts, index_dtype, T, K, E, ws.wc_global, ws.plan,
+    if (!plan.own_lists &&
+        launch_route(selected_experts, index_dtype, T, K, E, ws.wc_global, ws.plan,
                      TokenPrep{nullptr, nullptr, nullptr, I}, UnitSplit{0, 0, 0, 1000},
                      stream) != cudaSuccess)
       return MXFP4EL_ERR_CUDA;
@@ -291,7 +294,12 @@ extern "C" int mxfp4_expert_linear_quantized(
       g.x_scales = x_scales;
       g.w_packed = packed_weights;
       g.w_scales = scale_bytes;
-      g.plan = &ws.plan;
+      if (plan.own_lists) {
+        g.sel = selected_experts;
+        g.sel64 = index_dtype == MXFP4EL_INDEX_I64;
+      } else {
+        g.plan = &ws.plan;
+      }
       g.T = T;
       g.E = E;
       g.I = I;
@@ -303,6 +311,10 @@ extern "C" int mxfp4_expert_linear_quantized(
       if (launch_gemm_mx(g, stream) != cudaSuccess) return MXFP4EL_ERR_CUDA;
     }
   }
+  // The combine may read its other inputs before the product is done, unless the
+  // product is the call's first kernel: that one starts, and lets the combine
+  // start, while the kernel before the call may still be writing them.
+  const bool early = product && !plan.own_lists;
   return status_of(launch_combine(shared_output, selected_experts, index_dtype, mixture_weights,
-                                  ws.part, plan.splits, out, dtype, T, E, O, K, product, stream));
+                                  ws.part, plan.splits, out, dtype, T, E, O, K, early, stream));
 }

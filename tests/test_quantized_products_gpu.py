@@ -182,6 +182,47 @@ def test_experts_by_tokens_per_expert(counts):
     check_routed(lib.mxfp4_expert_linear_quantized(*x, *w, sel, p, ys), x, w, sel, p, ys, 544, BF16)
 
 
+@pytest.mark.parametrize("T,K,E", [(255, 1, 100), (64, 4, 90), (257, 1, 200), (128, 2, 300),
+                                   (32, 8, 3), (256, 1, 1), (43, 6, 40)])
+def test_experts_around_the_kernels_own_lists(T, K, E):
+    """Up to 256 pairs the product makes its routing lists itself."""
+    g = torch.Generator().manual_seed(T)
+    picks = torch.randint(-1, E + 1, (T, K), generator=g).tolist()
+    x, w, sel, p, ys = make_routed(T, E, K, 96, 70, F32, seed=2, picks=picks)
+    lib.device_errors()
+    for ids in (sel, sel.long()):
+        got = lib.mxfp4_expert_linear_quantized(*x, *w, ids, p, ys)
+        check_routed(got, x, w, sel, p, ys, 96, F32)
+        assert lib.device_errors() == sum(not 0 <= e < E for row in picks for e in row)
+
+
+def test_a_chain_of_calls_without_waiting():
+    """Router, quantiser and experts again and again, each on what the one before
+    wrote: no kernel may start on what is not there yet."""
+    T, E, K, I = 24, 12, 2, 256
+    w = rows(E, I, I, seed=5, lo=114, hi=118)
+    gate = torch.randn(I, E, generator=torch.Generator().manual_seed(1)).cuda()
+    x0 = torch.randn(T, I, generator=torch.Generator().manual_seed(2)).cuda().to(BF16)
+
+    def run(wait):
+        x, out = x0, []
+        for _ in range(30):
+            sel, p = lib.route_experts(x.float() @ gate, K, score="sigmoid")
+            q = lib.quantize_mxfp4(x)
+            if wait:
+                torch.cuda.synchronize()
+            x = lib.mxfp4_expert_linear_quantized(*q, *w, sel, p, x)
+            if wait:
+                torch.cuda.synchronize()
+            x = (x.float() / x.float().abs().amax(1, keepdim=True)).to(BF16)
+            out.append(x)
+        return out
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+
+
 @pytest.mark.parametrize("T", [4, 90])
 def test_experts_the_same_id_twice_and_ids_out_of_range(T):
     picks = [[1, 1, 5] if t % 3 == 0 else [-1, 2, 1 << 30] if t % 3 == 1 else [4, -7, 0]
