@@ -175,11 +175,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // The kept groups of one token as a bit mask. choice: the warp's E choices, or
-// logits where they rank as the choices do (NaN: not to be taken). *sure: the
-// border between kept and other groups is wider than the choices' error `err`
-// plus the roundings of their sums; err = 0: exact.
+// with by_logit (one expert stands for its group, no bias) the logits, which
+// rank as the choices do but for choices that round to the same number (NaN: not
+// to be taken). *sure: the border between kept and other groups is wider than
+// the choices' error `err` plus the roundings of their sums. score: of a logit.
+template <typename Score>
 __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float* choice,
-                                                 float err, bool* sure) {
+                                                 bool by_logit, float err, Score score,
+                                                 bool* sure) {
   const int lane = threadIdx.x & 31;
   // `lanes` neighbouring lanes (a power of two) share a group.
   const int lanes = 1 << (31 - __clz(32 / a.groups));
@@ -212,13 +215,26 @@ __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float
   }
   const bool valid = v == v, in = valid && rank < a.top_groups;
   const unsigned kept = __ballot_sync(kFullMask, in);
-  const uint32_t lo = __reduce_min_sync(kFullMask, in ? order_key(v) : 0xffffffffu);
-  const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? order_key(v) : 0u);
-  if (hi != 0u && kept != 0u) {
-    const float a_lo = key_value(lo), a_hi = key_value(hi);
+  const uint32_t k = valid ? order_key(v) : 0u;
+  const uint32_t lo = __reduce_min_sync(kFullMask, in ? k : 0xffffffffu);
+  const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? k : 0u);
+  auto apart = [&](uint32_t upper, uint32_t lower) {
+    const float u = by_logit ? score(key_value(upper)) : key_value(upper);
+    const float l = by_logit ? score(key_value(lower)) : key_value(lower);
     // (Experts may be kept out by a bias of -infinity.)
-    *sure = err == 0.f || (a_hi == -INFINITY && a_lo > -INFINITY) ||
-            a_lo - a_hi > 4.f * err + (fabsf(a_lo) + fabsf(a_hi)) * 0x1p-22f;
+    return (l == -INFINITY && u > -INFINITY) ||
+           u - l > 4.f * err + (fabsf(u) + fabsf(l)) * 0x1p-22f;
+  };
+  if (hi != 0u && kept != 0u) {
+    if (!by_logit || lo != hi) {
+      *sure = apart(lo, hi);
+    } else {
+      // Groups of the border's very logit are true ties and go by index; the
+      // others have to be above or below them for certain.
+      const uint32_t up = __reduce_min_sync(kFullMask, in && k > lo ? k : 0xffffffffu);
+      const uint32_t down = __reduce_max_sync(kFullMask, valid && !in && k < lo ? k : 0u);
+      *sure = (up == 0xffffffffu || apart(up, lo)) && (down == 0u || apart(lo, down));
+    }
   }
   return kept;
 }
@@ -291,7 +307,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
   if (a.groups > 1) {
     __syncwarp();
     bool sure = true;
-    const unsigned kept = route_groups(a, scratch, by_logit ? 0.f : err, &sure);
+    const unsigned kept =
+        route_groups(a, scratch, by_logit, err, [&](float l) { return choice_of(l, 0); }, &sure);
     if (!sure) return false;
     // e / group_size by a multiplication: exact for e * group_size < 2^20.
     const uint32_t mul = ((1u << 20) + a.group_size - 1) / a.group_size;
@@ -382,7 +399,18 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
   }
   const bool picked = lane < n && rank < a.K;
   float w = 0.f;
-  if (picked) w = kSoftmax ? expf(logit - top) * inv : 1.f / (1.f + expf(-logit));
+  if (picked) {
+    if constexpr (kSoftmax) {
+      // d + rest is logit - top exactly: d alone is off by half an ulp, which is
+      // many of the exponential where d is large.
+      const float d = logit - top, back = d - logit;
+      const float rest = (logit - (d - back)) - (top + back);
+      const float z = expf(d);
+      w = z > 0.f ? fmaf(z, rest, z) * inv : 0.f;      // rest is NaN for a logit of -infinity
+    } else {
+      w = 1.f / (1.f + expf(-logit));
+    }
+  }
   if (a.normalize) {
     float total = w;
 #pragma unroll

@@ -203,6 +203,23 @@ def test_route_what_is_not_finite(score, groups):
             assert not p.isnan().any()
 
 
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_groups_whose_scores_round_together(score, best):
+    """Different logits whose float64 scores are the same number (1, or 0.5, or
+    nearly the largest): groups of equal score go to the lower index."""
+    g = torch.Generator().manual_seed(3)
+    big = torch.randint(30, 60, (60, 32), generator=g).float()
+    small = torch.randint(-4, 5, (60, 32), generator=g) * 1e-20
+    mixed = torch.where(torch.rand(60, 32, generator=g) < 0.5, big, small)
+    far = torch.randint(-3, 3, (60, 32), generator=g) * 400.0
+    for logits in (big, small, mixed, far):
+        for top in (1, 3):
+            sel, p = lib.route_experts(logits.cuda(), 4, score=score, groups=8, top_groups=top,
+                                       group_best=best)
+            check_routed(logits, 4, sel, p, score=score, groups=8, top_groups=top, group_best=best)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_experts_kept_out_by_the_bias(score):
     logits = normal(200, 64, seed=6)
