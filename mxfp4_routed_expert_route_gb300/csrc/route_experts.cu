@@ -408,7 +408,8 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
       const float z = expf(d);
       w = z > 0.f ? fmaf(z, rest, z) * inv : 0.f;      // rest is NaN for a logit of -infinity
     } else {
-      w = 1.f / (1.f + expf(-logit));
+      const float z = expf(-fabsf(logit));         // no overflow, and small scores keep their bits
+      w = (logit >= 0.f ? 1.f : z) / (1.f + z);
     }
   }
   if (a.normalize) {

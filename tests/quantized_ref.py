@@ -2,7 +2,8 @@
 
 MXFP4 values and the quantiser are exact, so the tests ask for equal bits.
 The router's choice is made in float64 here as in the library; its weights are
-float32 there: a score is one exponential (2 ulp), an addition and a division
+float32 there: a score is one exponential (2 ulp; the softmax's difference of
+logits is carried in two terms, exactly), an addition and a division
 (half an ulp each, at most 3.5 ulp of 2^-23 together, with the sum of a softmax
 adding log2(1024) = 10 roundings of half an ulp of the larger operand at most
 when it is summed as a tree of 32 lanes over up to 32 terms each: 37 half ulps),

@@ -203,6 +203,26 @@ def test_route_what_is_not_finite(score, groups):
             assert not p.isnan().any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_weights_of_small_scores(score):
+    """Scores down to 2^-140, whose quotient by the sum plus 1e-20 is far from
+    small. A score under 2^-126 is off by half of 2^-149, and the divisor is at
+    least 1e-20: 7.1e-26 a weight, and as much again for the sum."""
+    logits = torch.linspace(-97, -30, 64).repeat(20, 1)[:, torch.randperm(64)]
+    logits[:, 0] += torch.arange(20)
+    if score == "softmax":
+        logits[:, 5] = 0.0                       # the others' scores are as small
+    sel, p = lib.route_experts(logits.cuda(), 24, score=score)
+    want_sel, want_p = ref.route(logits, 24, score=score)
+    assert torch.equal(sel.cpu(), want_sel)
+    torch.testing.assert_close(p.cpu().double(), want_p, rtol=ref.WEIGHT_RTOL, atol=1.5e-25)
+    low = logits - 60 * (logits > -60)
+    sel, p = lib.route_experts(low.cuda(), 24, score="sigmoid")
+    want_sel, want_p = ref.route(low, 24, score="sigmoid")
+    assert torch.equal(sel.cpu(), want_sel)
+    torch.testing.assert_close(p.cpu().double(), want_p, rtol=ref.WEIGHT_RTOL, atol=1.5e-25)
+
+
 @pytest.mark.parametrize("best", [1, 2])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_groups_whose_scores_round_together(score, best):
