@@ -701,7 +701,9 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
         const uintptr_t lo = (reinterpret_cast<uintptr_t>(from) + 15) & ~(uintptr_t)15;
         const uintptr_t hi =
             reinterpret_cast<uintptr_t>(from + (size_t)min(kBM, a.O - w.m0) * a.G) & ~(uintptr_t)15;
-        if (hi > lo) prefetch_l2(reinterpret_cast<const void*>(lo), (uint32_t)(hi - lo));
+        if (hi > lo)                                   // 64 KB: rows of 16384 values
+          prefetch_l2(reinterpret_cast<const void*>(lo),
+                      (uint32_t)min(hi - lo, (uintptr_t)65536));
       }
       if (lane == 0) sh.units[pu.idx] = w;
       __syncwarp();
