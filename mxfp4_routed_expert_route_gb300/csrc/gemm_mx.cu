@@ -38,14 +38,12 @@
 // zeros, and scale bytes past it are set to 0, so what is added is exactly 0;
 // MMAs wholly past the end are not issued.
 //
-// Wide blocks: two CTAs, on neighbouring SMs, take two tiles of one block at a
-// time, and each loads half of the token rows of every stage for both
-// (multicast). Alone, an SM reads 40 KB of codes per stage from L2, which
-// then bounds the dense product (15 TB/s). A stage's slot is free when the MMAs
-// of both CTAs are done with it.
+// Every CTA copies its own operands: this library is loaded wherever the
+// framework runs, and its copies name one CTA's memory alone. In wide blocks an SM
+// reads 40 KB of codes per stage from L2, which bounds the dense product.
 //
 // Warp roles in a CTA of 14 warps (one CTA per SM, persistent over units
-// (block, 128-row tile or pair of tiles, K split)):
+// (block, 128-row tile, K split)):
 //   warp 0      copies of codes (weights and tokens), one elected lane; TMEM
 //   warp 1      scale copies to tensor memory and MMAs, one elected lane
 //   warp 2      lists of the experts with tokens at start (routed; for up to 256
@@ -63,19 +61,18 @@
 //
 // What bounds it, on one GB300. Few tokens: the weights' bytes (16 tokens over
 // 384 experts of 7168 x 4096, 1.71 GB: 273 us, 6.3 TB/s, 94 % of a plain copy;
-// 8 tokens over 128 experts of 2880 x 5760, 253 MB: 54 us with lists and
+// 8 tokens over 128 experts of 2880 x 5760, 253 MB: 53 us with lists and
 // combine, of which some 8 us are the chain ids -> lists -> units -> first
-// copies). Many: dense 8192 x 7168 x 4096 in 94 us, 5.1 PFLOP/s; the tensor pipe
-// is active 54 % of the time, and the scale copies, which it runs in turn with
-// the MMAs, take a third as long again (six of about 28 cycles beside four MMAs
-// of 88 a stage); with neither copies nor scales the MMAs alone take 82 us. The
-// skewed prefill (8192 tokens, 8 of 384 experts) takes 1.55 ms here, 7.3 GB
-// of weights, rows and float32 results at 4.8 TB/s.
-// Measured on the way (dense 8192 x 7168 x 4096): copies and MMAs from loops of
-// one thread 114 us, from uniform warps 108 (the operands of copies and tcgen05
-// otherwise have to be made uniform at every issue); scales in two teams'
-// stages with the token rows read by each CTA alone 116, by the pair 102; four
-// stages instead of five 98; a third read of scales under way 115.
+// copies). Many: dense 8192 x 7168 x 4096 in 101 us, 4.8 PFLOP/s. Parts of it left
+// out: copies alone 90 us (40 KB a stage, 1.7 GB from L2 at 19 TB/s), MMAs alone
+// 79, MMAs and their scale copies 81, all but the copies of codes 86, all but the
+// scale copies 101. So reads from L2 bound it, the MMAs come close behind, and the
+// scale copies hide. The skewed prefill (8192 tokens, 8 of 384 experts, 7.3 GB of
+// weights, rows and float32 results) takes 1.56 ms here, 4.7 TB/s.
+// Measured on the way (dense 8192 x 7168 x 4096, other steps then missing): copies
+// and MMAs from loops of one thread 114 us, from uniform warps 108 (the operands
+// of copies and tcgen05 otherwise have to be made uniform at every issue); five
+// stages instead of four 109 against 101.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -116,9 +113,8 @@ struct Shape {
   static constexpr uint32_t kSfColsA = kSfPerStage * 4, kSfColsB = kSfPerStage * kBRowBlocks * 4;
   static constexpr uint32_t kSfCol = 2 * kN;
   static constexpr int kTmemStages = (int)((kTmemCols - kSfCol) / (kSfColsA + kSfColsB));
-  static constexpr int kCluster = kN == kMxWide ? 2 : 1;
   // More stages would fit, and do not help: what they leave of the SM's memory
-  // caches the scale bytes (8192 x 7168 x 4096: 5 stages 104 us, 4 stages 98).
+  // caches the scale bytes (8192 x 7168 x 4096: 5 stages 109 us, 4 stages 101).
   static constexpr int kStages = kN == kMxNarrow ? 8 : 4;
   // Scale warps: two teams of one warp for the weights' rows and one for the
   // tokens', or two (128 and 64 rows) when wide.
@@ -133,9 +129,8 @@ struct Shape {
 
 struct MxMaps {
   CUtensorMap a;      // weights' codes [E][O][I/2], box {128, 128, 1}, 128-byte swizzle
-  CUtensorMap b[kMxWide / 32];   // tokens' codes [rows][I/2], boxes {128, 16 (i + 1)} (half
-                                 // a block) when wide; else the first alone, {128, 32}, or
-                                 // {128, 1} (gathered)
+  CUtensorMap b[kMxWide / 32];   // tokens' codes [rows][I/2], boxes {128, 32 (i + 1)}; narrow:
+                                 // the first alone, {128, 32}, or {128, 1} (gathered)
 };
 
 struct MxKernelArgs {
@@ -197,36 +192,6 @@ __device__ __forceinline__ bool elect_one() {
       "}"
       : "=r"(e));
   return e != 0;
-}
-
-// A 2-D tiled load into the same place of every CTA of the cluster in `mask`; each
-// CTA's own barrier (at the same place too) gets the bytes.
-__device__ __forceinline__ void tma_load_2d_multicast(void* dst, const void* tmap, int x, int y,
-                                                      uint64_t* bar, uint16_t mask,
-                                                      uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5, %6;" ::"r"(
-          smem_addr(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(mask), "l"(policy)
-      : "memory");
-}
-// tc_commit on the barrier at this place in every CTA of the cluster in `mask`.
-__device__ __forceinline__ void tc_commit_multicast(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(smem_addr(bar)),
-      "h"(mask)
-      : "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
-               ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return (int)r;
 }
 
 // Four rows of 128 bytes by their row indices, one after another at dst.
@@ -295,11 +260,9 @@ struct RingPos {
 
 template <int kN, bool kRouted>
 __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const ExpertLists& ex,
-                                        int num_active, int idx, int rank) {
-  constexpr int kPair = Shape<kN>::kCluster;   // tiles of a unit, one per CTA of the cluster
+                                        int num_active, int idx) {
   Unit w;
-  const int mtiles = (a.mtiles + kPair - 1) / kPair;
-  const int per_block = mtiles * a.splits;
+  const int per_block = a.mtiles * a.splits;
   int first = 0, nblk, cnt, local;
   if constexpr (kRouted) {
     const int blk = idx / per_block;
@@ -327,8 +290,8 @@ __device__ __forceinline__ Unit unit_at(const MxKernelArgs& a, const ExpertLists
   w.tok0 = first + j * bsz;
   w.ntok = max(0, min(bsz, cnt - j * bsz));
   w.nmma = (w.ntok + 15) / 16 * 16;
-  w.split = rest / mtiles;
-  w.m0 = ((rest - w.split * mtiles) * kPair + rank) * kBM;     // may be past the last row
+  w.split = rest / a.mtiles;
+  w.m0 = (rest - w.split * a.mtiles) * kBM;
   const int nk = (a.G + kGroupsPerStage - 1) / kGroupsPerStage;
   w.kt0 = (int)((int64_t)w.split * nk / a.splits);
   w.kt1 = (int)((int64_t)(w.split + 1) * nk / a.splits);
@@ -598,8 +561,8 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&sh.full[s], 1 + S::kTeamWarps);       // the copies (bytes), a team's warps
-      mbar_init(&sh.empty[s], S::kCluster);            // the MMAs of every CTA that the
-    }                                                  // copies of this one write to
+      mbar_init(&sh.empty[s], 1);                      // the MMAs
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.d_full[b], 1);
       mbar_init(&sh.d_empty[b], kEpiWarps);
@@ -661,18 +624,16 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       if (lane == 0) {
         ex.blocks[na] = run;
         sh.num_active = na;
-        sh.num_units = run * ((a.mtiles + S::kCluster - 1) / S::kCluster) * a.splits;
+        sh.num_units = run * a.mtiles * a.splits;
       }
     } else if (lane == 0) {
       sh.num_active = 0;
-      sh.num_units = a.blocks * ((a.mtiles + S::kCluster - 1) / S::kCluster) * a.splits;
+      sh.num_units = a.blocks * a.mtiles * a.splits;
     }
   }
   tc_fence_before_sync();
   __syncthreads();
-  if constexpr (S::kCluster > 1) cluster_sync();       // the other's barriers are ready too
   tc_fence_after_sync();
-  const int rank = S::kCluster > 1 ? __shfl_sync(kFullMask, cluster_rank(), 0) : 0;
   const uint32_t tmem = __shfl_sync(kFullMask, sh.tmem_base, 0);
   const uint32_t ring_addr = __shfl_sync(kFullMask, smem_addr(ring), 0);
   bool ok = true;
@@ -681,10 +642,10 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
     // ------------------------------------------------------------ the units
     const int num_units = sh.num_units, num_active = sh.num_active;
     RingPos pu;
-    for (int idx = blockIdx.x / S::kCluster;; idx += gridDim.x / S::kCluster) {
+    for (int idx = blockIdx.x;; idx += gridDim.x) {
       Unit w;
       w.e = -1;
-      if (idx < num_units) w = unit_at<kN, kRouted>(a, ex, num_active, idx, rank);
+      if (idx < num_units) w = unit_at<kN, kRouted>(a, ex, num_active, idx);
       if (w.e >= 0 && w.ntok <= 0) continue;
       int t = 0;
       if (kGather && w.e >= 0)                  // past the block its last token
@@ -696,7 +657,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
       if (kGather) sh.rows[pu.idx][lane] = t;
       // The tile's scale bytes lie together: have them in L2 by the time the
       // scale warps ask, which they do only a few stages ahead.
-      if (lane == 0 && w.e >= 0 && w.m0 < a.O) {
+      if (lane == 0 && w.e >= 0) {
         const uint8_t* from = a.w_scales + ((size_t)w.e * a.O + w.m0) * a.G;
         const uintptr_t lo = (reinterpret_cast<uintptr_t>(from) + 15) & ~(uintptr_t)15;
         const uintptr_t hi =
@@ -757,15 +718,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
                 tma_gather4(stage + kStageA + q * 4 * kRowBytes, &maps.b[0], x, rows[q], bar,
                             pol_keep);
           } else {
-            // Each CTA of the pair loads half of the token rows for both.
-            static_assert(S::kCluster == 1 || S::kCluster == 2, "halves");
-            if constexpr (S::kCluster == 2) {
-              const int half = 16 * (load + 1);
-              tma_load_2d_multicast(stage + kStageA + rank * half * kRowBytes, &maps.b[load], x,
-                                    w.tok0 + rank * half, bar, (uint16_t)3, pol_keep);
-            } else {
-              tma_load_2d(stage + kStageA, &maps.b[load], x, w.tok0, bar, pol_keep);
-            }
+            tma_load_2d(stage + kStageA, &maps.b[load], x, w.tok0, bar, pol_keep);
           }
         }
         __syncwarp();
@@ -838,10 +791,7 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
             if (!end || j < last)
               tc_mma_mxf4(d, da + j * 2, db + j * 2, (j & 1) ? idesc2 : idesc0,
                           tsfa + 4 * (j / 2), tsfb + 4 * (j / 2) * S::kBRowBlocks, 1u);
-          if constexpr (S::kCluster > 1)
-            tc_commit_multicast(&sh.empty[idx], (uint16_t)((1 << S::kCluster) - 1));
-          else
-            tc_commit(&sh.empty[idx]);
+          tc_commit(&sh.empty[idx]);
           if (end) tc_commit(&sh.d_full[buf]);
         }
         __syncwarp();
@@ -936,11 +886,6 @@ gemm_mx_kernel(const __grid_constant__ MxMaps maps, const MxKernelArgs a) {
   __syncthreads();
   tc_fence_after_sync();
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
-  // No CTA goes while the other may still copy to it or arrive on its barriers.
-  if constexpr (S::kCluster > 1) {
-    __syncwarp();
-    cluster_sync();
-  }
 }
 
 // The token rows of a wide routed call in the lists' order, scale rows on
@@ -1029,25 +974,9 @@ cudaError_t launch_typed(const MxMaps& maps, MxKernelArgs args, int64_t units,
       opted[dev] = smem;
     }
   }
-  constexpr int kCluster = Shape<kN>::kCluster;
-  const int64_t most = num_sms() / kCluster;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min(units, most) * kCluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = kCluster > 1 ? 2 : 1;
-  const cudaError_t err = cudaLaunchKernelEx(&cfg, gemm_mx_kernel<kN, Out, kRouted>, maps, args);
-  if (err == cudaSuccess) note_launch();
-  return err;
+  return launch_after_previous(gemm_mx_kernel<kN, Out, kRouted>,
+                               dim3((unsigned)std::min<int64_t>(units, num_sms())), dim3(kThreads),
+                               smem, stream, maps, args);
 }
 
 bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
@@ -1066,15 +995,12 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
 namespace {
 
 // What units of this shape take, in quarters of a narrow stage (a quarter is
-// about 0.07 us). A round of units takes every SM (or pair of SMs) one unit: a
-// stage, narrow or wide with its MMAs' share of the width, and about a stage for
-// the unit itself. Splits of K are written, read and joined, 4 bytes a result
+// about 0.07 us). A round of units takes every SM one unit: a stage, narrow or wide
+// with its MMAs' share of the width, and about a stage for the unit itself. Splits of K are written, read and joined, 4 bytes a result
 // and split at some 3 MB a stage each way, by one launch more when dense.
 int64_t plan_cost(bool wide, int64_t blocks, int64_t width, int64_t mtiles, int64_t nk,
                   int64_t splits, int64_t results, bool routed) {
-  const int64_t pair = wide ? Shape<kMxWide>::kCluster : 1, sms = 152 / pair;
-  const int64_t units = blocks * ((mtiles + pair - 1) / pair) * splits;
-  const int64_t rounds = (units + sms - 1) / sms;
+  const int64_t rounds = (blocks * mtiles * splits + 151) / 152;
   const int64_t stage = wide ? 4 + width / 96 : 4;
   int64_t cost = rounds * ((nk + splits - 1) / splits * stage + 4);
   if (splits > 1) cost += (routed ? 0 : 24) + results * splits / 100000;
@@ -1132,8 +1058,7 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
       }
     }
   }
-  const int64_t pair = best.wide ? Shape<kMxWide>::kCluster : 1;
-  best.units = best.blocks * ((mtiles + pair - 1) / pair) * best.splits;
+  best.units = best.blocks * mtiles * best.splits;
   return best;
 }
 
@@ -1171,7 +1096,7 @@ cudaError_t launch_gemm_mx(const MxGemm& g, cudaStream_t stream) {
     const cuuint64_t strides[1] = {row};
     const bool gather = routed && !grouped;
     for (int i = 0; i < (wide ? kMxWide / 32 : 1); ++i) {
-      const cuuint32_t box[2] = {kRowBytes, gather ? 1u : wide ? 16u * (unsigned)(i + 1) : 32u};
+      const cuuint32_t box[2] = {kRowBytes, gather ? 1u : 32u * (unsigned)(i + 1)};
       if (!encode(&maps.b[i], rows, 2, dims, strides, box)) return cudaErrorInvalidValue;
     }
   }

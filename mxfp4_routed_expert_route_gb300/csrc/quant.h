@@ -40,7 +40,7 @@ struct MxPlan {
   bool wide;              // blocks of up to 192 tokens, else 32
   int splits;             // units that share K
   int64_t blocks;         // dense: blocks of tokens; routed: at most this many
-  int64_t units;          // blocks x 128-row tiles (pairs of them when wide) x splits
+  int64_t units;          // blocks x 128-row tiles x splits
   size_t grouped_bytes;   // routed: the token rows in the lists' order (0: the kernel
                           // gathers them itself)
   bool own_lists;         // routed: the kernel routes for itself
