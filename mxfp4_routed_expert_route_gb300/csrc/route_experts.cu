@@ -373,19 +373,25 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
   }
   if (by_choice) {
     // Neighbours in rank that are closer than the error, and not equal for
-    // having the same logit and bias: rank the candidates in float64.
+    // having the same logit and bias: rank the candidates in float64. The
+    // neighbours to look at end at rank K, or, where equal ones share the border,
+    // behind the last of those: any of them may stand at rank K - 1.
     if (lane < n) cid[rank] = lane;
     __syncwarp();
     const int at0 = cid[min(lane, max(n, 1) - 1)], at1 = cid[min(lane + 1, max(n, 1) - 1)];
     const float c = key_value(k);
     const float c0 = __shfl_sync(kFullMask, c, at0), c1 = __shfl_sync(kFullMask, c, at1);
-    bool close = lane < a.K && lane + 1 < n &&
-                 !(c0 - c1 > 2.f * err + (fabsf(c0) + fabsf(c1)) * 0x1p-23f);
-    if (__any_sync(kFullMask, close)) {
+    const bool close =
+        lane + 1 < n && !(c0 - c1 > 2.f * err + (fabsf(c0) + fabsf(c1)) * 0x1p-23f);
+    if (__any_sync(kFullMask, close && lane < a.K)) {
       const float b = lane < n ? a.bias[id] : 0.f;
-      const bool equal = __shfl_sync(kFullMask, logit, at0) == __shfl_sync(kFullMask, logit, at1);
-      if (__shfl_sync(kFullMask, b, at0) == __shfl_sync(kFullMask, b, at1) && equal) close = false;
-      if (__any_sync(kFullMask, close)) {
+      const float l0 = __shfl_sync(kFullMask, logit, at0), l1 = __shfl_sync(kFullMask, logit, at1);
+      const float b0 = __shfl_sync(kFullMask, b, at0), b1 = __shfl_sync(kFullMask, b, at1);
+      const bool equal = l0 == l1 && b0 == b1;
+      // The first pair from rank K - 1 on that is no tie (lane 31 has no pair).
+      const unsigned ties = __ballot_sync(kFullMask, close && equal) >> (a.K - 1);
+      const int last = a.K - 2 + __ffs((int)~ties);
+      if (__any_sync(kFullMask, close && !equal && lane <= last)) {
         if (kSoftmax) return false;                // the sum is needed in float64 too
         const double d = lane < n ? 1.0 / (1.0 + exp(-(double)logit)) + (double)b : 0.0;
         rank = 0;
