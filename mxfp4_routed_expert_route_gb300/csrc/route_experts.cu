@@ -177,8 +177,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // The kept groups of one token as a bit mask. choice: the warp's E choices, or
 // with by_logit (one expert stands for its group, no bias) the logits, which
 // rank as the choices do but for choices that round to the same number (NaN: not
-// to be taken). *sure: the border between kept and other groups is wider than
-// the choices' error `err` plus the roundings of their sums. score: of a logit.
+// to be taken). *sure: no other group's sum can be as large as a kept one's, each
+// sum being off by the two choices' error `err`, the roundings of those choices and
+// its own. Choices of opposite sign may be far larger than their sum, so their
+// roundings go by |best| + |second|: half an ulp (2^-24) for the choices, at most
+// that much again for the sum and once more for the border worked out here, under
+// 2^-22 of it together. score: of a logit.
 template <typename Score>
 __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float* choice,
                                                  bool by_logit, float err, Score score,
@@ -215,18 +219,28 @@ __device__ __forceinline__ unsigned route_groups(const RouteArgs& a, const float
   }
   const bool valid = v == v, in = valid && rank < a.top_groups;
   const unsigned kept = __ballot_sync(kFullMask, in);
+  if (!by_logit) {
+    // An infinite choice has no rounding (experts may be kept out by -infinity);
+    // finite ones whose sum passes float32 say nothing.
+    float size = fabsf(b0) < INFINITY ? fabsf(b0) : 0.f;
+    if (a.group_best > 1 && fabsf(b1) < INFINITY) size += fabsf(b1);
+    size = __shfl_sync(kFullMask, size, min(lane * lanes, 31));
+    const float off = 2.f * err + size * 0x1p-22f;
+    const float low = off < INFINITY ? v - off : -INFINITY;
+    const float high = off < INFINITY ? v + off : INFINITY;
+    const uint32_t lo = __reduce_min_sync(kFullMask, in ? order_key(low + 0.f) : 0xffffffffu);
+    const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? order_key(high + 0.f) : 0u);
+    *sure = lo > hi;
+    return kept;
+  }
   const uint32_t k = valid ? order_key(v) : 0u;
   const uint32_t lo = __reduce_min_sync(kFullMask, in ? k : 0xffffffffu);
   const uint32_t hi = __reduce_max_sync(kFullMask, valid && !in ? k : 0u);
   auto apart = [&](uint32_t upper, uint32_t lower) {
-    const float u = by_logit ? score(key_value(upper)) : key_value(upper);
-    const float l = by_logit ? score(key_value(lower)) : key_value(lower);
-    // (Experts may be kept out by a bias of -infinity.)
-    return (l == -INFINITY && u > -INFINITY) ||
-           u - l > 4.f * err + (fabsf(u) + fabsf(l)) * 0x1p-22f;
+    return score(key_value(upper)) - score(key_value(lower)) > 4.f * err;
   };
   if (hi != 0u && kept != 0u) {
-    if (!by_logit || lo != hi) {
+    if (lo != hi) {
       *sure = apart(lo, hi);
     } else {
       // Groups of the border's very logit are true ties and go by index; the

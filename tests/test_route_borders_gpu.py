@@ -57,3 +57,61 @@ def test_many_ties_of_nearly_equal_choices(score, groups, top):
     for bias in (torch.zeros(E), torch.full((E,), 0.25)):
         for K in (1, 2, 5, 9, 16):
             check(logits, K, bias, score=score, groups=groups, top_groups=top)
+
+
+def opposite(E, B):
+    """Biases +B and -B in turn, exact in float32."""
+    return torch.tensor([B, -B] * (E // 2), dtype=torch.float32)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("B", [1.0, 10.0, 64.0, 1e3, 3e4, 1e6])
+def test_groups_of_large_biases_of_both_signs(B, score):
+    """A group's two choices cancel, their roundings (at B's size) do not."""
+    g = torch.Generator().manual_seed(int(B))
+    T, E = 300, 64
+    for by in (1.0, 1e-2, 1e-4):
+        logits = by * torch.randn(T, E, generator=g)
+        for top in (1, 8, 31):
+            check(logits, 1, opposite(E, B), score=score, groups=32, top_groups=top)
+        check(logits, 3, opposite(E, B), score=score, groups=8, top_groups=3)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_one_group_of_large_biases_among_small_ones(score):
+    """The border lies between other groups, or at the one whose sums are rough."""
+    g = torch.Generator().manual_seed(4)
+    T, E = 400, 32
+    bias = 0.01 * torch.randn(E, generator=g)
+    bias[8:10] = torch.tensor([4096.0, -4096.0])
+    bias[10:12] = -1e5
+    for by in (1.0, 1e-3):
+        logits = by * torch.randn(T, E, generator=g)
+        for top in (1, 2, 4, 7):
+            check(logits, 2, bias, score=score, groups=8, top_groups=top)
+
+
+def test_group_sums_that_float32_puts_the_other_way_round():
+    """Biases of 1000: a choice is rounded to multiples of u = 2^-14. Group 0's
+    scores lie 0.6 u above such a multiple and are rounded up, group 1's 0.4 u
+    above, one of them a whole u higher, and are rounded down: group 1's sum is
+    the larger by 0.6 u and comes out smaller by u."""
+    u = 2.0 ** -14
+    s = torch.tensor([0.5 + 0.6 * u, 0.5 + 0.6 * u, 0.5 + 1.4 * u, 0.5 + 0.4 * u],
+                     dtype=torch.float64)
+    logits = torch.log(s / (1 - s)).float()[None].repeat(9, 1)
+    bias = torch.tensor([1000.0, -1000.0, 1000.0, -1000.0])
+    check(logits, 1, bias, score="sigmoid", groups=2, top_groups=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_of_infinite_biases_and_of_sums_past_float32(score):
+    g = torch.Generator().manual_seed(8)
+    inf, big = float("inf"), 3.0e38
+    logits = torch.randn(50, 16, generator=g)
+    for values in ((inf, 0.0, inf, 1.0, 0.0, 0.0, -inf, 0.0), (big, big, 2.9e38, big, 0.0, 0.0, 1.0, 1.0),
+                   (-big, -big, -big, -2.9e38, 0.0, -big, -inf, -inf), (inf, inf, big, big, inf, -big, 0.0, 0.0)):
+        bias = torch.tensor(values).repeat(2)
+        for groups, top in ((8, 1), (8, 2), (8, 5), (8, 7), (4, 2)):
+            check(logits, 2, bias, score=score, groups=groups, top_groups=top)
+            check(logits, 2, bias, score=score, groups=groups, top_groups=top, group_best=1)
