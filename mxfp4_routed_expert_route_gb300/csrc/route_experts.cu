@@ -499,9 +499,12 @@ cudaError_t launch_route_experts(const RouteArgs& a, int dtype, cudaStream_t str
                     ? (a.softmax ? kernel_for<true, __nv_bfloat16>(a.E)
                                  : kernel_for<false, __nv_bfloat16>(a.E))
                     : (a.softmax ? kernel_for<true, float>(a.E) : kernel_for<false, float>(a.E));
+  // Always the most that any call needs: a call of fewer experts on another thread
+  // would otherwise take it back between this line and the launch.
   if (smem > 48 * 1024) {
     const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(kWarps * scratch_bytes(kRouteMaxExperts)));
     if (err != cudaSuccess) return err;
   }
   kernel<<<blocks, kThreads, smem, stream>>>(a);
