@@ -417,15 +417,16 @@ cudaError_t launch_route(const void* sel, int index_dtype, int64_t T, int64_t K,
                         stream);
   }
   const size_t smem = wc_global ? 0 : kRouteWarps * (size_t)E * sizeof(int);
-  // Dynamic plus static shared memory above 48 KiB needs the opt-in.
+  // Dynamic plus static shared memory above 48 KiB needs the opt-in: the same for
+  // every call, so that none on another thread takes it back before the launch.
   if (smem > 40 * 1024) {
     cudaError_t err;
     if (index_dtype == kIndexI64)
-      err = cudaFuncSetAttribute(route_kernel<int64_t>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      err = cudaFuncSetAttribute(route_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kRouteSmemLimit);
     else
-      err = cudaFuncSetAttribute(route_kernel<int32_t>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      err = cudaFuncSetAttribute(route_kernel<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kRouteSmemLimit);
     if (err != cudaSuccess) return err;
   }
   if (index_dtype == kIndexI64)

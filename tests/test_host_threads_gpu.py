@@ -58,3 +58,31 @@ def test_routers_of_different_widths():
     """More than 768 experts take shared memory that the kernel has to be allowed
     first; a narrower call may not take it back from a wider one."""
     run_threads([router(E) for E in (1024, 776, 1024, 800)], 30000)
+
+
+def experts(E):
+    """An expert linear of 300 pairs, whose lists one block makes with counters in
+    shared memory: 128 bytes an expert."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    T, K, I, O = 300, 1, 32, 8
+    x, xs = lib.quantize_mxfp4(torch.randn(T, I, generator=g, device="cuda"))
+    w, ws = lib.quantize_mxfp4(torch.randn(E, O, I, generator=g, device="cuda"))
+    sel = torch.randint(0, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    p = torch.rand(T, K, generator=g, device="cuda")
+    ys = torch.randn(T, O, generator=g, device="cuda")
+    out = torch.empty_like(ys)
+    l = _native.load()
+    need = l.mxfp4_expert_linear_quantized_workspace_size(T, E, I, O, K)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    tensors = (x, xs, w, ws, sel, p, ys, out)
+
+    def call(stream):
+        return l.mxfp4_expert_linear_quantized(*(t.data_ptr() for t in tensors), T, E, I, O, K,
+                                               _native.DTYPE_F32, _native.INDEX_I32,
+                                               work.data_ptr(), need, stream)
+
+    return call, [out]
+
+
+def test_expert_linears_of_different_numbers_of_experts():
+    run_threads([experts(E) for E in (768, 384, 704, 400)], 10000)
