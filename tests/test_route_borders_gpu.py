@@ -115,3 +115,15 @@ def test_groups_of_infinite_biases_and_of_sums_past_float32(score):
         for groups, top in ((8, 1), (8, 2), (8, 5), (8, 7), (4, 2)):
             check(logits, 2, bias, score=score, groups=groups, top_groups=top)
             check(logits, 2, bias, score=score, groups=groups, top_groups=top, group_best=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 160, 192, 255, 256, 257,
+                               320, 383, 384, 385, 511, 512, 513, 768, 1023, 1024])
+def test_every_width_and_its_edges(E, score):
+    g = torch.Generator().manual_seed(E)
+    logits = 2.0 * torch.randn(12, E, generator=g)
+    bias = 0.1 * torch.randn(E, generator=g)
+    for K in (1, 8, 17, min(E, 32)):
+        check(logits, K, bias, score=score)
+        check(logits, K, torch.zeros(E), score=score)
