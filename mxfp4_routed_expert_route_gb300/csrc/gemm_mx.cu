@@ -63,16 +63,16 @@
 // 384 experts of 7168 x 4096, 1.71 GB: 273 us, 6.3 TB/s, 94 % of a plain copy;
 // 8 tokens over 128 experts of 2880 x 5760, 253 MB: 53 us with lists and
 // combine, of which some 8 us are the chain ids -> lists -> units -> first
-// copies). Many: dense 8192 x 7168 x 4096 in 101 us, 4.8 PFLOP/s. Parts of it left
-// out: copies alone 90 us (40 KB a stage, 1.7 GB from L2 at 19 TB/s), MMAs alone
-// 79, MMAs and their scale copies 81, all but the copies of codes 86, all but the
-// scale copies 101. So reads from L2 bound it, the MMAs come close behind, and the
-// scale copies hide. The skewed prefill (8192 tokens, 8 of 384 experts, 7.3 GB of
+// copies). Many: dense 8192 x 7168 x 4096 in 98 us, 4.9 PFLOP/s. Parts of it left
+// out: copies alone 85 us (40 KB a stage, 1.6 GB from L2 at 18 TB/s), MMAs alone
+// 81, MMAs and their scale copies 82, all but the copies of codes 87, all but the
+// MMAs 89, all but the stores of results 95, all but the scale copies 98. So reads
+// from L2 and the MMAs bound it together, the first a little more, and the scale
+// copies hide. The skewed prefill (8192 tokens, 8 of 384 experts, 7.3 GB of
 // weights, rows and float32 results) takes 1.56 ms here, 4.7 TB/s.
 // Measured on the way (dense 8192 x 7168 x 4096, other steps then missing): copies
 // and MMAs from loops of one thread 114 us, from uniform warps 108 (the operands
-// of copies and tcgen05 otherwise have to be made uniform at every issue); five
-// stages instead of four 109 against 101.
+// of copies and tcgen05 otherwise have to be made uniform at every issue).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -114,7 +114,7 @@ struct Shape {
   static constexpr uint32_t kSfCol = 2 * kN;
   static constexpr int kTmemStages = (int)((kTmemCols - kSfCol) / (kSfColsA + kSfColsB));
   // More stages would fit, and do not help: what they leave of the SM's memory
-  // caches the scale bytes (8192 x 7168 x 4096: 5 stages 109 us, 4 stages 101).
+  // caches the scale bytes (8192 x 7168 x 4096: 5 stages 105 us, 4 stages 98).
   static constexpr int kStages = kN == kMxNarrow ? 8 : 4;
   // Scale warps: two teams of one warp for the weights' rows and one for the
   // tokens', or two (128 and 64 rows) when wide.
@@ -994,16 +994,18 @@ bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
 
 namespace {
 
-// What units of this shape take, in quarters of a narrow stage (a quarter is
-// about 0.07 us). A round of units takes every SM one unit: a stage, narrow or wide
-// with its MMAs' share of the width, and about a stage for the unit itself. Splits of K are written, read and joined, 4 bytes a result
-// and split at some 3 MB a stage each way, by one launch more when dense.
-int64_t plan_cost(bool wide, int64_t blocks, int64_t width, int64_t mtiles, int64_t nk,
-                  int64_t splits, int64_t results, bool routed) {
+// What units of this shape take, in ns. A round of units takes every SM one unit:
+// its stages, each the longer the wider the copies (boxes of 32 tokens), and its
+// start and epilogue. With K split results are written and read in float32 for
+// every split, by one launch more when dense, by the combine when routed. Fitted to
+// 1 to 8192 tokens over weights of 1056 x 1001 to 7168 x 16384 (a round of 28 stages
+// takes 6.8 us in narrow units, 8.8 at 128 tokens, 9.4 at 192).
+int64_t plan_cost(int64_t blocks, int64_t width, int64_t mtiles, int64_t nk, int64_t splits,
+                  int64_t results, bool routed) {
   const int64_t rounds = (blocks * mtiles * splits + 151) / 152;
-  const int64_t stage = wide ? 4 + width / 96 : 4;
-  int64_t cost = rounds * ((nk + splits - 1) / splits * stage + 4);
-  if (splits > 1) cost += (routed ? 0 : 24) + results * splits / 100000;
+  const int64_t stage = 210 + (width + 31) / 32 * 32 / 2;
+  int64_t cost = rounds * ((nk + splits - 1) / splits * stage + 700);
+  if (splits > 1) cost += routed ? results * splits / 200 : 2200 + results * splits / 300;
   return cost;
 }
 
@@ -1019,17 +1021,23 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
   // Splits are for calls of few units.
   auto splits_for = [&](int64_t units) { return units > 4 * 152 ? 1 : most_splits; };
   if (routed) {
-    // Wide blocks where experts average more tokens than half a narrow block
-    // holds (32 experts of 2880 x 2880, 8 / 16 / 32 tokens each: narrow 38, 44,
-    // 61 us, wide 41, 44, 51); a batch of up to 32 tokens has no wider block.
+    // Wide blocks where experts average as many tokens as half a narrow block holds:
+    // 12 and 16 tokens each on 32 experts of 2880 x 2880 take 38 and 42 us narrow, 40
+    // and 42 wide; by Zipf's law (exponent 1.2) over 384 experts of 2880 x 2048, 8
+    // picks, 254 and 287 us narrow, 256 and 274 wide. Not up to 128 pairs, since lists
+    // and grouped rows are two launches more (4 experts of 4096 x 1024, 64 and 128
+    // pairs: narrow 11 and 14 us, wide 15 and 16; 8 experts, 192 and 256 pairs 17 and
+    // 20 narrow, 17 and 18 wide), nor for up to 32 tokens, where no block is wider.
     const int64_t active = std::min(E, T * K);
-    best.wide = T > kMxNarrow && T * K > 16 * active;
+    best.wide = T > kMxNarrow && T * K > 128 && T * K >= 16 * active;
     const int64_t n = best.wide ? kMxWide : kMxNarrow;
-    const int64_t width = std::min(n, (T * K + active - 1) / active);
     // Each expert's last block may be short.
     best.blocks = active + T * K / n;
-    for (int64_t s = 1; s <= splits_for(active * mtiles); ++s) {
-      const int64_t cost = plan_cost(best.wide, active, width, mtiles, nk, s, T * K * O, true);
+    // The cost is that of the blocks to be expected: half of an expert's last one.
+    const int64_t blocks = std::max(active, (active + 1) / 2 + (T * K + n - 1) / n);
+    const int64_t width = (T * K + blocks - 1) / blocks;
+    for (int64_t s = 1; s <= splits_for(blocks * mtiles); ++s) {
+      const int64_t cost = plan_cost(blocks, width, mtiles, nk, s, T * K * O, true);
       if (cost < least) {
         least = cost;
         best.splits = (int)s;
@@ -1038,8 +1046,10 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
     best.own_lists = !best.wide && T * K <= kMxOwnPairs;
     if (best.wide) best.grouped_bytes = (size_t)T * K * (size_t)(I / 2 + scale_pitch(I));
   } else {
-    // Up to 512 tokens either form (2880 x 5760: narrow blocks up to 256 tokens,
-    // 9 to 12 us against 15 to 30 in wide ones; 7168 x 16384: wide from 64 on).
+    // Up to 512 tokens either form, unsplit narrow / wide in us: 2880 x 5760, 64 tokens
+    // 7.4 / 7.6, 128 10.4 / 8.1, 512 20 / 9.9; 4096 x 512, 512 tokens 8.0 / 9.4.
+    // Splits pay for few tokens and long sums alone: 1 token of 7168 x 4096 10.5 us in
+    // one piece, 8.6 in four; 64 tokens 10.7 and 12.1.
     for (int wide = T <= 512 ? 0 : 1; wide < 2; ++wide) {
       const int64_t n = wide ? kMxWide : kMxNarrow, few = (T + n - 1) / n;
       // More blocks than needed may fill whole rounds of the SMs better.
@@ -1047,7 +1057,7 @@ MxPlan gemm_mx_plan(int64_t T, int64_t E, int64_t I, int64_t O, int64_t K, bool 
         const int64_t width = ((T + b - 1) / b + 15) / 16 * 16;
         const int64_t blocks = (T + width - 1) / width;   // equal ones, multiples of 16 tokens
         for (int64_t s = 1; s <= splits_for(blocks * mtiles); ++s) {
-          const int64_t cost = plan_cost(wide != 0, blocks, width, mtiles, nk, s, T * O, false);
+          const int64_t cost = plan_cost(blocks, width, mtiles, nk, s, T * O, false);
           if (cost < least) {
             least = cost;
             best.wide = wide != 0;
