@@ -48,15 +48,24 @@ extern "C" {
  * where `normalize` is not 0, times `scaling`.
  *
  * Ranks are those of scores and choices in float64, also where float32 does
- * not tell two apart; weights are computed in float32. An expert whose logit
- * or choice is NaN is never selected and has no share in the softmax; nor is
- * a group whose score is NaN (infinities of both signs). A softmax row whose
+ * not tell two apart; weights are computed in float32 (2^-18 relative at most,
+ * about 2^-24 as a rule). An expert whose logit or choice is NaN is never selected,
+ * nor is a group whose score is NaN (infinities of both signs); one whose logit is
+ * NaN has no share in the softmax. A softmax row whose
  * largest logit is infinite shares its weight among the experts that have
  * it. Slots that are left over get id -1 and weight 0, which the expert
  * linear skips.
  *
  * 0 < E <= 1024, 0 <= K <= 32, groups a divisor of E up to 32, K at most
- * top_groups * (E / groups); group_best 1 or 2; scaling finite.
+ * top_groups * (E / groups); group_best 1 or 2; scaling finite. Up to some 16
+ * picks most tokens are decided in float32 with an error bound; with more, tokens
+ * over more experts than picks go to float64, some 30 times as slow.
+ *
+ * mxfp4_router_topk (mxfp4_expert_linear.h) is the router that
+ * mxfp4_expert_linear_routed and the SwiGLU expert run in front: sigmoid, no groups,
+ * float32 logits, ranked by float32 choices. On the same formula the two may pick
+ * differently where float32 does not tell choices apart; take this one where the
+ * choice is made in a call of its own.
  */
 #define MXFP4EL_SCORE_SOFTMAX 0
 #define MXFP4EL_SCORE_SIGMOID 1

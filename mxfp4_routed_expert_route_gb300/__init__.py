@@ -245,7 +245,9 @@ def router_topk(router_logits: torch.Tensor, router_bias: torch.Tensor | None, K
     """(selected_experts (T, K) int32, mixture_weights (T, K) float32): the K
     experts of highest sigmoid(logit) + bias per token, highest first, ties to
     the lower index, weighted by their raw scores normalised to sum to
-    ``scaling`` (see mxfp4_router_topk in the C header)."""
+    ``scaling`` (see mxfp4_router_topk in the C header). Ranked by float32 choices,
+    as in :func:`mxfp4_expert_linear_routed`; :func:`route_experts` ranks by float64
+    ones, has softmax scores and groups, and is the faster (32768 x 384: 28 us, 97 here)."""
     lg, b, T, E = _router_args(router_logits, router_bias, K)
     sel = torch.empty((T, K), dtype=torch.int32, device=lg.device)
     p = torch.empty((T, K), dtype=torch.float32, device=lg.device)

@@ -13,8 +13,11 @@
 //
 // In float32 (route_fast) every lane holds E/32 choices as order-preserving
 // integers. The (K+1)-th largest of the 32 lanes' maxima is at most the
-// (K+1)-th largest choice, so the choices from there up are candidates, a few
-// more than K; they are gathered to one lane each and ranked by counting.
+// (K+1)-th largest choice, so the choices from there up are candidates: a few
+// more than K while K is well below 32. They are gathered to one lane each and
+// ranked by counting; a token with more than 32 of them goes to float64 as a whole.
+// That bounds the speed from some 16 picks on (32768 x 384, sigmoid with a bias): 8
+// picks 28 us, 12 31, 16 53, 18 119, 20 386, 24 819, 32 801.
 // 32768 x 384 with a bias: 28 to 30 us against 7.8 us for reading the logits,
 // 690 instructions a token at 70 % of the issue rate (38 us and 840 with both
 // kinds of score in one kernel, 48 us and 1120 with a NaN check per expert
@@ -417,6 +420,10 @@ __device__ __forceinline__ bool route_fast(const RouteArgs& a, const Tok* row, f
       }
     }
   }
+  // Weights in float32: an exponential, the picks' sum and a quotient, 5.4e-8 off in
+  // norm (2^-18 relative at most). Sum and quotient in float64 would give 4.5e-8,
+  // the scores too 2.8e-8, half an ulp; but float64 instructions are so few a cycle
+  // that 32768 x 384 would take 66 and 109 us for 28.
   const bool picked = lane < n && rank < a.K;
   float w = 0.f;
   if (picked) {

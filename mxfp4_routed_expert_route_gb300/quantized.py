@@ -69,7 +69,9 @@ def route_experts(logits: torch.Tensor, K: int, *, score: str = "softmax",
     float64 scores rank them; their weights are their scores, normalised to
     sum to ``scaling`` or, without ``normalize``, times ``scaling``. Slots that
     NaN logits leave over get id -1 and weight 0. At most 1024 experts, 32
-    groups and K = 32. See mxfp4_route_experts in the C header.
+    groups and K = 32; fast up to some 16 picks. :func:`router_topk` computes the same
+    without groups and for a sigmoid alone, and ranks by float32 choices, as the
+    calls that route for themselves do. See mxfp4_route_experts in the C header.
     """
     shape, stride, dtype, index = logits.shape, logits.stride(), logits.dtype, logits.get_device()
     if index < 0 or dtype not in _DTYPES or len(shape) != 2:
